@@ -317,6 +317,203 @@ ss_status ss_state_update_conv(float* state, void* conv_state, const void* x,
                                int delta_softplus, void* out, int64_t batch, int64_t d_inner,
                                int64_t d_state, ss_dtype dtype, uint32_t flags, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The recurrent block around a per-channel recurrence: a gated linear recurrence (one real state
+ * per channel, its decay and its input both gated by the token), the layer norm with the residual
+ * add in front of a block, and the causal depthwise convolution as an operator of its own, with
+ * the gradients of all three and their one-token forms.  A block is
+ *
+ *     norm -> projection -> convolution -> gate projections -> recurrence -> projection
+ *
+ * where the projections are the caller's matrix products.  The convolution is separate here (and
+ * not fused into the scan, as in ss_scan_fwd_conv) because the gates are projections of its
+ * output.  Two arguments are shared:
+ *   starts : (batch, seqlen) bytes or NULL.  A nonzero byte at step t begins a new sequence in
+ *            the row: nothing before t reaches t or any later step, not even an infinity or a
+ *            NaN, and no gradient flows back across it.  Rows that pack several sequences are
+ *            the usual case.  A nonzero byte at t = 0 cuts off h0 / x_prev.
+ *   io dtype : SS_F32 or SS_BF16 as above; parameters, states, statistics and every gradient
+ *            that is a sum over tokens are float32, and all arithmetic is float32.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Steps between two states that the forward saves for the backward. */
+#define SS_GATED_CHUNK 64
+
+/*
+ * Gated linear recurrence.  For batch row b and channel d:
+ *
+ *     rg_t = sigmoid(r[b,t,d] + r_bias[d])       how far the state decays at this token
+ *     ig_t = sigmoid(i[b,t,d] + i_bias[d])       how much of the token enters it
+ *     a_t  = exp(A[d] * rg_t)                    A <= 0: a decay in (0, 1]
+ *     h_t  = a_t h_{t-1} + sqrt(1 - a_t^2) ig_t x[b,t,d]       (no h_{t-1} where starts[b,t])
+ *     out  = h_t * silu(z[b,t,d])                (when z is given)
+ *
+ *   x, r, i, z, out  : (batch, seqlen, d_inner) io dtype.  z == NULL: out = h.
+ *   A                : (d_inner) float32, not above 0 (a channel with A > 0 gives NaN).
+ *   r_bias, i_bias   : (d_inner) float32, NULL means 0.
+ *   h0, h_last       : (batch, d_inner) float32; NULL: zeros / not written.
+ *   states           : NULL, or (batch, ceil(seqlen / SS_GATED_CHUNK), d_inner) float32: the
+ *                      state after every SS_GATED_CHUNK steps (and after the last step), for
+ *                      ss_gated_scan_bwd.  ss_gated_scan_states_bytes() bytes.
+ *   workspace        : ss_gated_scan_fwd_workspace_bytes() bytes, 16-byte aligned; may be NULL
+ *                      when that is 0.  Its contents need no preparation and mean nothing after
+ *                      the call; calls that may run at the same time need one each.
+ * 1 - a^2 is formed without cancellation (as -expm1(2 A rg)).  Results do not depend on how the
+ * sequence is cut over workgroups, and two runs agree bit for bit.
+ * Outputs must not overlap the inputs, each other or the workspace (SS_ERR_INVALID_ARG); d_inner
+ * above 2^24 or seqlen above 2^31 - 1 -> SS_ERR_UNSUPPORTED.  Empty sizes are a no-op (with
+ * seqlen == 0, h_last receives h0, or zeros).
+ */
+ss_status ss_gated_scan_fwd(const void* x, const void* r, const void* i, const float* A,
+                            const float* r_bias, const float* i_bias, const void* z,
+                            const uint8_t* starts, const float* h0, float* h_last, void* out,
+                            float* states, int64_t batch, int64_t seqlen, int64_t d_inner,
+                            ss_dtype dtype, void* workspace, size_t workspace_bytes,
+                            void* stream);
+size_t ss_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner,
+                                         ss_dtype dtype);
+size_t ss_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t d_inner);
+
+/*
+ * Gradients of ss_gated_scan_fwd for the upstream gradients dout (io dtype, required) and
+ * dh_last (float32, NULL: 0), by the adjoint recurrence
+ *
+ *     lam_t = dout_t silu(z_t) + a_{t+1} lam_{t+1}       (no second term where starts[b,t+1])
+ *     dx = lam s ig;   di = lam s x ig (1 - ig);   dz = dout h silu'(z);   s = sqrt(1 - a^2)
+ *     dr = dl A rg (1 - rg);   dA = sum dl rg;   dl = lam (a h_{t-1} - ig x a^2 / s)
+ *     dr_bias = sum dr;   di_bias = sum di;   dh0 = a_0 lam_0 (0 where starts[b,0])
+ * Where a = 1 exactly (s = 0) the second term of dl counts as 0: a gate that has underflowed
+ * passes no gradient.
+ *   states            : what ss_gated_scan_fwd saved for the same inputs, or NULL: the states
+ *                       are then recomputed by a pass of its own (into the workspace).
+ *   dx, dr, di        : (batch, seqlen, d_inner) io dtype, required; dz likewise with z.
+ *   dA                : (d_inner) float32, required.  dr_bias, di_bias: (d_inner) float32, NULL:
+ *                       not written.  Sums over batch rows and steps, in a fixed order: two runs
+ *                       agree bit for bit.  Zeros when there are no tokens.
+ *   dh0               : (batch, d_inner) float32, NULL: not written.
+ *   workspace         : ss_gated_scan_bwd_workspace_bytes(..., states != NULL) bytes, 16-byte
+ *                       aligned; the same rules as the forward's.
+ */
+ss_status ss_gated_scan_bwd(const void* x, const void* r, const void* i, const float* A,
+                            const float* r_bias, const float* i_bias, const void* z,
+                            const uint8_t* starts, const float* h0, const void* dout,
+                            const float* dh_last, const float* states, void* dx, void* dr,
+                            void* di, void* dz, float* dA, float* dr_bias, float* di_bias,
+                            float* dh0, int64_t batch, int64_t seqlen, int64_t d_inner,
+                            ss_dtype dtype, void* workspace, size_t workspace_bytes,
+                            void* stream);
+size_t ss_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner,
+                                         ss_dtype dtype, int states_given);
+
+/*
+ * One token of the gated linear recurrence: state (batch, d_inner) float32 is advanced IN PLACE;
+ * x, r, i, z, out: (batch, d_inner) io dtype; the rest as in ss_gated_scan_fwd.  state and out
+ * must not overlap the inputs or each other.
+ */
+ss_status ss_gated_state_update(float* state, const void* x, const void* r, const void* i,
+                                const float* A, const float* r_bias, const float* i_bias,
+                                const void* z, void* out, int64_t batch, int64_t d_inner,
+                                ss_dtype dtype, void* stream);
+
+/*
+ * Layer norm over the last axis, with the residual add in front of it:
+ *
+ *     s = x + residual;   mu = mean(s);   rstd = 1 / sqrt(mean((s - mu)^2) + eps)
+ *     out = (s - mu) rstd weight + bias
+ *
+ *   x, out           : (rows, dim) io dtype.
+ *   residual, sum    : (rows, dim) float32.  The residual stream is float32 whatever the io
+ *                      dtype: it collects one term per layer, and rounding each partial sum to
+ *                      bfloat16 would lose what the deep layers add.  residual == NULL: s = x.
+ *                      sum == NULL: s is not written.  (residual NULL with sum given widens x.)
+ *   weight, bias     : (dim) float32, NULL means 1 / 0.
+ *   mean, rstd       : (rows) float32 statistics for the backward; NULL: not written.
+ *   eps              : not negative (SS_ERR_INVALID_ARG).
+ * The variance is the mean of squared differences from the mean, not a difference of moments.
+ * Outputs must not overlap the inputs or each other.  rows == 0 or dim == 0 is a no-op.
+ * dim above 2^24 -> SS_ERR_UNSUPPORTED.
+ */
+ss_status ss_layer_norm_fwd(const void* x, const float* residual, const float* weight,
+                            const float* bias, float eps, void* out, float* sum, float* mean,
+                            float* rstd, int64_t rows, int64_t dim, ss_dtype dtype,
+                            void* stream);
+
+/*
+ * Gradients of ss_layer_norm_fwd: with xh = (s - mean) rstd and g = dout weight,
+ *
+ *     ds      = rstd (g - mean(g) - xh mean(g xh)) + dsum
+ *     dweight = sum over rows of dout xh;   dbias = sum over rows of dout
+ *
+ *   dout       : (rows, dim) in `dtype`.
+ *   s          : (rows, dim) in `s_dtype`: x itself (s_dtype == dtype) or the float32 sum the
+ *                forward wrote.
+ *   mean, rstd : as the forward wrote them.      weight: as the forward's.
+ *   dsum       : (rows, dim) float32 upstream gradient of sum, NULL: 0.
+ *   dx         : ds in `dtype`, the gradient of x.  dresidual: ds in float32, the gradient of
+ *                residual.  At least one is required.
+ *   dweight, dbias : (dim) float32, NULL: not written.  Summed in a fixed order: two runs agree
+ *                bit for bit.  Zeros when rows == 0.
+ *   workspace  : ss_layer_norm_bwd_workspace_bytes() bytes, 16-byte aligned; one per call that
+ *                may run at the same time.
+ */
+ss_status ss_layer_norm_bwd(const void* dout, const void* s, ss_dtype s_dtype,
+                            const float* weight, const float* mean, const float* rstd,
+                            const float* dsum, void* dx, float* dresidual, float* dweight,
+                            float* dbias, int64_t rows, int64_t dim, ss_dtype dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+size_t ss_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
+/*
+ * Causal depthwise convolution, the front end of ss_scan_fwd_conv as an operator of its own:
+ *
+ *     p[b,t,d] = bias[d] + sum_{j<k} weight[d,j] x[b, t-(k-1)+j, d];   out = silu(p) or p
+ *
+ *   x, out       : (batch, seqlen, d_inner) io dtype.
+ *   weight       : (d_inner, k) float32, k in 1..4 (SS_ERR_UNSUPPORTED otherwise).
+ *   bias         : (d_inner) float32, NULL means 0.
+ *   x_prev       : (batch, k-1, d_inner) io dtype, the inputs before t = 0 (oldest first), NULL:
+ *                  zeros.
+ *   silu         : nonzero -> out = silu(p), zero -> out = p.
+ * out must not overlap the inputs.  d_inner above 2^24 or seqlen above 2^31 - 1 ->
+ * SS_ERR_UNSUPPORTED.  Empty sizes are a no-op.
+ */
+ss_status ss_causal_conv_fwd(const void* x, const float* weight, const float* bias,
+                             const void* x_prev, const uint8_t* starts, int silu, void* out,
+                             int64_t batch, int64_t seqlen, int64_t d_inner, int32_t k,
+                             ss_dtype dtype, void* stream);
+
+/*
+ * Gradients of ss_causal_conv_fwd, with g = dout silu'(p) (p recomputed) or dout:
+ *
+ *     dx_t = sum_j weight[j] g_{t+(k-1)-j};   dweight[j] = sum g_t x_{t-(k-1)+j};
+ *     dbias = sum g;   dx_prev as dx at the steps before t = 0    (none across a start)
+ *
+ *   dx             : (batch, seqlen, d_inner) io dtype, required.
+ *   dweight        : (d_inner, k) float32, required.  dbias: (d_inner) float32, NULL: not
+ *                    written.  Summed over batch rows and steps in a fixed order: two runs agree
+ *                    bit for bit.  Zeros when there are no tokens.
+ *   dx_prev        : (batch, k-1, d_inner) io dtype, NULL: not written (needs x_prev).
+ *   workspace      : ss_causal_conv_bwd_workspace_bytes() bytes, 16-byte aligned; one per call
+ *                    that may run at the same time.
+ */
+ss_status ss_causal_conv_bwd(const void* x, const float* weight, const float* bias,
+                             const void* x_prev, const uint8_t* starts, int silu,
+                             const void* dout, void* dx, float* dweight, float* dbias,
+                             void* dx_prev, int64_t batch, int64_t seqlen, int64_t d_inner,
+                             int32_t k, ss_dtype dtype, void* workspace, size_t workspace_bytes,
+                             void* stream);
+size_t ss_causal_conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner,
+                                          int32_t k, ss_dtype dtype);
+
+/*
+ * One token of the convolution: the window is [conv_state (batch, k-1, d_inner), x (batch,
+ * d_inner)]; conv_state is shifted IN PLACE (oldest dropped, x appended).  conv_state may be
+ * NULL when k == 1; conv_state and out must not overlap the inputs or each other.
+ */
+ss_status ss_causal_conv_update(void* conv_state, const void* x, const float* weight,
+                                const float* bias, int silu, void* out, int64_t batch,
+                                int64_t d_inner, int32_t k, ss_dtype dtype, void* stream);
+
 /* Static description of a status code. */
 const char* ss_status_string(ss_status s);
 

@@ -12,6 +12,7 @@
 
 #include "ss_scan.h"
 #include "ss_bwd.h"
+#include "ss_host.h"
 #include "ss_launch.h"
 #include "ss_scan2.h"
 
@@ -22,10 +23,11 @@
 static __device__ __align__(256) unsigned char scratch[SS_NOALLOC_SCRATCH_BYTES];
 
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
 
-ss_status fail(ss_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace ss::host {
+
 ss_status fail(ss_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -39,24 +41,11 @@ ss_status ok() {
   return SS_OK;
 }
 
-bool mul_ok(int64_t a, int64_t b, int64_t* r) { return !__builtin_mul_overflow(a, b, r); }
+}  // namespace ss::host
 
-struct Range {
-  const char* name;
-  uintptr_t lo, hi;  // [lo, hi)
-};
+namespace {
 
-Range range(const char* name, const void* p, int64_t elems, int64_t esize) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{name, lo, p ? lo + static_cast<uintptr_t>(elems * esize) : lo};
-}
-
-bool overlap(const Range& a, const Range& b) {
-  if (a.lo == a.hi || b.lo == b.hi) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-bool aligned(const void* p, int64_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using namespace ss::host;
 
 constexpr int kMaxDevices = 64;
 std::mutex g_scratch_mu;
@@ -127,12 +116,6 @@ size_t ws_bytes(int64_t batch, int64_t d_inner, int64_t d_state, int32_t nseg) {
   const int64_t rows = batch * d_inner;
   const int64_t per = rows * d_state + rows;  // floats per summarised segment
   return static_cast<size_t>((nseg - 1) * per) * sizeof(float) + 256;
-}
-
-ss_status check_dtype(ss_dtype dt, int64_t* esize) {
-  if (dt == SS_F32) { *esize = 4; return SS_OK; }
-  if (dt == SS_BF16) { *esize = 2; return SS_OK; }
-  return fail(SS_ERR_UNSUPPORTED, "unknown dtype %d", static_cast<int>(dt));
 }
 
 ss_status check_flags(uint32_t flags, uint32_t allowed = SS_FLAG_ZOH_EXACT) {
@@ -769,6 +752,6 @@ const char* ss_status_string(ss_status s) {
 
 const char* ss_last_error(void) { return g_err; }
 
-int ss_version(void) { return 101; }
+int ss_version(void) { return 102; }
 
 }  // extern "C"

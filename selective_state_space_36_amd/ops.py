@@ -19,6 +19,7 @@ SS_OK, SS_ERR_INVALID_ARG, SS_ERR_UNSUPPORTED, SS_ERR_HIP = 0, 1, 2, 3
 SS_F32, SS_BF16 = 0, 1
 SS_FLAG_ZOH_EXACT = 1
 SS_FLAG_STATES_GIVEN = 2
+SS_GATED_CHUNK = 64
 
 # Every symbol declared in include/ss_scan.h, with its ctypes signature.
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -51,6 +52,25 @@ SIGNATURES = {
                                _i64, _i64, _i64, _i32, _vp]),
     "ss_state_update_ex": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int,
                                   _vp, _i64, _i64, _i64, _i32, _u32, _vp]),
+    "ss_gated_scan_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "ss_gated_scan_fwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "ss_gated_scan_states_bytes": (_sz, [_i64, _i64, _i64]),
+    "ss_gated_scan_bwd": (_i32, [_vp] * 20 + [_i64, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "ss_gated_scan_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, ctypes.c_int]),
+    "ss_gated_state_update": (_i32, [_vp] * 9 + [_i64, _i64, _i32, _vp]),
+    "ss_layer_norm_fwd": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp, _i64,
+                                 _i64, _i32, _vp]),
+    "ss_layer_norm_bwd": (_i32, [_vp, _vp, _i32] + [_vp] * 8 + [_i64, _i64, _i32, _vp, _sz,
+                                                                _vp]),
+    "ss_layer_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "ss_causal_conv_fwd": (_i32, [_vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _i64, _i64, _i64,
+                                  _i32, _i32, _vp]),
+    "ss_causal_conv_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
+                                  _i64, _i64, _i64, _i32, _i32, _vp, _sz, _vp]),
+    "ss_causal_conv_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "ss_causal_conv_update": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_int, _vp, _i64, _i64, _i32,
+                                     _i32, _vp]),
     "ss_status_string": (ctypes.c_char_p, [_i32]),
     "ss_last_error": (ctypes.c_char_p, []),
     "ss_version": (ctypes.c_int, []),
@@ -433,4 +453,368 @@ def state_update_conv(state, conv_state, x, conv_weight, conv_bias, delta, A, B,
         _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(delta_bias),
         1 if delta_softplus else 0, _ptr(out), batch, d_inner, d_state, code,
         SS_FLAG_ZOH_EXACT if zoh_exact else 0, _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# The recurrent block's operators.  They run on their inputs' device; `stream` (a
+# torch.cuda.Stream) is as if the call stood under torch.cuda.stream(stream): outputs and
+# workspaces are allocated for it, and the inputs are marked as used on it.
+
+_IO = {torch.float32: SS_F32, torch.bfloat16: SS_BF16}
+
+
+def _io_code(x) -> int:
+    code = _IO.get(x.dtype)
+    if code is None:
+        raise TypeError(f"io tensors must be float32 or bfloat16, got {x.dtype}")
+    return code
+
+
+def _shape(name, t, ndim):
+    if t.dim() != ndim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {ndim} dimensions")
+    return t.shape
+
+
+def _expect(device, dtype, shape, *named) -> None:
+    """Every (name, tensor) pair that is not None: on `device`, contiguous, of dtype and shape."""
+    for name, t in named:
+        if t is None:
+            continue
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _expect_starts(starts, device, shape) -> None:
+    if starts is not None:
+        if starts.dtype is not torch.bool and starts.dtype is not torch.uint8:
+            raise TypeError(f"starts must be bool or uint8, got {starts.dtype}")
+        _expect(device, starts.dtype, shape, ("starts", starts))
+
+
+def _elsewhere(x, stream) -> bool:
+    """Whether the call has to be moved: to `stream`, or to x's device when that is not the
+    current one.  Raises for a tensor that is not on a GPU."""
+    if not x.is_cuda:
+        raise ValueError("the tensors must be GPU tensors")
+    return stream is not None or x.device.index != torch.cuda.current_device()
+
+
+def _moved(fn, x, stream, args, kw):
+    if stream is None:
+        with torch.cuda.device(x.device):
+            return fn(*args, **kw)
+    if stream.device != x.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {x.device}")
+    with torch.cuda.stream(stream):
+        res = fn(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+    return res
+
+
+def _scratch(workspace, nbytes, device):
+    """(pointer, size, tensor) of the caller's workspace or of one allocated here."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _raw_stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _gated_fwd(x, r, i, A, r_bias, i_bias, z, starts, h0, out, h_last, states, want_last,
+               want_states, workspace):
+    code = _io_code(x)
+    batch, L, d = shape = _shape("x", x, 3)
+    dev = x.device
+    f32 = torch.float32
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if want_last and h_last is None:
+        h_last = torch.empty((batch, d), dtype=f32, device=dev)
+    nct = (L + SS_GATED_CHUNK - 1) // SS_GATED_CHUNK
+    if want_states and states is None:
+        states = torch.empty((batch, nct, d), dtype=f32, device=dev)
+    _expect(dev, x.dtype, shape, ("x", x), ("r", r), ("i", i), ("z", z), ("out", out))
+    _expect(dev, f32, (d,), ("A", A), ("r_bias", r_bias), ("i_bias", i_bias))
+    _expect(dev, f32, (batch, d), ("h0", h0), ("h_last", h_last))
+    _expect(dev, f32, (batch, nct, d), ("states", states))
+    _expect_starts(starts, dev, (batch, L))
+    l = lib()
+    nbytes = l.ss_gated_scan_fwd_workspace_bytes(batch, L, d, code)
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_gated_scan_fwd(
+        x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(), _ptr(r_bias), _ptr(i_bias),
+        _ptr(z), _ptr(starts), _ptr(h0), _ptr(h_last), out.data_ptr(), _ptr(states), batch, L, d,
+        code, ws, ws_len, _raw_stream()))
+    return out, states, h_last
+
+
+def gated_scan_fwd(x, r, i, A, r_bias=None, i_bias=None, z=None, starts=None, h0=None,
+                   return_last_state=False, out=None, h_last=None, workspace=None, stream=None):
+    """Gated linear recurrence over a sequence (ss_gated_scan_fwd):
+
+        a_t = exp(A sigmoid(r_t + r_bias)),
+        h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t + i_bias) x_t,   out = h (or h silu(z))
+
+    x, r, i, z: (batch, L, d_inner), float32 or bfloat16; A (not above 0), r_bias, i_bias:
+    (d_inner,) float32; starts: (batch, L) bool or uint8, true where a new sequence begins in the
+    row; h0: (batch, d_inner) float32.  Returns out (and h_last when return_last_state).
+    workspace: uint8 device buffer of ss_gated_scan_fwd_workspace_bytes bytes (allocated here
+    when None); calls that may overlap need one each."""
+    if _elsewhere(x, stream):
+        return _moved(gated_scan_fwd, x, stream, (x, r, i, A),
+                      dict(r_bias=r_bias, i_bias=i_bias, z=z, starts=starts, h0=h0,
+                           return_last_state=return_last_state, out=out, h_last=h_last,
+                           workspace=workspace))
+    out, _, h_last = _gated_fwd(x, r, i, A, r_bias, i_bias, z, starts, h0, out, h_last, None,
+                                return_last_state, False, workspace)
+    return (out, h_last) if return_last_state else out
+
+
+def gated_scan_fwd_states(x, r, i, A, r_bias=None, i_bias=None, z=None, starts=None, h0=None,
+                          return_last_state=False, out=None, h_last=None, states=None,
+                          workspace=None, stream=None):
+    """gated_scan_fwd that also saves the state after every SS_GATED_CHUNK steps, for
+    gated_scan_bwd(..., states=states).  states: (batch, ceil(L / SS_GATED_CHUNK), d_inner)
+    float32, allocated here when None.  Returns (out, states), or (out, states, h_last) with
+    return_last_state."""
+    if _elsewhere(x, stream):
+        return _moved(gated_scan_fwd_states, x, stream, (x, r, i, A),
+                      dict(r_bias=r_bias, i_bias=i_bias, z=z, starts=starts, h0=h0,
+                           return_last_state=return_last_state, out=out, h_last=h_last,
+                           states=states, workspace=workspace))
+    out, states, h_last = _gated_fwd(x, r, i, A, r_bias, i_bias, z, starts, h0, out, h_last,
+                                     states, return_last_state, True, workspace)
+    return (out, states, h_last) if return_last_state else (out, states)
+
+
+def gated_scan_bwd(x, r, i, A, dout, r_bias=None, i_bias=None, z=None, starts=None, h0=None,
+                   dh_last=None, states=None, want_dbias=True, want_dh0=True, workspace=None,
+                   stream=None):
+    """Gradients of gated_scan_fwd (ss_gated_scan_bwd) for the upstream gradient dout (shape and
+    dtype of out) and optionally dh_last.  Returns a dict: dx, dr, di, dz (io dtype; dz None
+    without z), dA, dr_bias, di_bias (float32, the biases' None when not wanted), dh0 (float32,
+    None when not wanted).  states: as gated_scan_fwd_states saved them for the same inputs;
+    None: recomputed here."""
+    if _elsewhere(x, stream):
+        return _moved(gated_scan_bwd, x, stream, (x, r, i, A, dout),
+                      dict(r_bias=r_bias, i_bias=i_bias, z=z, starts=starts, h0=h0,
+                           dh_last=dh_last, states=states, want_dbias=want_dbias,
+                           want_dh0=want_dh0, workspace=workspace))
+    code = _io_code(x)
+    batch, L, d = shape = _shape("x", x, 3)
+    dev = x.device
+    f32 = torch.float32
+    nct = (L + SS_GATED_CHUNK - 1) // SS_GATED_CHUNK
+    _expect(dev, x.dtype, shape, ("x", x), ("r", r), ("i", i), ("z", z), ("dout", dout))
+    _expect(dev, f32, (d,), ("A", A), ("r_bias", r_bias), ("i_bias", i_bias))
+    _expect(dev, f32, (batch, d), ("h0", h0), ("dh_last", dh_last))
+    _expect(dev, f32, (batch, nct, d), ("states", states))
+    _expect_starts(starts, dev, (batch, L))
+    e = lambda s, t: torch.empty(s, dtype=t, device=dev)  # noqa: E731
+    g = dict(dx=e(shape, x.dtype), dr=e(shape, x.dtype), di=e(shape, x.dtype),
+             dz=e(shape, x.dtype) if z is not None else None, dA=e((d,), f32),
+             dr_bias=e((d,), f32) if want_dbias else None,
+             di_bias=e((d,), f32) if want_dbias else None,
+             dh0=e((batch, d), f32) if want_dh0 else None)
+    l = lib()
+    nbytes = l.ss_gated_scan_bwd_workspace_bytes(batch, L, d, code, states is not None)
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_gated_scan_bwd(
+        x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(), _ptr(r_bias), _ptr(i_bias),
+        _ptr(z), _ptr(starts), _ptr(h0), dout.data_ptr(), _ptr(dh_last), _ptr(states),
+        _ptr(g["dx"]), _ptr(g["dr"]), _ptr(g["di"]), _ptr(g["dz"]), _ptr(g["dA"]),
+        _ptr(g["dr_bias"]), _ptr(g["di_bias"]), _ptr(g["dh0"]), batch, L, d, code, ws, ws_len,
+        _raw_stream()))
+    return g
+
+
+def gated_state_update(state, x, r, i, A, r_bias=None, i_bias=None, z=None, out=None,
+                       stream=None):
+    """One token of the gated linear recurrence (ss_gated_state_update); `state` (batch, d_inner)
+    float32 is advanced in place.  x, r, i, z: (batch, d_inner).  Returns out."""
+    if _elsewhere(x, stream):
+        return _moved(gated_state_update, x, stream, (state, x, r, i, A),
+                      dict(r_bias=r_bias, i_bias=i_bias, z=z, out=out))
+    code = _io_code(x)
+    batch, d = shape = _shape("x", x, 2)
+    dev = x.device
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _expect(dev, x.dtype, shape, ("x", x), ("r", r), ("i", i), ("z", z), ("out", out))
+    _expect(dev, torch.float32, (d,), ("A", A), ("r_bias", r_bias), ("i_bias", i_bias))
+    _expect(dev, torch.float32, shape, ("state", state))
+    _check(lib().ss_gated_state_update(
+        state.data_ptr(), x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(), _ptr(r_bias),
+        _ptr(i_bias), _ptr(z), out.data_ptr(), batch, d, code, _raw_stream()))
+    return out
+
+
+def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, return_sum=None,
+                   return_stats=False, out=None, sum_out=None, stream=None):
+    """Layer norm over the last axis of x + residual (ss_layer_norm_fwd).
+
+    x: (..., dim) float32 or bfloat16; residual: the same shape, float32 (the residual stream);
+    weight, bias: (dim,) float32.  Returns out alone, or a tuple of out, then the float32 sum
+    x + residual (return_sum: by default with a residual), then mean and rstd, (...) float32, with
+    return_stats (layer_norm_bwd takes them)."""
+    if _elsewhere(x, stream):
+        return _moved(layer_norm_fwd, x, stream, (x,),
+                      dict(weight=weight, bias=bias, residual=residual, eps=eps,
+                           return_sum=return_sum, return_stats=return_stats, out=out,
+                           sum_out=sum_out))
+    code = _io_code(x)
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    shape, dev, f32 = x.shape, x.device, torch.float32
+    dim = shape[-1]
+    rows = x.numel() // dim if dim else 0
+    if return_sum is None:
+        return_sum = residual is not None
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if return_sum and sum_out is None:
+        sum_out = torch.empty(shape, dtype=f32, device=dev)
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+        rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
+    _expect(dev, x.dtype, shape, ("x", x), ("out", out))
+    _expect(dev, f32, shape, ("residual", residual), ("sum_out", sum_out))
+    _expect(dev, f32, (dim,), ("weight", weight), ("bias", bias))
+    _check(lib().ss_layer_norm_fwd(
+        x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias), eps, out.data_ptr(),
+        _ptr(sum_out), _ptr(mean), _ptr(rstd), rows, dim, code, _raw_stream()))
+    res = (out, *((sum_out,) if return_sum else ()), *((mean, rstd) if return_stats else ()))
+    return res if len(res) > 1 else out
+
+
+def layer_norm_bwd(dout, s, weight, mean, rstd, dsum=None, want_dx=True, want_dresidual=False,
+                   want_dparams=True, workspace=None, stream=None):
+    """Gradients of layer_norm_fwd (ss_layer_norm_bwd) for the upstream gradient dout of out and
+    optionally dsum (float32) of the sum.  s: what was normalised, x itself (dout's dtype) or the
+    float32 sum; weight: (dim,) float32 or None; mean, rstd: the forward's statistics.  Returns a
+    dict: dx (dout's dtype), dresidual (float32), dweight, dbias ((dim,) float32), None where not
+    wanted.  dx and dresidual hold the same gradient, in the dtypes of x and of residual."""
+    if _elsewhere(dout, stream):
+        return _moved(layer_norm_bwd, dout, stream, (dout, s, weight, mean, rstd),
+                      dict(dsum=dsum, want_dx=want_dx, want_dresidual=want_dresidual,
+                           want_dparams=want_dparams, workspace=workspace))
+    code = _io_code(dout)
+    if dout.dim() < 1:
+        raise ValueError("dout needs at least one dimension")
+    shape, dev, f32 = dout.shape, dout.device, torch.float32
+    dim = shape[-1]
+    rows = dout.numel() // dim if dim else 0
+    s_dtype = f32 if s.dtype is f32 else dout.dtype
+    _expect(dev, dout.dtype, shape, ("dout", dout))
+    _expect(dev, s_dtype, shape, ("s", s))
+    _expect(dev, f32, shape, ("dsum", dsum))
+    _expect(dev, f32, (dim,), ("weight", weight))
+    _expect(dev, f32, shape[:-1], ("mean", mean), ("rstd", rstd))
+    e = lambda shp, t: torch.empty(shp, dtype=t, device=dev)  # noqa: E731
+    g = dict(dx=e(shape, dout.dtype) if want_dx else None,
+             dresidual=e(shape, f32) if want_dresidual else None,
+             dweight=e((dim,), f32) if want_dparams else None,
+             dbias=e((dim,), f32) if want_dparams else None)
+    l = lib()
+    nbytes = l.ss_layer_norm_bwd_workspace_bytes(rows, dim) if want_dparams else 0
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_layer_norm_bwd(
+        dout.data_ptr(), s.data_ptr(), _IO[s_dtype], _ptr(weight), mean.data_ptr(),
+        rstd.data_ptr(), _ptr(dsum), _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
+        _ptr(g["dbias"]), rows, dim, code, ws, ws_len, _raw_stream()))
+    return g
+
+
+def _conv_sizes(x, weight, x_prev, starts, bias, ndim):
+    shape = _shape("x", x, ndim)
+    d, dev = shape[-1], x.device
+    k = _shape("weight", weight, 2)[1]
+    _expect(dev, torch.float32, (d, k), ("weight", weight))
+    _expect(dev, torch.float32, (d,), ("bias", bias))
+    _expect(dev, x.dtype, (shape[0], max(k - 1, 0), d), ("x_prev", x_prev))
+    _expect_starts(starts, dev, shape[:2])
+    return shape, k
+
+
+def causal_conv_fwd(x, weight, bias=None, x_prev=None, starts=None, silu=True, out=None,
+                    stream=None):
+    """Causal depthwise convolution (ss_causal_conv_fwd), the front end of scan_fwd_conv as an
+    operator of its own: out = silu(bias + sum_j weight[:, j] x_{t-(k-1)+j}), or the bare sum with
+    silu=False.  x: (batch, L, d_inner) float32 or bfloat16; weight: (d_inner, k) float32, k in
+    1..4; bias: (d_inner,) float32; x_prev: (batch, k-1, d_inner) io dtype, the inputs before the
+    first step; starts: (batch, L) bool or uint8, true where a new sequence begins in the row."""
+    if _elsewhere(x, stream):
+        return _moved(causal_conv_fwd, x, stream, (x, weight),
+                      dict(bias=bias, x_prev=x_prev, starts=starts, silu=silu, out=out))
+    code = _io_code(x)
+    shape, k = _conv_sizes(x, weight, x_prev, starts, bias, 3)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _expect(x.device, x.dtype, shape, ("x", x), ("out", out))
+    _check(lib().ss_causal_conv_fwd(
+        x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(x_prev), _ptr(starts),
+        1 if silu else 0, out.data_ptr(), *shape, k, code, _raw_stream()))
+    return out
+
+
+def causal_conv_bwd(x, weight, dout, bias=None, x_prev=None, starts=None, silu=True,
+                    want_dbias=True, workspace=None, stream=None):
+    """Gradients of causal_conv_fwd (ss_causal_conv_bwd).  Returns a dict: dx (io dtype), dweight
+    ((d_inner, k) float32), dbias ((d_inner,) float32, None when not wanted), dx_prev (io dtype,
+    None without x_prev)."""
+    if _elsewhere(x, stream):
+        return _moved(causal_conv_bwd, x, stream, (x, weight, dout),
+                      dict(bias=bias, x_prev=x_prev, starts=starts, silu=silu,
+                           want_dbias=want_dbias, workspace=workspace))
+    code = _io_code(x)
+    shape, k = _conv_sizes(x, weight, x_prev, starts, bias, 3)
+    dev, f32 = x.device, torch.float32
+    _expect(dev, x.dtype, shape, ("x", x), ("dout", dout))
+    e = lambda s, t: torch.empty(s, dtype=t, device=dev)  # noqa: E731
+    g = dict(dx=e(shape, x.dtype), dweight=e(weight.shape, f32),
+             dbias=e(shape[2:], f32) if want_dbias else None,
+             dx_prev=e(x_prev.shape, x.dtype) if x_prev is not None else None)
+    l = lib()
+    nbytes = l.ss_causal_conv_bwd_workspace_bytes(*shape, k, code)
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_causal_conv_bwd(
+        x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(x_prev), _ptr(starts),
+        1 if silu else 0, dout.data_ptr(), _ptr(g["dx"]), _ptr(g["dweight"]), _ptr(g["dbias"]),
+        _ptr(g["dx_prev"]), *shape, k, code, ws, ws_len, _raw_stream()))
+    return g
+
+
+def causal_conv_update(conv_state, x, weight, bias=None, silu=True, out=None, stream=None):
+    """One token of the convolution (ss_causal_conv_update): conv_state (batch, k-1, d_inner) io
+    dtype is shifted in place, x: (batch, d_inner).  Returns out."""
+    if _elsewhere(x, stream):
+        return _moved(causal_conv_update, x, stream, (conv_state, x, weight),
+                      dict(bias=bias, silu=silu, out=out))
+    code = _io_code(x)
+    shape, k = _conv_sizes(x, weight, None, None, bias, 2)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _expect(x.device, x.dtype, shape, ("x", x), ("out", out))
+    _expect(x.device, x.dtype, (shape[0], max(k - 1, 0), shape[1]), ("conv_state", conv_state))
+    _check(lib().ss_causal_conv_update(
+        conv_state.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), 1 if silu else 0,
+        out.data_ptr(), *shape, k, code, _raw_stream()))
     return out

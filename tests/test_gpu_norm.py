@@ -1,0 +1,143 @@
+"""Layer norm with the residual add on the GPU, forward and gradients, against float64."""
+import numpy as np
+import pytest
+
+from oracle import block_twin as bt
+from tests.block_helpers import Guarded, check, gpu
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from selective_state_space_36_amd import ops
+    ops.lib()
+    yield
+
+
+def ops():
+    from selective_state_space_36_amd import ops as o
+    return o
+
+
+class Case:
+    def __init__(self, seed, rows, dim, io, residual, params=True, shift=0.0, offset=0):
+        print(f"  case rows={rows} dim={dim} {io} residual={residual} shift={shift}", flush=True)
+        rng = np.random.default_rng(seed)
+        n = lambda *s: rng.standard_normal(s)  # noqa: E731
+        self.io, self.residual = io, residual
+        self.x, self.vx = gpu(n(rows, dim) + shift, io, offset)
+        self.w, self.vw = gpu(1 + 0.1 * n(dim) if params else None, "f32", offset)
+        self.b, self.vb = gpu(0.1 * n(dim) if params else None)
+        self.res, self.vres = gpu(3 * n(rows, dim) if residual else None, "f32", offset)
+        self.dout, self.vdout = gpu(n(rows, dim), io, offset)
+        self.dsum, self.vdsum = gpu(n(rows, dim) if residual else None)
+
+    def check(self):
+        o = ops()
+        r = o.layer_norm_fwd(self.x, self.w, self.b, residual=self.res, return_stats=True)
+        out, total, mean, rstd = r if self.residual else (r[0], None, *r[1:])
+        ref, s, vm, vr, _ = bt.norm_fwd(self.vx, self.vw, self.vb, self.vres)
+        check(out, ref, self.io, "out")
+        check(mean, vm, "f32", "mean")
+        check(rstd, vr, "f32", "rstd")
+        if self.residual:
+            check(total, s, "f32", "sum")
+        g = o.layer_norm_bwd(self.dout, total if self.residual else self.x, self.w, mean, rstd,
+                             dsum=self.dsum, want_dresidual=True)
+        want = bt.norm_bwd(self.vdout, self.vx, self.vw, self.vres, self.vdsum)
+        check(g["dx"], want["ds"], self.io, "dx")
+        check(g["dresidual"], want["ds"], "f32", "dresidual")
+        check(g["dweight"], want["dweight"], "f32", "dweight")
+        check(g["dbias"], want["dbias"], "f32", "dbias")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,dim", [(1, 1), (1, 2560), (3, 2), (5, 63), (4, 64), (7, 100),
+                                      (2, 768), (33, 130), (9, 1027), (300, 96), (3, 4096),
+                                      (2, 5121), (5, 8200), (2, 20001)])
+def test_forward_and_gradients(rows, dim, residual, io):
+    Case(rows * 10 + dim, rows, dim, io, residual).check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_without_parameters(io):
+    Case(1, 6, 200, io, True, params=False).check()
+    Case(2, 6, 200, io, False, params=False).check()
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_misaligned(offset, io):
+    Case(offset, 5, 256, io, True, offset=offset).check()
+
+
+def test_many_rows():
+    Case(3, 3001, 72, "bf16", True).check()
+
+
+@pytest.mark.parametrize("dim", [100, 2560])
+def test_a_mean_far_from_zero_does_not_cost_the_variance(dim):
+    Case(4, 4, dim, "f32", False, shift=300.0).check()
+
+
+def test_a_constant_row():
+    o = ops()
+    x = torch.full((3, 700), 2.5, device="cuda")
+    b = torch.randn(700, device="cuda")
+    out, mean, rstd = o.layer_norm_fwd(x, None, b, return_stats=True)
+    assert torch.equal(out, b.expand(3, 700)) and torch.equal(mean, x[:, 0])
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e5 ** 0.5), rtol=1e-6)
+
+
+def test_a_bad_row_leaves_the_others_alone():
+    c = Case(5, 6, 320, "f32", True)
+    c.x[2, 5] = float("nan")
+    c.x[4, 0] = float("inf")
+    out, s, mean, rstd = ops().layer_norm_fwd(c.x, c.w, c.b, residual=c.res, return_stats=True)
+    good = [0, 1, 3, 5]
+    assert torch.isfinite(out[good]).all() and torch.isnan(out[[2, 4]]).all()
+    g = ops().layer_norm_bwd(c.dout, s, c.w, mean, rstd)
+    assert torch.isfinite(g["dx"][good]).all() and torch.isnan(g["dx"][[2, 4]]).all()
+
+
+def test_sum_without_residual_and_leading_dimensions():
+    x = torch.randn(2, 3, 5, 40, device="cuda", dtype=torch.bfloat16)
+    out, s, mean, rstd = ops().layer_norm_fwd(x, return_sum=True, return_stats=True)
+    assert torch.equal(s, x.float()) and mean.shape == (2, 3, 5)
+    flat = ops().layer_norm_fwd(x.view(30, 40))
+    assert torch.equal(out.view(30, 40), flat)
+    g = ops().layer_norm_bwd(torch.ones_like(x), s, None, mean, rstd, want_dparams=False)
+    assert g["dx"].shape == x.shape and g["dweight"] is None and g["dresidual"] is None
+
+
+def test_two_runs_agree_and_writes_stay_inside():
+    c = Case(6, 777, 515, "bf16", True)
+    o = ops()
+    out, s = Guarded((777, 515), torch.bfloat16), Guarded((777, 515), torch.float32)
+    _, _, mean, rstd = o.layer_norm_fwd(c.x, c.w, c.b, residual=c.res, out=out.t, sum_out=s.t,
+                                        return_stats=True)
+    ws = Guarded((max(16, o.lib().ss_layer_norm_bwd_workspace_bytes(777, 515)),), torch.uint8)
+    run = lambda: o.layer_norm_bwd(c.dout, s.t, c.w, mean, rstd, dsum=c.dsum,  # noqa: E731
+                                   want_dresidual=True, workspace=ws.t)
+    first = run()
+    for _ in range(3):
+        again = run()
+        for k in first:
+            assert torch.equal(first[k], again[k]), k
+    assert out.intact() and s.intact() and ws.intact()
+
+
+def test_empty_sizes():
+    o = ops()
+    e = torch.empty(0, 16, device="cuda")
+    out, mean, rstd = o.layer_norm_fwd(e, return_stats=True)
+    assert out.shape == (0, 16)
+    g = o.layer_norm_bwd(e, e, None, mean, rstd)
+    assert not g["dweight"].any() and not g["dbias"].any() and g["dx"].shape == (0, 16)
+    assert o.layer_norm_fwd(torch.empty(3, 0, device="cuda")).shape == (3, 0)
