@@ -85,6 +85,13 @@ bool sizes_ok(int64_t batch, int64_t seqlen, int64_t d_inner) {
          mul_ok(batch, d_inner, &n) && mul_ok(n, seqlen + 8, &n) && n / 64 < kMaxGrid;
 }
 
+// The recurrence's launch has at most one workgroup per 64 steps and 64 channels of a batch row.
+ss_status check_tiles(int64_t batch, int64_t seqlen, int64_t d_inner) {
+  if (batch * ((d_inner + 63) / 64) * ((seqlen + 63) / 64) > kMaxGrid)
+    return fail(SS_ERR_INVALID_ARG, "too many tiles (batch * seqlen * d_inner)");
+  return SS_OK;
+}
+
 int64_t chunks_of(int64_t seqlen) { return (seqlen + SS_GATED_CHUNK - 1) / SS_GATED_CHUNK; }
 
 }  // namespace
@@ -121,6 +128,7 @@ ss_status ss_gated_scan_fwd(const void* x, const void* r, const void* i, const f
     if ((s = check_arrays(in, 1, out1, 1)) != SS_OK) return s;
     return launched(h0 ? ss::launch_copy(h_last, h0, rows, st) : ss::launch_zero(h_last, rows, st));
   }
+  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
   const size_t need = ss::gated_fwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16);
   const Arr in[] = {{"x", x, n, es, true}, {"r", r, n, es, true}, {"i", i, n, es, true},
                     {"A", A, d_inner, 4, true}, {"r_bias", r_bias, d_inner, 4, false},
@@ -161,6 +169,7 @@ ss_status ss_gated_scan_bwd(const void* x, const void* r, const void* i, const f
   if (s != SS_OK) return s;
   if ((s = check_sizes(batch, seqlen, d_inner, &n)) != SS_OK) return s;
   if (d_inner == 0) return ok();
+  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
   const int64_t rows = batch * d_inner;
   const bool some = n > 0;
   const size_t need = some ? ss::gated_bwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16,

@@ -83,9 +83,10 @@ __global__ __launch_bounds__(64) void gated_reduce_kernel(GatedArgs p, const flo
 
 }  // namespace
 
-size_t gated_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool, bool given) {
+size_t gated_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool bf16, bool given) {
   const int64_t rows = batch * d_inner, chunks = (seqlen + kC - 1) / kC;
-  return static_cast<size_t>(rows) * sizeof(float) * (3 + (given ? 0 : chunks));
+  return static_cast<size_t>(rows) * sizeof(float) * (3 + (given ? 0 : chunks)) + 16 +
+         (given ? 0 : gated_fwd_ws_bytes(batch, seqlen, d_inner, bf16));
 }
 
 hipError_t launch_gated_bwd(const GatedArgs& a, bool bf16, hipStream_t stream) {
@@ -97,6 +98,8 @@ hipError_t launch_gated_bwd(const GatedArgs& a, bool bf16, hipStream_t stream) {
     f.h_last = nullptr;
     f.states = part + 3 * a.batch * a.d_inner;
     states = f.states;
+    const uintptr_t end = reinterpret_cast<uintptr_t>(f.states + a.batch * a.n_chunks * a.d_inner);
+    f.workspace = reinterpret_cast<void*>((end + 15) / 16 * 16);
     const hipError_t e = launch_gated_fwd(f, bf16, stream);
     if (e != hipSuccess) return e;
   }

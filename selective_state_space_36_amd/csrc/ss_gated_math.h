@@ -32,4 +32,96 @@ __device__ __forceinline__ Decay decay_f(float l) {
   return Decay{a, sqrt_hw(v)};
 }
 
+// ------------------------------------------------------------------ pieces of the recurrence
+//
+// A piece of consecutive steps maps the state before it to the state after it as h -> P h + H.
+// P is the product of the piece's decays and H its end state from zero.  P = 0 means exactly that
+// a sequence starts inside the piece, so that nothing before it may pass, not even an infinity or
+// a NaN; a product that is only too small for float32 is held at the smallest normal number
+// instead (an error below 2^-126 of the state), so that a NaN before it is not lost.
+constexpr float kTinyDecay = 1.17549435e-38f;
+struct Piece {
+  float P, H;
+};
+__device__ __forceinline__ float advance(Piece p, float h) {
+  return p.P == 0.0f ? p.H : fmaf(p.P, h, p.H);
+}
+__device__ __forceinline__ Piece then(Piece first, Piece second) {
+  const float P = first.P == 0.0f || second.P == 0.0f ? 0.0f
+                                                      : fmaxf(first.P * second.P, kTinyDecay);
+  return Piece{P, advance(second, first.H)};
+}
+
+// V consecutive elements per lane as one load or store.
+template <class IO, int V>
+struct Lanes;
+template <>
+struct Lanes<BF16, 1> {
+  using raw = uint16_t;
+  static __device__ __forceinline__ float get(raw r, int) { return BF16::widen(r); }
+  static __device__ __forceinline__ raw put(const float* f) { return BF16::from_float(f[0]); }
+};
+template <>
+struct Lanes<BF16, 2> {
+  using raw = uint32_t;
+  static __device__ __forceinline__ float get(raw r, int v) {
+    return __uint_as_float(v ? r & 0xffff0000u : r << 16);
+  }
+  static __device__ __forceinline__ raw put(const float* f) {
+    return BF16::from_float(f[0]) | static_cast<uint32_t>(BF16::from_float(f[1])) << 16;
+  }
+};
+template <>
+struct Lanes<BF16, 4> {
+  using raw = uint2;
+  static __device__ __forceinline__ float get(raw r, int v) {
+    return Lanes<BF16, 2>::get(v < 2 ? r.x : r.y, v & 1);
+  }
+  static __device__ __forceinline__ raw put(const float* f) {
+    return uint2{Lanes<BF16, 2>::put(f), Lanes<BF16, 2>::put(f + 2)};
+  }
+};
+template <>
+struct Lanes<BF16, 8> {
+  using raw = uint4;
+  static __device__ __forceinline__ float get(raw r, int v) {
+    return Lanes<BF16, 2>::get(v < 2 ? r.x : v < 4 ? r.y : v < 6 ? r.z : r.w, v & 1);
+  }
+  static __device__ __forceinline__ raw put(const float* f) {
+    return uint4{Lanes<BF16, 2>::put(f), Lanes<BF16, 2>::put(f + 2), Lanes<BF16, 2>::put(f + 4),
+                 Lanes<BF16, 2>::put(f + 6)};
+  }
+};
+template <>
+struct Lanes<F32, 1> {
+  using raw = float;
+  static __device__ __forceinline__ float get(raw r, int) { return r; }
+  static __device__ __forceinline__ raw put(const float* f) { return f[0]; }
+};
+template <>
+struct Lanes<F32, 2> {
+  using raw = float2;
+  static __device__ __forceinline__ float get(raw r, int v) { return v ? r.y : r.x; }
+  static __device__ __forceinline__ raw put(const float* f) { return float2{f[0], f[1]}; }
+};
+template <>
+struct Lanes<F32, 4> {
+  using raw = float4;
+  static __device__ __forceinline__ float get(raw r, int v) {
+    return v == 0 ? r.x : v == 1 ? r.y : v == 2 ? r.z : r.w;
+  }
+  static __device__ __forceinline__ raw put(const float* f) {
+    return float4{f[0], f[1], f[2], f[3]};
+  }
+};
+
+template <class IO, int V>
+__device__ __forceinline__ typename Lanes<IO, V>::raw load_lanes(const typename IO::elem* p) {
+  return *reinterpret_cast<const typename Lanes<IO, V>::raw*>(p);
+}
+template <class IO, int V>
+__device__ __forceinline__ void store_lanes(typename IO::elem* p, const float* f) {
+  *reinterpret_cast<typename Lanes<IO, V>::raw*>(p) = Lanes<IO, V>::put(f);
+}
+
 }  // namespace ss
