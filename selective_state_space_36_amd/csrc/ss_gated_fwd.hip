@@ -35,27 +35,29 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, int
   const bool active = c0 < p.d_inner;
   const int64_t c = active ? c0 : 0;
   const int64_t t0 = static_cast<int64_t>(seg) * kTile + wave * kSteps;
-  const int64_t last = p.seqlen - 1;
-
   const int64_t row0 = b * p.seqlen;
-  auto at = [&](const void* base, int j) {  // this lane's channels at the wave's step j
-    const int64_t t = t0 + j < last ? t0 + j : last;
-    return static_cast<const elem*>(base) + (row0 + t) * p.d_inner + c;
-  };
+  // the wave's rows: kSteps of them, or what is left of the sequence (none past its end)
+  const int64_t left = p.seqlen - t0;
+  const int n = left < 0 ? 0 : left < kSteps ? static_cast<int>(left) : kSteps;
+  const int64_t first = (row0 + t0) * p.d_inner;
+  const uint32_t row = static_cast<uint32_t>(p.d_inner) * sizeof(elem);
+  const uint32_t col = active ? static_cast<uint32_t>(c) * sizeof(elem) : kOffNone;
+  auto rows = [&](const void* base) { return rows_of<IO, V>(base, n ? first : 0, n * row); };
   typename L::raw xr[kSteps], rr[kSteps], ir[kSteps], zr[kSteps];
+  {
+    const Rows<IO, V> R = rows(p.r), I = rows(p.i), X = rows(p.x);
 #pragma unroll
-  for (int j = 0; j < kSteps; ++j) {
-    rr[j] = load_lanes<IO, V>(at(p.r, j));
-    ir[j] = load_lanes<IO, V>(at(p.i, j));
-    xr[j] = load_lanes<IO, V>(at(p.x, j));
+    for (int j = 0; j < kSteps; ++j) {
+      rr[j] = R.load(col + j * row);
+      ir[j] = I.load(col + j * row);
+      xr[j] = X.load(col + j * row);
+    }
   }
   uint32_t fresh = 0;  // bit j: a sequence starts at step j
   if (PACKED) {
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) {
-      const int64_t t = t0 + j < last ? t0 + j : last;
-      fresh |= (p.starts[row0 + t] && t0 + j <= last ? 1u : 0u) << j;
-    }
+    for (int j = 0; j < kSteps; ++j)
+      if (j < n) fresh |= (p.starts[row0 + t0 + j] ? 1u : 0u) << j;
     fresh = __builtin_amdgcn_readfirstlane(fresh);
   }
   float A[V], rb[V], ib[V];
@@ -72,7 +74,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, int
   for (int v = 0; v < V; ++v) piece[v] = Piece{1.0f, 0.0f};
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
-    const bool beyond = t0 + j > last;
+    const bool beyond = j >= n;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const float rg = sigmoid_f(L::get(rr[j], v) + rb[v]);
@@ -90,8 +92,9 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, int
     for (int v = 0; v < V; ++v) piece[v].P = 0.0f;
   }
   if (GATE) {
+    const Rows<IO, V> Z = rows(p.z);
 #pragma unroll
-    for (int j = 0; j < kSteps; ++j) zr[j] = load_lanes<IO, V>(at(p.z, j));
+    for (int j = 0; j < kSteps; ++j) zr[j] = Z.load(col + j * row);
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) pieces[wave][v][lane] = piece[v];
@@ -131,10 +134,9 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, int
     for (int v = 0; v < V; ++v) h[v] = advance(pieces[k][v][lane], h[v]);
   }
 
+  const Rows<IO, V> O = rows(p.out);
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
-    const int64_t t = t0 + j;
-    if (t > last) break;
     float y[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -142,18 +144,20 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, int
       h[v] = cut ? in[j][v] : fmaf(a[j][v], h[v], in[j][v]);
       y[v] = GATE ? h[v] * silu_f(L::get(zr[j], v)) : h[v];
     }
-    if (active) {
-      if (p.out)
-        store_lanes<IO, V>(static_cast<elem*>(p.out) + (row0 + t) * p.d_inner + c, y);
-      if (p.states && ((t + 1) % SS_GATED_CHUNK == 0 || t == last)) {
-        float* s = p.states + (b * p.n_chunks + t / SS_GATED_CHUNK) * p.d_inner + c;
+    if (p.out) O.store(y, col + j * row);
+  }
+  // The wave that holds the last step of a chunk or of the sequence (its steps past the end left
+  // the state as it was).
+  static_assert(SS_GATED_CHUNK % kSteps == 0, "a chunk ends with a wave's last step");
+  if (n > 0 && active) {
+    if (p.states && (left <= kSteps || (t0 + kSteps) % SS_GATED_CHUNK == 0)) {
+      float* s = p.states + (b * p.n_chunks + t0 / SS_GATED_CHUNK) * p.d_inner + c;
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = h[v];
-      }
-      if (p.h_last && t == last) {
+      for (int v = 0; v < V; ++v) s[v] = h[v];
+    }
+    if (p.h_last && left <= kSteps) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.h_last[b * p.d_inner + c + v] = h[v];
-      }
+      for (int v = 0; v < V; ++v) p.h_last[b * p.d_inner + c + v] = h[v];
     }
   }
 }

@@ -16,11 +16,7 @@ __device__ __forceinline__ float sigmoid_f(float v) {
 // the series -w (1 + w/2 + w^2/6 + w^3/24 + w^4/120 + w^5/720), whose rest is below w^6/5040 =
 // 5e-8 relative there; elsewhere 1 - a a as one fused multiply-add, where the one-ulp error of a
 // grows by at most 2 a^2 / (1 - a^2) = 7.
-struct Decay {
-  float a, s;
-};
-__device__ __forceinline__ Decay decay_f(float l) {
-  const float a = exp2_hw(l * kLog2e);
+__device__ __forceinline__ float decay_scale(float l, float a) {
   const float w = 2.0f * l;
   float q = 1.0f / 720.0f;
   q = fmaf(q, w, 1.0f / 120.0f);
@@ -29,7 +25,14 @@ __device__ __forceinline__ Decay decay_f(float l) {
   q = fmaf(q, w, 0.5f);
   q = fmaf(q, w, 1.0f);
   const float v = w > -0.25f ? -w * q : fmaf(-a, a, 1.0f);
-  return Decay{a, sqrt_hw(v)};
+  return sqrt_hw(v);
+}
+struct Decay {
+  float a, s;
+};
+__device__ __forceinline__ Decay decay_f(float l) {
+  const float a = exp2_hw(l * kLog2e);
+  return Decay{a, decay_scale(l, a)};
 }
 
 // ------------------------------------------------------------------ pieces of the recurrence
@@ -115,13 +118,43 @@ struct Lanes<F32, 4> {
   }
 };
 
+// A run of consecutive rows of one array, V channels per lane: a buffer resource over exactly
+// those rows, so that rows past the end read as 0 and are not written, lanes past the last channel
+// pass kOffNone and do neither, and an access costs one 32-bit offset register that all arrays
+// share.  The whole offset is in that register: the range check subtracts a scalar offset from
+// the size, which is no check where the difference would be negative.
 template <class IO, int V>
-__device__ __forceinline__ typename Lanes<IO, V>::raw load_lanes(const typename IO::elem* p) {
-  return *reinterpret_cast<const typename Lanes<IO, V>::raw*>(p);
-}
+struct Rows {
+  using raw = typename Lanes<IO, V>::raw;
+  rsrc_t r;
+  __device__ __forceinline__ raw load(uint32_t off) const {
+    if constexpr (sizeof(raw) == 2)
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+    else if constexpr (sizeof(raw) == 4)
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    else if constexpr (sizeof(raw) == 8)
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+    else
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  }
+  __device__ __forceinline__ void store(const float* f, uint32_t off) const {
+    const raw v = Lanes<IO, V>::put(f);
+    using v2u = __attribute__((ext_vector_type(2))) unsigned int;
+    using v4u = __attribute__((ext_vector_type(4))) unsigned int;
+    if constexpr (sizeof(raw) == 2)
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, 0);
+    else if constexpr (sizeof(raw) == 4)
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+    else if constexpr (sizeof(raw) == 8)
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, v), r, off, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, off, 0, 0);
+  }
+};
+// `first`: the first row's element offset in the array, `bytes`: of the whole run (below 2^31).
 template <class IO, int V>
-__device__ __forceinline__ void store_lanes(typename IO::elem* p, const float* f) {
-  *reinterpret_cast<typename Lanes<IO, V>::raw*>(p) = Lanes<IO, V>::put(f);
+__device__ __forceinline__ Rows<IO, V> rows_of(const void* base, int64_t first, uint32_t bytes) {
+  return Rows<IO, V>{make_buf(static_cast<const typename IO::elem*>(base) + first, bytes)};
 }
 
 }  // namespace ss
