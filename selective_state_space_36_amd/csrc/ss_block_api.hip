@@ -85,9 +85,9 @@ bool sizes_ok(int64_t batch, int64_t seqlen, int64_t d_inner) {
          mul_ok(batch, d_inner, &n) && mul_ok(n, seqlen + 8, &n) && n / 64 < kMaxGrid;
 }
 
-// The recurrence's launch has at most one workgroup per 64 steps and 64 channels of a batch row.
+// The sequence operators launch at most one workgroup per 16 steps and 64 channels of a batch row.
 ss_status check_tiles(int64_t batch, int64_t seqlen, int64_t d_inner) {
-  if (batch * ((d_inner + 63) / 64) * ((seqlen + 63) / 64) > kMaxGrid)
+  if (batch * ((d_inner + 63) / 64) * ((seqlen + 15) / 16) > kMaxGrid)
     return fail(SS_ERR_INVALID_ARG, "too many tiles (batch * seqlen * d_inner)");
   return SS_OK;
 }
@@ -333,6 +333,7 @@ ss_status ss_causal_conv_fwd(const void* x, const float* weight, const float* bi
   if ((s = check_width(k)) != SS_OK) return s;
   if ((s = check_sizes(batch, seqlen, d_inner, &n)) != SS_OK) return s;
   if (n == 0) return ok();
+  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
   const Arr in[] = {{"x", x, n, es, true}, {"weight", weight, d_inner * k, 4, true},
                     {"bias", bias, d_inner, 4, false},
                     {"x_prev", x_prev, batch * (k - 1) * d_inner, es, false},
@@ -364,6 +365,7 @@ ss_status ss_causal_conv_bwd(const void* x, const float* weight, const float* bi
   if ((s = check_width(k)) != SS_OK) return s;
   if ((s = check_sizes(batch, seqlen, d_inner, &n)) != SS_OK) return s;
   if (d_inner == 0) return ok();
+  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
   const bool some = n > 0;
   const int64_t prev = batch * (k - 1) * d_inner;
   if (dx_prev && !x_prev && prev > 0)

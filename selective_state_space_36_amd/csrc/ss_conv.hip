@@ -1,149 +1,444 @@
 // ss_conv.hip -- the causal depthwise convolution, its gradients and its one-token form.
+//
+// All three stream: each lane owns V channels, holds their k taps in registers and walks steps
+// with the last k - 1 inputs in registers, so an input is read once per wave.  Where sequences
+// start inside a row, taps that would cross a start are left out by comparing the number of starts
+// up to the two steps; these numbers are the same for the whole wave (scalar registers).
 #include "ss_block.h"
 #include "ss_gated_math.h"
+
+#include <type_traits>
 
 namespace ss {
 namespace {
 
-// x at step t of row b (t may be negative: the window before the sequence).
-template <class IO>
-__device__ __forceinline__ float tap(const ConvArgs& p, int64_t b, int64_t t, int64_t d) {
-  using elem = typename IO::elem;
-  if (t >= 0) return IO::load(static_cast<const elem*>(p.x), (b * p.seqlen + t) * p.d_inner + d);
-  return p.x_prev ? IO::load(static_cast<const elem*>(p.x_prev),
-                             (b * (p.k - 1) + p.k - 1 + t) * p.d_inner + d)
-                  : 0.0f;
-}
+constexpr int kFwdSteps = 16;  // steps of one wave of the forward
+constexpr int kWaves = 4;      // waves of a workgroup, on consecutive runs of steps
+constexpr int kStride = 8;     // steps whose rows the backward has in flight
 
-__device__ __forceinline__ bool fresh(const ConvArgs& p, int64_t b, int64_t t) {
-  return p.starts && p.starts[b * p.seqlen + t];
-}
-
-template <class IO>
-__device__ float preact(const ConvArgs& p, int64_t b, int64_t t, int64_t d) {
-  int far = 0;  // the oldest tap in the same sequence
-  while (far < p.k - 1 && !(t - far >= 0 && fresh(p, b, t - far))) ++far;
-  float acc = p.bias ? p.bias[d] : 0.0f;
-  for (int lag = far; lag >= 0; --lag)
-    acc = fmaf(p.weight[d * p.k + p.k - 1 - lag], tap<IO>(p, b, t - lag, d), acc);
-  return acc;
-}
-
-template <class IO>
-__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs p) {
-  const int64_t e = blockIdx.x * 256ll + threadIdx.x;
-  if (e >= p.batch * p.seqlen * p.d_inner) return;
-  const int64_t d = e % p.d_inner, bt = e / p.d_inner;
-  const float v = preact<IO>(p, bt / p.seqlen, bt % p.seqlen, d);
-  static_cast<typename IO::elem*>(p.out)[e] = IO::from_float(p.silu ? silu_f(v) : v);
-}
-
-template <class IO>
-__device__ float pre_grad(const ConvArgs& p, int64_t b, int64_t t, int64_t d) {
-  float g = IO::load(static_cast<const typename IO::elem*>(p.dout),
-                     (b * p.seqlen + t) * p.d_inner + d);
-  if (p.silu) {
-    const float v = preact<IO>(p, b, t, d);
-    const float sg = sigmoid_f(v);
-    g *= sg * fmaf(v, 1.0f - sg, 1.0f);
+// One lane's taps: w[j][v] for channels c .. c + V - 1, and the bias.
+template <int V, int K>
+struct Taps {
+  float w[K][V], bias[V];
+  __device__ __forceinline__ void load(const ConvArgs& p, int64_t c) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int j = 0; j < K; ++j) w[j][v] = p.weight[(c + v) * K + j];
+      bias[v] = p.bias ? p.bias[c + v] : 0.0f;
+    }
   }
-  return g;
+};
+
+// Bit j: a sequence starts at step t + j of row b, for j < n.
+__device__ __forceinline__ uint32_t starts_mask(const ConvArgs& p, int64_t b, int64_t t, int n) {
+  const int lane = threadIdx.x & 63;
+  const bool in = lane < n && t + lane >= 0 && t + lane < p.seqlen;
+  return static_cast<uint32_t>(__ballot(in && p.starts[b * p.seqlen + (in ? t + lane : 0)]));
 }
 
-// dx (and dx_prev for t < 0), one thread per element.
-template <class IO>
-__global__ __launch_bounds__(256) void conv_dx_kernel(ConvArgs p) {
-  const int64_t e = blockIdx.x * 256ll + threadIdx.x;
-  const int64_t steps = p.seqlen + p.k - 1;
-  if (e >= p.batch * steps * p.d_inner) return;
-  const int64_t d = e % p.d_inner, bt = e / p.d_inner;
-  const int64_t b = bt / steps, t = bt % steps - (p.k - 1);
-  if (t < 0 && !p.dx_prev) return;
-  float acc = 0.0f;
-  for (int lag = 0; lag < p.k && t + lag < p.seqlen; ++lag) {
-    if (t + lag < 0) continue;
-    if (lag > 0 && fresh(p, b, t + lag)) break;  // a start between t and t + lag cuts the tap
-    acc = fmaf(p.weight[d * p.k + p.k - 1 - lag], pre_grad<IO>(p, b, t + lag, d), acc);
-  }
+// Where a wave works: a run of steps of one batch row and 64 V channels.
+struct Place {
+  int64_t b, t0, c;
+  bool active;
+};
+template <int V>
+__device__ __forceinline__ Place place(const ConvArgs& p, int64_t group, int64_t item,
+                                       int64_t runs, int64_t run_steps) {
+  const int64_t c0 = group * (64 * V) + static_cast<int64_t>(threadIdx.x & 63) * V;
+  const bool active = c0 < p.d_inner;
+  return Place{item / runs, item % runs * run_steps, active ? c0 : 0, active};
+}
+
+// The k - 1 rows before step t0 (t0 is 0 or at least k - 1): of x, or of x_prev, or none.
+template <class IO, int V, int K>
+__device__ __forceinline__ Rows<IO, V> rows_before(const ConvArgs& p, int64_t b, int64_t t0) {
+  const uint32_t bytes = static_cast<uint32_t>((K - 1) * p.d_inner) * sizeof(typename IO::elem);
+  if (t0 > 0) return rows_of<IO, V>(p.x, (b * p.seqlen + t0 - (K - 1)) * p.d_inner, bytes);
+  return rows_of<IO, V>(p.x_prev, p.x_prev ? b * (K - 1) * p.d_inner : 0, p.x_prev ? bytes : 0);
+}
+
+template <class IO, int V, int K, bool PACKED>
+__global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs p, uint32_t groups,
+                                                               int64_t runs) {
   using elem = typename IO::elem;
-  if (t >= 0)
-    static_cast<elem*>(p.dx)[(b * p.seqlen + t) * p.d_inner + d] = IO::from_float(acc);
-  else
-    static_cast<elem*>(p.dx_prev)[(b * (p.k - 1) + p.k - 1 + t) * p.d_inner + d] =
-        IO::from_float(acc);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t item = static_cast<int64_t>(blockIdx.x / groups) * kWaves + wave;
+  if (item >= p.batch * runs) return;
+  const Place at = place<V>(p, blockIdx.x % groups, item, runs, kFwdSteps);
+  const int64_t left = p.seqlen - at.t0;
+  const int n = left < kFwdSteps ? static_cast<int>(left) : kFwdSteps;
+  const uint32_t row = static_cast<uint32_t>(p.d_inner) * sizeof(elem);
+  const uint32_t col = at.active ? static_cast<uint32_t>(at.c) * sizeof(elem) : kOffNone;
+  const int64_t first = (at.b * p.seqlen + at.t0) * p.d_inner;
+  const auto H = rows_before<IO, V, K>(p, at.b, at.t0);
+  const auto X = rows_of<IO, V>(p.x, first, n * row);
+  typename Lanes<IO, V>::raw x[kFwdSteps + K - 1];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) x[j] = H.load(col + j * row);
+#pragma unroll
+  for (int j = 0; j < kFwdSteps; ++j) x[K - 1 + j] = X.load(col + j * row);
+  // seq[j]: starts up to the row of x[j]; the first row's own start does not matter
+  uint32_t mask = 0;
+  if (PACKED) mask = starts_mask(p, at.b, at.t0 - (K - 1), kFwdSteps + K - 1);
+  Taps<V, K> taps;
+  taps.load(p, at.c);
+  const auto O = rows_of<IO, V>(p.out, first, n * row);
+#pragma unroll
+  for (int j = 0; j < kFwdSteps; ++j) {
+    float y[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) y[v] = taps.bias[v];
+#pragma unroll
+    for (int q = 0; q < K; ++q) {  // x[j + q] is K - 1 - q steps back
+      // a start at one of the steps after that row, up to this one, cuts it off
+      const uint32_t between = ((1u << (K - 1 - q)) - 1) << (j + q + 1);
+      if (PACKED && (mask & between)) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        y[v] = fmaf(taps.w[q][v], Lanes<IO, V>::get(x[j + q], v), y[v]);
+    }
+    if (p.silu) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) y[v] = silu_f(y[v]);
+    }
+    O.store(y, col + j * row);
+  }
 }
 
-// dweight and dbias, one thread per channel over all tokens.
-template <class IO>
-__global__ __launch_bounds__(64) void conv_dw_kernel(ConvArgs p) {
-  const int64_t d = blockIdx.x * 64ll + threadIdx.x;
-  if (d >= p.d_inner) return;
-  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s = 0.0f;
-  for (int64_t b = 0; b < p.batch; ++b)
-    for (int64_t t = 0; t < p.seqlen; ++t) {
-      const float g = pre_grad<IO>(p, b, t, d);
-      s += g;
-      for (int lag = 0; lag < p.k; ++lag) {
-        w[lag] = fmaf(g, tap<IO>(p, b, t - lag, d), w[lag]);
-        if (t - lag < 0 ? false : fresh(p, b, t - lag)) break;
+// One wave walks `steps` steps from t0 and the k - 1 after them (whose g the last dx need; their
+// own dx and sums belong to the next wave), kStride rows in flight.  The rows of sums of a
+// workgroup's waves are added in LDS into part[workgroup][K + 1][d_inner].
+template <class IO, int V, int K, bool PACKED>
+__global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint32_t groups,
+                                                               int64_t runs, int32_t steps,
+                                                               float* part) {
+  using elem = typename IO::elem;
+  using L = Lanes<IO, V>;
+  __shared__ float fold[kWaves][(K + 1) * V][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t line = blockIdx.x / groups;
+  const int64_t item = line * kWaves + wave;
+  const bool some = item < p.batch * runs;
+  const Place at = place<V>(p, blockIdx.x % groups, some ? item : 0, runs, steps);
+  const int64_t left = p.seqlen - at.t0;
+  const int n = !some ? 0 : left < steps ? static_cast<int>(left) : steps;  // steps of its own
+  const int all = n + K - 1;                                                // steps it walks
+  const int have = !some ? 0 : left < all ? static_cast<int>(left) : all;   // that exist
+  const uint32_t row = static_cast<uint32_t>(p.d_inner) * sizeof(elem);
+  const uint32_t col = at.active ? static_cast<uint32_t>(at.c) * sizeof(elem) : kOffNone;
+  const int64_t first = (at.b * p.seqlen + at.t0) * p.d_inner;
+
+  float dw[K][V], db[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    db[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j][v] = 0.0f;
+  }
+  if (some) {
+    Taps<V, K> taps;
+    taps.load(p, at.c);
+    // x and g at the K - 1 steps before the current one, and the starts up to them
+    float xw[K][V], gw[K][V];
+    uint32_t seq[K];
+    {
+      const auto H = rows_before<IO, V, K>(p, at.b, at.t0);
+      uint32_t mask = 0;
+      if (PACKED) mask = starts_mask(p, at.b, at.t0 - (K - 1), K - 1);
+      uint32_t s = 0;
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        const auto raw = H.load(col + j * row);
+        if (PACKED) s += mask >> j & 1;
+        seq[j] = s;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          xw[j][v] = L::get(raw, v);
+          gw[j][v] = 0.0f;
+        }
+      }
+      seq[K - 1] = s;
+    }
+    const bool prev = at.t0 == 0 && p.dx_prev;
+    const auto DP = rows_of<IO, V>(p.dx_prev, prev ? at.b * (K - 1) * p.d_inner : 0,
+                                   prev ? (K - 1) * row : 0);
+    typename L::raw xn[kStride], gn[kStride];
+    uint32_t starts = 0;
+    // rows are addressed kStride at a time, so that 32-bit offsets reach for any d_inner
+    auto fetch = [&](int s0) {
+      const int more = have - s0 < 0 ? 0 : have - s0 < kStride ? have - s0 : kStride;
+      const int64_t f = more ? first + s0 * p.d_inner : 0;
+      const auto X = rows_of<IO, V>(p.x, f, more * row);
+      const auto G = rows_of<IO, V>(p.dout, f, more * row);
+#pragma unroll
+      for (int j = 0; j < kStride; ++j) {
+        xn[j] = X.load(col + j * row);
+        gn[j] = G.load(col + j * row);
+      }
+      if (PACKED) starts = starts_mask(p, at.b, at.t0 + s0, kStride);
+    };
+    fetch(0);
+    for (int s0 = 0; s0 < all; s0 += kStride) {
+      typename L::raw xr[kStride], gr[kStride];
+#pragma unroll
+      for (int j = 0; j < kStride; ++j) {
+        xr[j] = xn[j];
+        gr[j] = gn[j];
+      }
+      const uint32_t now = starts;
+      // dx trails by K - 1 steps
+      static_assert(kStride >= K, "the first rows hold a whole window");
+      const int skip = s0 ? 0 : K - 1, r0 = s0 ? s0 - (K - 1) : 0;
+      const int rest = n - r0 < 0 ? 0 : n - r0 < kStride ? n - r0 : kStride;
+      const auto DX = rows_of<IO, V>(p.dx, first + (rest ? r0 * p.d_inner : 0), rest * row);
+      if (s0 + kStride < all) fetch(s0 + kStride);
+#pragma unroll
+      for (int j = 0; j < kStride; ++j) {
+        const int s = s0 + j;
+        if (s >= all) break;
+        if (PACKED) seq[K - 1] += now >> j & 1;
+        float g[V], pre[V], dx[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          xw[K - 1][v] = L::get(xr[j], v);
+          g[v] = L::get(gr[j], v);
+          pre[v] = taps.bias[v];
+        }
+#pragma unroll
+        for (int q = 0; q < K; ++q) {
+          if (PACKED && seq[q] != seq[K - 1]) continue;
+#pragma unroll
+          for (int v = 0; v < V; ++v) pre[v] = fmaf(taps.w[q][v], xw[q][v], pre[v]);
+        }
+        if (p.silu) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            const float sg = sigmoid_f(pre[v]);
+            g[v] *= sg * fmaf(pre[v], 1.0f - sg, 1.0f);
+          }
+        }
+        if (s >= have) {  // past the end of the sequence: no gradient, whatever silu' gave
+#pragma unroll
+          for (int v = 0; v < V; ++v) g[v] = 0.0f;
+        }
+        if (s < n) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) db[v] += g[v];
+#pragma unroll
+          for (int q = 0; q < K; ++q) {
+            if (PACKED && seq[q] != seq[K - 1]) continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v) dw[q][v] = fmaf(g[v], xw[q][v], dw[q][v]);
+          }
+        }
+        // the step K - 1 back now has every g it takes part in: gw[q] is g at q steps after it
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          gw[K - 1][v] = g[v];
+          dx[v] = 0.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < K; ++q) {
+          if (PACKED && seq[q] != seq[0]) continue;
+#pragma unroll
+          for (int v = 0; v < V; ++v) dx[v] = fmaf(taps.w[K - 1 - q][v], gw[q][v], dx[v]);
+        }
+        if (s >= K - 1)
+          DX.store(dx, col + (j - skip) * row);
+        else if (prev)
+          DP.store(dx, col + s * row);
+#pragma unroll
+        for (int q = 0; q + 1 < K; ++q) {
+          seq[q] = seq[q + 1];
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            xw[q][v] = xw[q + 1][v];
+            gw[q][v] = gw[q + 1][v];
+          }
+        }
       }
     }
-  for (int lag = 0; lag < p.k; ++lag) p.dweight[d * p.k + p.k - 1 - lag] = w[lag];
-  if (p.dbias) p.dbias[d] = s;
-}
-
-template <class IO>
-__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs p) {
-  using elem = typename IO::elem;
-  const int64_t e = blockIdx.x * 256ll + threadIdx.x;
-  if (e >= p.batch * p.d_inner) return;
-  const int64_t b = e / p.d_inner, d = e % p.d_inner;
-  elem* st = static_cast<elem*>(p.conv_state) + b * (p.k - 1) * p.d_inner + d;
-  const elem xv = static_cast<const elem*>(p.x)[e];
-  float acc = p.bias ? p.bias[d] : 0.0f;
-  for (int j = 0; j < p.k; ++j) {
-    const elem v = j < p.k - 1 ? st[j * p.d_inner] : xv;
-    acc = fmaf(p.weight[d * p.k + j], IO::widen(v), acc);
-    if (j > 0) st[(j - 1) * p.d_inner] = v;
   }
-  static_cast<elem*>(p.out)[e] = IO::from_float(p.silu ? silu_f(acc) : acc);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+#pragma unroll
+    for (int q = 0; q < K; ++q) fold[wave][q * V + v][lane] = dw[q][v];
+    fold[wave][K * V + v][lane] = db[v];
+  }
+  __syncthreads();
+  if (!at.active) return;
+  for (int q = wave; q <= K; q += kWaves) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float s = fold[0][q * V + v][lane];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) s += fold[w][q * V + v][lane];
+      part[(line * (K + 1) + q) * p.d_inner + at.c + v] = s;
+    }
+  }
 }
 
-dim3 blocks(int64_t n, int per) { return dim3(static_cast<unsigned>((n + per - 1) / per)); }
+// Sums part[lines][K + 1][d_inner] over the lines: 16 threads of lines by 16 channels, then the 16
+// in order.
+__global__ __launch_bounds__(256) void conv_reduce_kernel(ConvArgs p, const float* part,
+                                                          int64_t lines) {
+  __shared__ float lds[16][17];
+  const int q = blockIdx.y;
+  if (q == p.k && !p.dbias) return;
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+  const int64_t d = blockIdx.x * 16ll + x;
+  float acc = 0.0f;
+  if (d < p.d_inner) {
+    const float* src = part + q * p.d_inner + d;
+    for (int64_t r = y; r < lines; r += 16) acc += src[r * (p.k + 1) * p.d_inner];
+  }
+  lds[y][x] = acc;
+  __syncthreads();
+  if (y == 0 && d < p.d_inner) {
+    float s = lds[0][x];
+    for (int k = 1; k < 16; ++k) s += lds[k][x];
+    if (q == p.k)
+      p.dbias[d] = s;
+    else
+      p.dweight[d * p.k + q] = s;
+  }
+}
+
+// One token: V channels of one batch row per thread.
+template <class IO, int V, int K>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs p, int64_t lanes) {
+  using elem = typename IO::elem;
+  using raw = typename Lanes<IO, V>::raw;
+  const int64_t id = blockIdx.x * 256ll + threadIdx.x;
+  if (id >= p.batch * lanes) return;
+  const int64_t b = id / lanes, c = id % lanes * V;
+  raw* out = reinterpret_cast<raw*>(static_cast<elem*>(p.out) + b * p.d_inner + c);
+  raw x[K];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j)
+    x[j] = *reinterpret_cast<const raw*>(static_cast<const elem*>(p.conv_state) +
+                                         (b * (K - 1) + j) * p.d_inner + c);
+  x[K - 1] = *reinterpret_cast<const raw*>(static_cast<const elem*>(p.x) + b * p.d_inner + c);
+  Taps<V, K> taps;
+  taps.load(p, c);
+  float y[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    y[v] = taps.bias[v];
+#pragma unroll
+    for (int j = 0; j < K; ++j) y[v] = fmaf(taps.w[j][v], Lanes<IO, V>::get(x[j], v), y[v]);
+    if (p.silu) y[v] = silu_f(y[v]);
+  }
+  *out = Lanes<IO, V>::put(y);
+#pragma unroll
+  for (int j = 0; j + 1 < K; ++j)
+    *reinterpret_cast<raw*>(static_cast<elem*>(p.conv_state) + (b * (K - 1) + j) * p.d_inner +
+                            c) = x[j + 1];
+}
+
+// Steps per wave of the backward.
+constexpr int kBwdSteps = 64;
+
+int64_t lines_of(int64_t batch, int64_t seqlen) {
+  const int64_t runs = (seqlen + kBwdSteps - 1) / kBwdSteps;
+  return (batch * runs + kWaves - 1) / kWaves;
+}
+
+template <class F>
+void with_width(int32_t k, F f) {
+  using std::integral_constant;
+  if (k == 1) f(integral_constant<int, 1>{});
+  else if (k == 2) f(integral_constant<int, 2>{});
+  else if (k == 3) f(integral_constant<int, 3>{});
+  else f(integral_constant<int, 4>{});
+}
+
+template <class IO, int V>
+hipError_t launch_fwd(const ConvArgs& a, hipStream_t stream) {
+  const int64_t groups = (a.d_inner + 64 * V - 1) / (64 * V);
+  const int64_t runs = (a.seqlen + kFwdSteps - 1) / kFwdSteps;
+  const dim3 grid(static_cast<unsigned>((a.batch * runs + kWaves - 1) / kWaves * groups));
+  const dim3 block(64 * kWaves);
+  const uint32_t g = static_cast<uint32_t>(groups);
+  with_width(a.k, [&](auto k) {
+    if (a.starts)
+      hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, true>), grid, block, 0, stream, a, g, runs);
+    else
+      hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, false>), grid, block, 0, stream, a, g, runs);
+  });
+  return hipGetLastError();
+}
+
+template <class IO, int V>
+hipError_t launch_bwd(const ConvArgs& a, hipStream_t stream) {
+  const int64_t groups = (a.d_inner + 64 * V - 1) / (64 * V);
+  const int64_t runs = (a.seqlen + kBwdSteps - 1) / kBwdSteps;
+  const int64_t lines = lines_of(a.batch, a.seqlen);
+  const dim3 grid(static_cast<unsigned>(lines * groups)), block(64 * kWaves);
+  const uint32_t g = static_cast<uint32_t>(groups);
+  float* part = static_cast<float*>(a.workspace);
+  with_width(a.k, [&](auto k) {
+    if (a.starts)
+      hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, true>), grid, block, 0, stream, a, g, runs,
+                         kBwdSteps, part);
+    else
+      hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, false>), grid, block, 0, stream, a, g, runs,
+                         kBwdSteps, part);
+  });
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(conv_reduce_kernel,
+                     dim3(static_cast<unsigned>((a.d_inner + 15) / 16), a.k + 1), dim3(256), 0,
+                     stream, a, part, lines);
+  return hipGetLastError();
+}
+
+template <class IO, int V>
+hipError_t launch_step(const ConvArgs& a, hipStream_t stream) {
+  const int64_t lanes = a.d_inner / V;
+  const dim3 grid(static_cast<unsigned>((a.batch * lanes + 255) / 256));
+  with_width(a.k, [&](auto k) {
+    hipLaunchKernelGGL((conv_step_kernel<IO, V, k>), grid, dim3(256), 0, stream, a, lanes);
+  });
+  return hipGetLastError();
+}
+
+// Whether v channels per lane fit: whole groups, and every io pointer aligned to one.
+template <class IO>
+bool lanes_of(const ConvArgs& a, int v) {
+  const void* all[] = {a.x, a.x_prev, a.out, a.conv_state, a.dout, a.dx, a.dx_prev};
+  uintptr_t bits = 0;
+  for (const void* q : all) bits |= reinterpret_cast<uintptr_t>(q);
+  return a.d_inner % v == 0 && bits % (v * sizeof(typename IO::elem)) == 0;
+}
 
 }  // namespace
 
-size_t conv_bwd_ws_bytes(int64_t, int64_t, int64_t, int32_t, bool) { return 0; }
+size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int32_t k, bool) {
+  return static_cast<size_t>(lines_of(batch, seqlen) * (k + 1) * d_inner) * sizeof(float);
+}
 
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf16, hipStream_t stream) {
-  const dim3 grid = blocks(a.batch * a.seqlen * a.d_inner, 256);
-  if (bf16)
-    hipLaunchKernelGGL((conv_fwd_kernel<BF16>), grid, dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL((conv_fwd_kernel<F32>), grid, dim3(256), 0, stream, a);
-  return hipGetLastError();
+  if (bf16) {
+    if (lanes_of<BF16>(a, 4)) return launch_fwd<BF16, 4>(a, stream);
+    return lanes_of<BF16>(a, 2) ? launch_fwd<BF16, 2>(a, stream) : launch_fwd<BF16, 1>(a, stream);
+  }
+  return lanes_of<F32>(a, 2) ? launch_fwd<F32, 2>(a, stream) : launch_fwd<F32, 1>(a, stream);
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, bool bf16, hipStream_t stream) {
-  const dim3 gx = blocks(a.batch * (a.seqlen + a.k - 1) * a.d_inner, 256);
-  const dim3 gw = blocks(a.d_inner, 64);
-  if (bf16) {
-    hipLaunchKernelGGL((conv_dx_kernel<BF16>), gx, dim3(256), 0, stream, a);
-    hipLaunchKernelGGL((conv_dw_kernel<BF16>), gw, dim3(64), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((conv_dx_kernel<F32>), gx, dim3(256), 0, stream, a);
-    hipLaunchKernelGGL((conv_dw_kernel<F32>), gw, dim3(64), 0, stream, a);
-  }
-  return hipGetLastError();
+  if (bf16)
+    return lanes_of<BF16>(a, 2) ? launch_bwd<BF16, 2>(a, stream) : launch_bwd<BF16, 1>(a, stream);
+  return lanes_of<F32>(a, 2) ? launch_bwd<F32, 2>(a, stream) : launch_bwd<F32, 1>(a, stream);
 }
 
 hipError_t launch_conv_step(const ConvArgs& a, bool bf16, hipStream_t stream) {
-  const dim3 grid = blocks(a.batch * a.d_inner, 256);
   if (bf16)
-    hipLaunchKernelGGL((conv_step_kernel<BF16>), grid, dim3(256), 0, stream, a);
-  else
-    hipLaunchKernelGGL((conv_step_kernel<F32>), grid, dim3(256), 0, stream, a);
-  return hipGetLastError();
+    return lanes_of<BF16>(a, 4) ? launch_step<BF16, 4>(a, stream)
+                                : launch_step<BF16, 1>(a, stream);
+  return lanes_of<F32>(a, 4) ? launch_step<F32, 4>(a, stream) : launch_step<F32, 1>(a, stream);
 }
 
 }  // namespace ss

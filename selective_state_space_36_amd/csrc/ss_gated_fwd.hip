@@ -54,12 +54,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_fwd_kernel(GatedArgs p, int
     }
   }
   uint32_t fresh = 0;  // bit j: a sequence starts at step j
-  if (PACKED) {
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j)
-      if (j < n) fresh |= (p.starts[row0 + t0 + j] ? 1u : 0u) << j;
-    fresh = __builtin_amdgcn_readfirstlane(fresh);
-  }
+  if (PACKED) fresh = static_cast<uint32_t>(__ballot(lane < n && p.starts[row0 + t0 + lane]));
   float A[V], rb[V], ib[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {

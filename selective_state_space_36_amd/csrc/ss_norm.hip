@@ -1,48 +1,283 @@
 // ss_norm.hip -- layer norm over the last axis with the residual add, and its gradients.
+//
+// A row lies in the registers of TPR threads (64, 256 or 1024), K groups of V consecutive columns
+// each, so it is read once: the mean, then the squared differences from it, then the output all
+// come from the same registers.  Sums run over the lanes of a wave by DPP, over the waves through
+// LDS.  Rows too wide for that (over 16384 columns, or 8192 that are not groups of four) are read
+// again for each pass by the wide kernels.
 #include "ss_block.h"
-#include "ss_device.h"
+#include "ss_rows.h"
+
+#include <type_traits>
 
 namespace ss {
 namespace {
 
-constexpr int kThreads = 256;
-
-// Sum over the workgroup, the same in every lane.
-__device__ float block_sum(float v, float* lds) {
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < kThreads / 64; ++w) s += lds[w];
-  return s;
+// Sum over the wave, the same in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += row_ror<8>(v);
+  v += row_ror<4>(v);
+  v += row_ror<2>(v);
+  v += row_ror<1>(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
 }
 
-// One workgroup per row, three passes over it.
+// Sums of N values over the TPR threads of a row, the same in every thread.  `lds` holds N rows
+// of 16 floats; `phase` alternates between two of them, so that one barrier per sum is enough.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* lds, int phase) {
+#pragma unroll
+  for (int q = 0; q < N; ++q) v[q] = wave_sum(v[q]);
+  if constexpr (TPR > 64) {
+    constexpr int kW = TPR / 64;
+    float* at = lds + (phase & 1) * N * 16;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int q = 0; q < N; ++q) at[q * 16 + (threadIdx.x >> 6)] = v[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      float s = at[q * 16];
+#pragma unroll
+      for (int w = 1; w < kW; ++w) s += at[q * 16 + w];
+      v[q] = s;
+    }
+  }
+}
+
+template <int TPR>
+constexpr int kBlock = TPR < 256 ? 256 : TPR;  // threads of a workgroup
+
+template <class IO, int V, int TPR, int K>
+__global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(NormArgs p) {
+  __shared__ float lds[2 * 16];
+  constexpr int kRows = kBlock<TPR> / TPR;
+  const int tid = threadIdx.x % TPR;
+  const int sub = kRows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  if (row >= p.rows) return;  // only where the workgroup's rows do not meet at a barrier
+  const uint32_t dim = static_cast<uint32_t>(p.dim);
+  const int64_t at = row * p.dim;
+  const auto X = rows_of<IO, V>(p.x, at, dim * sizeof(typename IO::elem));
+  const auto W = rows_of<F32, V>(p.weight, 0, p.weight ? dim * 4 : 0);
+  const auto B = rows_of<F32, V>(p.bias, 0, p.bias ? dim * 4 : 0);
+  typename Lanes<IO, V>::raw xr[K];
+  typename Lanes<F32, V>::raw rr[K], wr[K], br[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t col = (k * TPR + tid) * V;
+    xr[k] = X.load(col * sizeof(typename IO::elem));
+  }
+  if (p.residual) {
+    const auto R = rows_of<F32, V>(p.residual, at, dim * 4);
+#pragma unroll
+    for (int k = 0; k < K; ++k) rr[k] = R.load((k * TPR + tid) * V * 4);
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    wr[k] = W.load((k * TPR + tid) * V * 4);
+    br[k] = B.load((k * TPR + tid) * V * 4);
+  }
+  float s[K][V], sum[1] = {0.0f};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s[k][v] = Lanes<IO, V>::get(xr[k], v);
+      if (p.residual) s[k][v] += Lanes<F32, V>::get(rr[k], v);
+      sum[0] += s[k][v];
+    }
+  }
+  if (p.sum) {
+    const auto S = rows_of<F32, V>(p.sum, at, dim * 4);
+#pragma unroll
+    for (int k = 0; k < K; ++k) S.store(s[k], (k * TPR + tid) * V * 4);
+  }
+  const float n = static_cast<float>(p.dim);
+  row_sums<TPR>(sum, lds, 0);
+  const float mu = sum[0] / n;
+  float sq[1] = {0.0f};
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const bool in = (k * TPR + tid) * V < dim;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      s[k][v] -= mu;
+      const float c = in ? s[k][v] : 0.0f;
+      sq[0] = fmaf(c, c, sq[0]);
+    }
+  }
+  row_sums<TPR>(sq, lds, 1);
+  const float rstd = 1.0f / __builtin_sqrtf(sq[0] / n + p.eps);
+  const auto O = rows_of<IO, V>(p.out, at, dim * sizeof(typename IO::elem));
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float y[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const float w = p.weight ? Lanes<F32, V>::get(wr[k], v) : 1.0f;
+      y[v] = fmaf(s[k][v] * rstd, w, Lanes<F32, V>::get(br[k], v));
+    }
+    O.store(y, (k * TPR + tid) * V * sizeof(typename IO::elem));
+  }
+  if (tid == 0) {
+    if (p.mean) p.mean[row] = mu;
+    if (p.rstd) p.rstd[row] = rstd;
+  }
+}
+
+// Each row group of the launch walks the rows with the launch's stride and adds dweight and dbias
+// in its registers; part[strand][2][dim] takes one line per workgroup.
+template <class IO, class S, int V, int TPR, int K>
+__global__ __launch_bounds__(kBlock<TPR>) void norm_bwd_kernel(NormArgs p, float* part) {
+  constexpr int kRows = kBlock<TPR> / TPR;
+  __shared__ float lds[4 * 16];
+  __shared__ float fold[kRows > 1 ? kRows * 2 * V * K * TPR : 1];
+  const int tid = threadIdx.x % TPR;
+  const int sub = kRows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
+  const uint32_t dim = static_cast<uint32_t>(p.dim);
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  const auto W = rows_of<F32, V>(p.weight, 0, p.weight ? dim * 4 : 0);
+  float w[K][V], dw[K][V], db[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const auto wr = W.load((k * TPR + tid) * V * 4);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w[k][v] = p.weight ? Lanes<F32, V>::get(wr, v) : 1.0f;
+      dw[k][v] = db[k][v] = 0.0f;
+    }
+  }
+  typename Lanes<IO, V>::raw gr[K];
+  typename Lanes<S, V>::raw sr[K];
+  typename Lanes<F32, V>::raw ur[K];
+  float mu = 0.0f, rstd = 0.0f;
+  // A row past the last one reads as zeros, without an access (empty resources).
+  auto fetch = [&](int64_t row) {
+    const bool in = row < p.rows;
+    const int64_t at = in ? row * p.dim : 0;
+    const auto G = rows_of<IO, V>(p.dout, at, in ? dim * sizeof(typename IO::elem) : 0);
+    const auto X = rows_of<S, V>(p.x, at, in ? dim * sizeof(typename S::elem) : 0);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      gr[k] = G.load((k * TPR + tid) * V * sizeof(typename IO::elem));
+      sr[k] = X.load((k * TPR + tid) * V * sizeof(typename S::elem));
+    }
+    if (p.dsum) {
+      const auto U = rows_of<F32, V>(p.dsum, at, in ? dim * 4 : 0);
+#pragma unroll
+      for (int k = 0; k < K; ++k) ur[k] = U.load((k * TPR + tid) * V * 4);
+    }
+    mu = in ? p.mean_in[row] : 0.0f;
+    rstd = in ? p.rstd_in[row] : 0.0f;
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
+  fetch(row);
+  int phase = 0;
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRows; first < p.rows;
+       first += stride, row += stride, ++phase) {
+    float xh[K][V], g[K][V], u[K][V], sums[2] = {0.0f, 0.0f};
+    const float rs = rstd;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const bool in = (k * TPR + tid) * V < dim;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float dy = Lanes<IO, V>::get(gr[k], v);
+        xh[k][v] = in ? (Lanes<S, V>::get(sr[k], v) - mu) * rs : 0.0f;
+        g[k][v] = dy * w[k][v];
+        dw[k][v] = fmaf(dy, xh[k][v], dw[k][v]);
+        db[k][v] += dy;
+        sums[0] += g[k][v];
+        sums[1] = fmaf(g[k][v], xh[k][v], sums[1]);
+        u[k][v] = p.dsum ? Lanes<F32, V>::get(ur[k], v) : 0.0f;
+      }
+    }
+    fetch(row + stride);  // in flight over the sums and the stores
+    row_sums<TPR>(sums, lds, phase);
+    const float c1 = sums[0] * inv, c2 = sums[1] * inv;
+    const bool live = row < p.rows;
+    const int64_t at = live ? row * p.dim : 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[k][v] = fmaf(rs, g[k][v] - c1 - xh[k][v] * c2, u[k][v]);
+    }
+    if (p.dx) {
+      const auto O = rows_of<IO, V>(p.dx, at, live ? dim * sizeof(typename IO::elem) : 0);
+#pragma unroll
+      for (int k = 0; k < K; ++k) O.store(u[k], (k * TPR + tid) * V * sizeof(typename IO::elem));
+    }
+    if (p.dresidual) {
+      const auto O = rows_of<F32, V>(p.dresidual, at, live ? dim * 4 : 0);
+#pragma unroll
+      for (int k = 0; k < K; ++k) O.store(u[k], (k * TPR + tid) * V * 4);
+    }
+  }
+  if (!part) return;
+  if constexpr (kRows > 1) {  // the row groups' sums into the first one's, in order
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        fold[((sub * 2 * K + k) * V + v) * TPR + tid] = dw[k][v];
+        fold[((sub * 2 * K + K + k) * V + v) * TPR + tid] = db[k][v];
+      }
+    }
+    __syncthreads();
+    if (sub) return;
+    for (int r = 1; r < kRows; ++r) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          dw[k][v] += fold[((r * 2 * K + k) * V + v) * TPR + tid];
+          db[k][v] += fold[((r * 2 * K + K + k) * V + v) * TPR + tid];
+        }
+      }
+    }
+  }
+  const int64_t line = static_cast<int64_t>(blockIdx.x) * 2 * p.dim;
+  const auto PW = rows_of<F32, V>(part, line, dim * 4);
+  const auto PB = rows_of<F32, V>(part, line + p.dim, dim * 4);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    PW.store(dw[k], (k * TPR + tid) * V * 4);
+    PB.store(db[k], (k * TPR + tid) * V * 4);
+  }
+}
+
+// ------------------------------------------------------------------------------------- wide rows
+
+constexpr int kWide = 1024;
+
 template <class IO>
-__global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs p) {
+__global__ __launch_bounds__(kWide) void norm_fwd_wide_kernel(NormArgs p) {
   using elem = typename IO::elem;
-  __shared__ float lds[kThreads / 64];
+  __shared__ float lds[2 * 16];
   const int64_t row = blockIdx.x, at = row * p.dim;
   auto value = [&](int64_t c) {
     const float x = IO::load(static_cast<const elem*>(p.x), at + c);
     return p.residual ? x + p.residual[at + c] : x;
   };
-  float s = 0.0f;
-  for (int64_t c = threadIdx.x; c < p.dim; c += kThreads) s += value(c);
-  const float mu = block_sum(s, lds) / static_cast<float>(p.dim);
-  float v = 0.0f;
-  for (int64_t c = threadIdx.x; c < p.dim; c += kThreads) {
+  const float n = static_cast<float>(p.dim);
+  float s[1] = {0.0f}, sq[1] = {0.0f};
+  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) s[0] += value(c);
+  row_sums<kWide>(s, lds, 0);
+  const float mu = s[0] / n;
+  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
     const float t = value(c) - mu;
-    v = fmaf(t, t, v);
+    sq[0] = fmaf(t, t, sq[0]);
   }
-  const float var = block_sum(v, lds) / static_cast<float>(p.dim);
-  const float rstd = 1.0f / __builtin_sqrtf(var + p.eps);
-  for (int64_t c = threadIdx.x; c < p.dim; c += kThreads) {
+  row_sums<kWide>(sq, lds, 1);
+  const float rstd = 1.0f / __builtin_sqrtf(sq[0] / n + p.eps);
+  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
     const float t = value(c);
-    const float xh = (t - mu) * rstd;
     const float w = p.weight ? p.weight[c] : 1.0f, b = p.bias ? p.bias[c] : 0.0f;
-    static_cast<elem*>(p.out)[at + c] = IO::from_float(fmaf(xh, w, b));
+    static_cast<elem*>(p.out)[at + c] = IO::from_float(fmaf((t - mu) * rstd, w, b));
     if (p.sum) p.sum[at + c] = t;
   }
   if (threadIdx.x == 0) {
@@ -52,71 +287,193 @@ __global__ __launch_bounds__(kThreads) void norm_fwd_kernel(NormArgs p) {
 }
 
 template <class IO, class S>
-__global__ __launch_bounds__(kThreads) void norm_bwd_kernel(NormArgs p) {
+__global__ __launch_bounds__(kWide) void norm_bwd_wide_kernel(NormArgs p) {
   using elem = typename IO::elem;
-  __shared__ float lds[kThreads / 64];
+  __shared__ float lds[4 * 16];
   const int64_t row = blockIdx.x, at = row * p.dim;
   const float mu = p.mean_in[row], rstd = p.rstd_in[row];
   const auto* sp = static_cast<const typename S::elem*>(p.x);
-  float s1 = 0.0f, s2 = 0.0f;
-  for (int64_t c = threadIdx.x; c < p.dim; c += kThreads) {
-    const float xh = (S::load(sp, at + c) - mu) * rstd;
-    const float g = IO::load(static_cast<const elem*>(p.dout), at + c) *
-                    (p.weight ? p.weight[c] : 1.0f);
-    s1 += g;
-    s2 = fmaf(g, xh, s2);
+  auto hat = [&](int64_t c) { return (S::load(sp, at + c) - mu) * rstd; };
+  auto grad = [&](int64_t c) {
+    return IO::load(static_cast<const elem*>(p.dout), at + c) * (p.weight ? p.weight[c] : 1.0f);
+  };
+  float s[2] = {0.0f, 0.0f};
+  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
+    const float g = grad(c);
+    s[0] += g;
+    s[1] = fmaf(g, hat(c), s[1]);
   }
-  const float c1 = block_sum(s1, lds) / static_cast<float>(p.dim);
-  const float c2 = block_sum(s2, lds) / static_cast<float>(p.dim);
-  for (int64_t c = threadIdx.x; c < p.dim; c += kThreads) {
-    const float xh = (S::load(sp, at + c) - mu) * rstd;
-    const float g = IO::load(static_cast<const elem*>(p.dout), at + c) *
-                    (p.weight ? p.weight[c] : 1.0f);
-    float ds = rstd * (g - c1 - xh * c2);
-    if (p.dsum) ds += p.dsum[at + c];
+  row_sums<kWide>(s, lds, 0);
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  const float c1 = s[0] * inv, c2 = s[1] * inv;
+  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
+    const float ds = fmaf(rstd, grad(c) - c1 - hat(c) * c2, p.dsum ? p.dsum[at + c] : 0.0f);
     if (p.dx) static_cast<elem*>(p.dx)[at + c] = IO::from_float(ds);
     if (p.dresidual) p.dresidual[at + c] = ds;
   }
 }
 
-// One thread per column over all rows.
+// dweight and dbias of wide rows: one thread per column and strand of rows.
 template <class IO, class S>
-__global__ __launch_bounds__(64) void norm_param_kernel(NormArgs p) {
+__global__ __launch_bounds__(256) void norm_param_wide_kernel(NormArgs p, float* part) {
   using elem = typename IO::elem;
-  const int64_t c = blockIdx.x * 64ll + threadIdx.x;
+  const int64_t c = blockIdx.x * 256ll + threadIdx.x;
   if (c >= p.dim) return;
   const auto* sp = static_cast<const typename S::elem*>(p.x);
   float w = 0.0f, b = 0.0f;
-  for (int64_t row = 0; row < p.rows; ++row) {
+  for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
     const float dy = IO::load(static_cast<const elem*>(p.dout), row * p.dim + c);
     w = fmaf(dy, (S::load(sp, row * p.dim + c) - p.mean_in[row]) * p.rstd_in[row], w);
     b += dy;
   }
-  if (p.dweight) p.dweight[c] = w;
-  if (p.dbias) p.dbias[c] = b;
+  part[(2 * static_cast<int64_t>(blockIdx.y)) * p.dim + c] = w;
+  part[(2 * static_cast<int64_t>(blockIdx.y) + 1) * p.dim + c] = b;
+}
+
+// Sums the strands' lines of part[strand][2][dim]: 16 threads of lines by 16 columns, then the 16
+// in order.
+__global__ __launch_bounds__(256) void norm_reduce_kernel(const float* part, int64_t strands,
+                                                          int64_t dim, float* dweight,
+                                                          float* dbias) {
+  __shared__ float lds[16][17];
+  float* out = blockIdx.y ? dbias : dweight;
+  if (!out) return;
+  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+  const int64_t c = blockIdx.x * 16ll + x;
+  float acc = 0.0f;
+  if (c < dim) {
+    const float* src = part + blockIdx.y * dim + c;
+    for (int64_t r = y; r < strands; r += 16) acc += src[2 * r * dim];
+  }
+  lds[y][x] = acc;
+  __syncthreads();
+  if (y == 0 && c < dim) {
+    float s = lds[0][x];
+    for (int k = 1; k < 16; ++k) s += lds[k][x];
+    out[c] = s;
+  }
+}
+
+// --------------------------------------------------------------------------------------- dispatch
+
+// Threads per row: the fewest that hold it in registers, 0 for a wide row.
+int threads_per_row(int64_t dim, int v) {
+  const int64_t each = v == 4 ? 16 : 8;
+  return dim <= 64 * each ? 64 : dim <= 256 * each ? 256 : dim <= 1024 * each ? 1024 : 0;
+}
+
+// Lines of partial sums, and with them workgroups of the backward: enough to fill the card, few
+// enough that the lines stay a small part of the traffic.
+constexpr int64_t kStrands = 1024;
+int64_t strands_of(int64_t rows, int rows_per_group) {
+  const int64_t n = (rows + rows_per_group - 1) / rows_per_group;
+  return n < kStrands ? n : kStrands;
+}
+
+template <class IO, int V, int TPR, int K>
+void fwd(const NormArgs& a, hipStream_t stream) {
+  constexpr int kRows = kBlock<TPR> / TPR;
+  hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K>),
+                     dim3(static_cast<unsigned>((a.rows + kRows - 1) / kRows)),
+                     dim3(kBlock<TPR>), 0, stream, a);
+}
+
+template <class IO, class S, int V, int TPR, int K>
+void bwd(const NormArgs& a, float* part, int64_t* lines, hipStream_t stream) {
+  *lines = strands_of(a.rows, kBlock<TPR> / TPR);
+  hipLaunchKernelGGL((norm_bwd_kernel<IO, S, V, TPR, K>), dim3(static_cast<unsigned>(*lines)),
+                     dim3(kBlock<TPR>), 0, stream, a, part);
+}
+
+// Calls f with the instance's V, TPR and K: groups of four columns (V = 4) in up to four rounds,
+// single columns (V = 1) in up to eight.
+template <int V, int TPR, class F>
+void with_rounds(int64_t dim, F f) {
+  const int64_t k = (dim + TPR * V - 1) / (TPR * V);
+  using std::integral_constant;
+  auto go = [&](auto kk) { f(integral_constant<int, V>{}, integral_constant<int, TPR>{}, kk); };
+  if constexpr (V == 4) {
+    if (k <= 1) go(integral_constant<int, 1>{});
+    else if (k <= 2) go(integral_constant<int, 2>{});
+    else if (k <= 3) go(integral_constant<int, 3>{});
+    else go(integral_constant<int, 4>{});
+  } else {
+    if (k <= 2) go(integral_constant<int, 2>{});
+    else if (k <= 5) go(integral_constant<int, 5>{});
+    else go(integral_constant<int, 8>{});
+  }
+}
+template <class F>
+void with_shape(int64_t dim, bool quads, int tpr, F f) {
+  if (quads) {
+    if (tpr == 64) with_rounds<4, 64>(dim, f);
+    else if (tpr == 256) with_rounds<4, 256>(dim, f);
+    else with_rounds<4, 1024>(dim, f);
+  } else {
+    if (tpr == 64) with_rounds<1, 64>(dim, f);
+    else if (tpr == 256) with_rounds<1, 256>(dim, f);
+    else with_rounds<1, 1024>(dim, f);
+  }
+}
+
+template <class IO>
+hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
+  const uintptr_t wide = reinterpret_cast<uintptr_t>(a.residual) |
+                         reinterpret_cast<uintptr_t>(a.sum) |
+                         reinterpret_cast<uintptr_t>(a.weight) |
+                         reinterpret_cast<uintptr_t>(a.bias);
+  const uintptr_t io = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out);
+  const bool quads = a.dim % 4 == 0 && wide % 16 == 0 && io % (4 * sizeof(typename IO::elem)) == 0;
+  const int tpr = threads_per_row(a.dim, quads ? 4 : 1);
+  if (!tpr)
+    hipLaunchKernelGGL((norm_fwd_wide_kernel<IO>), dim3(static_cast<unsigned>(a.rows)),
+                       dim3(kWide), 0, stream, a);
+  else
+    with_shape(a.dim, quads, tpr, [&](auto v, auto t, auto k) { fwd<IO, v, t, k>(a, stream); });
+  return hipGetLastError();
 }
 
 template <class IO, class S>
 hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL((norm_bwd_kernel<IO, S>), dim3(static_cast<unsigned>(a.rows)),
-                     dim3(kThreads), 0, stream, a);
-  if (a.dweight || a.dbias)
-    hipLaunchKernelGGL((norm_param_kernel<IO, S>),
-                       dim3(static_cast<unsigned>((a.dim + 63) / 64)), dim3(64), 0, stream, a);
+  const uintptr_t wide = reinterpret_cast<uintptr_t>(a.dsum) |
+                         reinterpret_cast<uintptr_t>(a.dresidual) |
+                         reinterpret_cast<uintptr_t>(a.weight);
+  const uintptr_t io = reinterpret_cast<uintptr_t>(a.dout) | reinterpret_cast<uintptr_t>(a.dx);
+  const bool quads = a.dim % 4 == 0 && wide % 16 == 0 &&
+                     io % (4 * sizeof(typename IO::elem)) == 0 &&
+                     reinterpret_cast<uintptr_t>(a.x) % (4 * sizeof(typename S::elem)) == 0;
+  const int tpr = threads_per_row(a.dim, quads ? 4 : 1);
+  float* part = a.dweight || a.dbias ? static_cast<float*>(a.workspace) : nullptr;
+  int64_t lines = 0;
+  if (!tpr) {
+    hipLaunchKernelGGL((norm_bwd_wide_kernel<IO, S>), dim3(static_cast<unsigned>(a.rows)),
+                       dim3(kWide), 0, stream, a);
+    if (part) {
+      const int64_t cols = (a.dim + 255) / 256;
+      lines = a.rows < 64 ? a.rows : 64;
+      hipLaunchKernelGGL((norm_param_wide_kernel<IO, S>),
+                         dim3(static_cast<unsigned>(cols), static_cast<unsigned>(lines)),
+                         dim3(256), 0, stream, a, part);
+    }
+  } else {
+    with_shape(a.dim, quads, tpr,
+               [&](auto v, auto t, auto k) { bwd<IO, S, v, t, k>(a, part, &lines, stream); });
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !part) return e;
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.dim + 15) / 16), 2),
+                     dim3(256), 0, stream, part, lines, a.dim, a.dweight, a.dbias);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t norm_bwd_ws_bytes(int64_t, int64_t) { return 0; }
+size_t norm_bwd_ws_bytes(int64_t rows, int64_t dim) {
+  return static_cast<size_t>((rows < kStrands ? rows : kStrands) * 2 * dim) * sizeof(float);
+}
 
 hipError_t launch_norm_fwd(const NormArgs& a, bool bf16, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.rows));
-  if (bf16)
-    hipLaunchKernelGGL((norm_fwd_kernel<BF16>), grid, dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((norm_fwd_kernel<F32>), grid, dim3(kThreads), 0, stream, a);
-  return hipGetLastError();
+  return bf16 ? launch_fwd<BF16>(a, stream) : launch_fwd<F32>(a, stream);
 }
 
 hipError_t launch_norm_bwd(const NormArgs& a, bool bf16, hipStream_t stream) {
