@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from .rounding import (Bounded, exp, one_minus_square, rcp, sigmoid, sqrt, stack, where)
+from .rounding import (Bounded, U, exp, one_minus_square, rcp, sigmoid, sqrt, stack, where)
 
 
 def _silu(z):
@@ -23,7 +23,12 @@ def _silu_grad(z):
 
 
 def _bias(v, b):
-    return Bounded(v) + (0.0 if b is None else b)
+    """v + b.  It may be formed as fma(v, c, c b) with c = -log2(e): c b then rounds by itself,
+    which is U |b| in v + b."""
+    if b is None:
+        return Bounded(v)
+    s = Bounded(v) + b
+    return Bounded(s.v, s.e + U * np.abs(b))
 
 
 def gates(x, r, i, A, r_bias=None, i_bias=None):

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libssscan.so")
 SOURCES = ["ss_api.hip", "ss_scan_fwd.hip", "ss_scan_zoh.hip", "ss_scan_conv.hip",
            "ss_scan_conv_zoh.hip", "ss_state_update.hip", "ss_scan_bwd.hip", "ss_scan2.hip",
-           "ss_scan2_mfma.hip", "ss_block_api.hip", "ss_block_fill.hip", "ss_gated_fwd.hip",
+           "ss_scan2_mfma.hip", "ss_block_api.hip", "ss_block_util.hip", "ss_gated_fwd.hip",
            "ss_gated_bwd.hip", "ss_gated_step.hip", "ss_norm.hip", "ss_conv.hip"]
 ARCH = "gfx950"
 

@@ -115,4 +115,22 @@ hipError_t launch_zero(float* p, int64_t n, hipStream_t stream);
 hipError_t launch_zero_bytes(void* p, int64_t bytes, hipStream_t stream);
 hipError_t launch_copy(float* dst, const float* src, int64_t n, hipStream_t stream);
 
+// Sums over the lines of partial results, for up to five outputs of `cols` values:
+// out[c * out_stride] = sum over r < lines of src[r * stride + c], in a fixed order.
+struct ColumnSums {
+  struct Job {
+    const float* src;
+    float* out;
+    int64_t out_stride;
+  };
+  Job job[5];
+  int32_t jobs;
+  int64_t lines, stride, cols;
+  // Adds an output; a null one is not wanted.
+  void add(const float* src, float* out, int64_t out_stride) {
+    if (out) job[jobs++] = Job{src, out, out_stride};
+  }
+};
+hipError_t launch_column_sums(const ColumnSums& p, hipStream_t stream);
+
 }  // namespace ss

@@ -280,32 +280,6 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
   }
 }
 
-// Sums part[lines][K + 1][d_inner] over the lines: 16 threads of lines by 16 channels, then the 16
-// in order.
-__global__ __launch_bounds__(256) void conv_reduce_kernel(ConvArgs p, const float* part,
-                                                          int64_t lines) {
-  __shared__ float lds[16][17];
-  const int q = blockIdx.y;
-  if (q == p.k && !p.dbias) return;
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const int64_t d = blockIdx.x * 16ll + x;
-  float acc = 0.0f;
-  if (d < p.d_inner) {
-    const float* src = part + q * p.d_inner + d;
-    for (int64_t r = y; r < lines; r += 16) acc += src[r * (p.k + 1) * p.d_inner];
-  }
-  lds[y][x] = acc;
-  __syncthreads();
-  if (y == 0 && d < p.d_inner) {
-    float s = lds[0][x];
-    for (int k = 1; k < 16; ++k) s += lds[k][x];
-    if (q == p.k)
-      p.dbias[d] = s;
-    else
-      p.dweight[d * p.k + q] = s;
-  }
-}
-
 // One token: V channels of one batch row per thread.
 template <class IO, int V, int K>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs p, int64_t lanes) {
@@ -389,10 +363,13 @@ hipError_t launch_bwd(const ConvArgs& a, hipStream_t stream) {
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(conv_reduce_kernel,
-                     dim3(static_cast<unsigned>((a.d_inner + 15) / 16), a.k + 1), dim3(256), 0,
-                     stream, a, part, lines);
-  return hipGetLastError();
+  ColumnSums c{};
+  c.lines = lines;
+  c.stride = (a.k + 1) * a.d_inner;
+  c.cols = a.d_inner;
+  for (int q = 0; q < a.k; ++q) c.add(part + q * a.d_inner, a.dweight + q, a.k);
+  c.add(part + a.k * a.d_inner, a.dbias, 1);
+  return launch_column_sums(c, stream);
 }
 
 template <class IO, int V>

@@ -1,6 +1,6 @@
 // ss_gated_chain.h -- how the workgroups of the gated recurrence hand the state from tile to tile.
 //
-// A workgroup owns one tile: T steps of one batch row and 64 V channels.  The sequence is a chain
+// A workgroup owns one tile: T steps of one batch row and 64 channels, one per lane.  The sequence is a chain
 // of tiles per (batch row, channel group); a tile needs the state at its start, which depends on
 // every tile before it.  Two passes (summaries, then outputs) would read the inputs twice; here
 // each tile is read once: it reduces its steps to a Piece, publishes it, picks up the pieces and
@@ -13,10 +13,10 @@
 // 64-bit atomic at device scope carries value and validity together, so no fence is needed (a
 // device-scope release would write back the XCD's whole L2).
 //
-// A tile reads the W tiles before it at once, one per wave, and waits until each holds a piece and
-// one of them an end state, then runs from the nearest end state forward.  Every tile's end state
-// is formed as advance(piece, state before) whoever forms it, so the result does not depend on
-// timing: two runs agree bit for bit.
+// One wave of the workgroup reads the kWindow tiles before its own at once, until there is an end
+// state among them and a piece in every slot nearer than it, then runs forward from that state.
+// Every tile's end state is formed as advance(piece, state before) whoever forms it, so the result
+// does not depend on timing: two runs agree bit for bit.
 //
 // Tiles are numbered by a counter that workgroups draw from as they start, with the tiles that are
 // waited on first.  So a workgroup waits only for ones that are running or done, and every wait
@@ -31,8 +31,12 @@ namespace ss {
 using slot_t = unsigned long long;
 
 // Workspace of a chain: the counter (in the first kChainHead bytes), then the slots
-// [segment][batch row][channel group][64 V].  All of it is cleared before the launch.
+// [segment][batch row][channel group][64].  All of it is cleared before the launch.
 constexpr int64_t kChainHead = 256;
+inline int64_t chain_bytes(int64_t batch, int64_t segments, int64_t d_inner) {
+  if (segments <= 1) return 0;
+  return kChainHead + batch * segments * ((d_inner + 63) / 64 * 64) * 8;
+}
 constexpr int kMaxPolls = 1 << 20;
 
 __device__ __forceinline__ slot_t pack(Piece p) {
@@ -57,67 +61,28 @@ __device__ __forceinline__ uint32_t draw_tile(uint32_t* counter, uint32_t* lds) 
   return __builtin_amdgcn_readfirstlane(*lds);
 }
 
-// The state before tile `pos` of a chain (pos >= 1 tiles come before it), for V channels per
-// lane.  `slots` points at this lane's first channel in tile 0 of the chain and `stride` slots lie
-// between tiles.  Called by every wave of the workgroup; `look` holds W = blockDim / 64 rows.
-template <int V>
-__device__ __forceinline__ void state_before(const slot_t* slots, int64_t stride, int64_t pos,
-                                             slot_t* look, float* state) {
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = blockDim.x >> 6;
-  const int n = pos < waves ? static_cast<int>(pos) : waves;  // tiles looked at
-  const slot_t* mine = slots + (pos - 1 - wave) * stride;
-  const slot_t lost = pack(Piece{0.0f, __builtin_nanf("")});
-  int polls = 0;                       // this wave's
-  for (int round = 0;; ++round) {      // the same in every wave: all see the same `look`
-    if (wave < n) {
-      slot_t s[V];
-      for (;;) {
-        bool full = true;
+// The state before tile `pos` >= 1 of a chain, for this lane's channel.  `slots` points at the
+// channel in tile 0 of the chain and `stride` slots lie between tiles.  For one wave.
+constexpr int kWindow = 4;
+__device__ __forceinline__ float look_back(const slot_t* slots, int64_t stride, int64_t pos) {
+  const slot_t* nearest = slots + (pos - 1) * stride;
+  for (int poll = 0; poll < kMaxPolls; ++poll) {
+    // (with fewer tiles before it, tile 0 repeatedly: its slot only ever holds an end state)
+    slot_t s[kWindow];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          s[v] = peek(mine + v);
-          full &= s[v] != 0;
-        }
-        if (__all(full)) break;
-        if (++polls > kMaxPolls) {
+    for (int k = 0; k < kWindow; ++k) s[k] = peek(nearest - (k < pos ? k : pos - 1) * stride);
+    bool known = false;
+    float state = 0.0f;
 #pragma unroll
-          for (int v = 0; v < V; ++v) s[v] = lost;
-          break;
-        }
-        __builtin_amdgcn_s_sleep(1);
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) look[(wave * V + v) * 64 + lane] = s[v];
+    for (int k = kWindow - 1; k >= 0; --k) {
+      const Piece p = unpack(s[k]);
+      known = s[k] != 0 && (known || p.P == 0.0f);
+      state = advance(p, state);
     }
-    __syncthreads();
-    // from the farthest tile looked at to the nearest; known from the first end state on
-    bool known[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      known[v] = false;
-      state[v] = 0.0f;
-    }
-    for (int k = n - 1; k >= 0; --k) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const Piece p = unpack(look[(k * V + v) * 64 + lane]);
-        known[v] |= p.P == 0.0f;
-        state[v] = advance(p, state[v]);
-      }
-    }
-    bool all = true;
-#pragma unroll
-    for (int v = 0; v < V; ++v) all &= known[v];
-    if (__all(all)) return;
-    if (round >= kMaxPolls) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) state[v] = known[v] ? state[v] : __builtin_nanf("");
-      return;
-    }
-    __syncthreads();  // every wave has read `look` before it is written again
+    if (__all(known)) return state;
+    __builtin_amdgcn_s_sleep(1);
   }
+  return __builtin_nanf("");
 }
 
 }  // namespace ss

@@ -9,30 +9,27 @@ __device__ __forceinline__ float sqrt_hw(float x) { return __builtin_amdgcn_sqrt
 __device__ __forceinline__ float sigmoid_f(float v) {
   return rcp_hw(1.0f + exp2_hw(-v * kLog2e));
 }
-
-// The decay a = e^l and the input's scale s = sqrt(1 - a^2) for l = A rg <= 0.
-//
-// 1 - a^2 = -expm1(w), w = 2 l.  Near w = 0 the difference 1 - a^2 cancels, so for |w| < 1/4 it is
-// the series -w (1 + w/2 + w^2/6 + w^3/24 + w^4/120 + w^5/720), whose rest is below w^6/5040 =
-// 5e-8 relative there; elsewhere 1 - a a as one fused multiply-add, where the one-ulp error of a
-// grows by at most 2 a^2 / (1 - a^2) = 7.
-__device__ __forceinline__ float decay_scale(float l, float a) {
-  const float w = 2.0f * l;
-  float q = 1.0f / 720.0f;
-  q = fmaf(q, w, 1.0f / 120.0f);
-  q = fmaf(q, w, 1.0f / 24.0f);
-  q = fmaf(q, w, 1.0f / 6.0f);
-  q = fmaf(q, w, 0.5f);
-  q = fmaf(q, w, 1.0f);
-  const float v = w > -0.25f ? -w * q : fmaf(-a, a, 1.0f);
-  return sqrt_hw(v);
+// sigmoid(v + bias) for nb = -bias log2(e): one fused multiply-add instead of two operations.
+__device__ __forceinline__ float sigmoid_biased(float v, float nb) {
+  return rcp_hw(1.0f + exp2_hw(fmaf(v, -kLog2e, nb)));
 }
-struct Decay {
-  float a, s;
-};
-__device__ __forceinline__ Decay decay_f(float l) {
-  const float a = exp2_hw(l * kLog2e);
-  return Decay{a, decay_scale(l, a)};
+
+// For the decay a = 2^y (y = A rg log2(e) <= 0): the input's scale sqrt(1 - a^2).
+//
+// 1 - a^2 = -expm1(w), w = 2 y ln 2.  Near w = 0 the difference 1 - a^2 cancels, so for w > -1/4
+// it is the series -w (1 + w/2 + w^2/6 + w^3/24 + w^4/120 + w^5/720), whose rest is below
+// w^6/5040 = 5e-8 relative there, with the powers of 2 ln 2 in its coefficients; elsewhere
+// 1 - a a as one fused multiply-add, where the one-ulp error of a grows by at most
+// 2 a^2 / (1 - a^2) = 7.
+__device__ __forceinline__ float decay_scale(float y, float a) {
+  constexpr double k = 1.3862943611198906;  // 2 ln 2
+  float q = static_cast<float>(-k * k * k * k * k * k / 720.0);
+  q = fmaf(q, y, static_cast<float>(-k * k * k * k * k / 120.0));
+  q = fmaf(q, y, static_cast<float>(-k * k * k * k / 24.0));
+  q = fmaf(q, y, static_cast<float>(-k * k * k / 6.0));
+  q = fmaf(q, y, static_cast<float>(-k * k / 2.0));
+  q = fmaf(q, y, static_cast<float>(-k));
+  return sqrt_hw(y > static_cast<float>(-0.25 / k) ? y * q : fmaf(-a, a, 1.0f));
 }
 
 // ------------------------------------------------------------------ pieces of the recurrence

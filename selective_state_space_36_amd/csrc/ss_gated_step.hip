@@ -28,10 +28,10 @@ __global__ __launch_bounds__(256) void gated_step_kernel(GatedStepArgs p, int64_
   float h[V], y[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const float rg = sigmoid_f(L::get(r, v) + LF::get(rb, v));
-    const float ig = sigmoid_f(L::get(i, v) + LF::get(ib, v));
-    const Decay k = decay_f(LF::get(A, v) * rg);
-    h[v] = fmaf(k.a, LF::get(s, v), k.s * ig * L::get(x, v));
+    const float rg = sigmoid_biased(L::get(r, v), -LF::get(rb, v) * kLog2e);
+    const float ig = sigmoid_biased(L::get(i, v), -LF::get(ib, v) * kLog2e);
+    const float l = LF::get(A, v) * kLog2e * rg, a = exp2_hw(l);
+    h[v] = fmaf(a, LF::get(s, v), decay_scale(l, a) * ig * L::get(x, v));
     y[v] = GATE ? h[v] * silu_f(L::get(z, v)) : h[v];
   }
   *reinterpret_cast<typename LF::raw*>(p.state + e) = LF::put(h);

@@ -330,30 +330,6 @@ __global__ __launch_bounds__(256) void norm_param_wide_kernel(NormArgs p, float*
   part[(2 * static_cast<int64_t>(blockIdx.y) + 1) * p.dim + c] = b;
 }
 
-// Sums the strands' lines of part[strand][2][dim]: 16 threads of lines by 16 columns, then the 16
-// in order.
-__global__ __launch_bounds__(256) void norm_reduce_kernel(const float* part, int64_t strands,
-                                                          int64_t dim, float* dweight,
-                                                          float* dbias) {
-  __shared__ float lds[16][17];
-  float* out = blockIdx.y ? dbias : dweight;
-  if (!out) return;
-  const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-  const int64_t c = blockIdx.x * 16ll + x;
-  float acc = 0.0f;
-  if (c < dim) {
-    const float* src = part + blockIdx.y * dim + c;
-    for (int64_t r = y; r < strands; r += 16) acc += src[2 * r * dim];
-  }
-  lds[y][x] = acc;
-  __syncthreads();
-  if (y == 0 && c < dim) {
-    float s = lds[0][x];
-    for (int k = 1; k < 16; ++k) s += lds[k][x];
-    out[c] = s;
-  }
-}
-
 // --------------------------------------------------------------------------------------- dispatch
 
 // Threads per row: the fewest that hold it in registers, 0 for a wide row.
@@ -461,9 +437,13 @@ hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !part) return e;
-  hipLaunchKernelGGL(norm_reduce_kernel, dim3(static_cast<unsigned>((a.dim + 15) / 16), 2),
-                     dim3(256), 0, stream, part, lines, a.dim, a.dweight, a.dbias);
-  return hipGetLastError();
+  ColumnSums c{};
+  c.lines = lines;
+  c.stride = 2 * a.dim;
+  c.cols = a.dim;
+  c.add(part, a.dweight, 1);
+  c.add(part + a.dim, a.dbias, 1);
+  return launch_column_sums(c, stream);
 }
 
 }  // namespace
