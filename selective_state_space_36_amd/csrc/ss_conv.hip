@@ -140,31 +140,26 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
   if (some) {
     Taps<V, K> taps;
     taps.load(p, at.c);
-    // x and g at the K - 1 steps before the current one, and the starts up to them
+    // x and g at the K - 1 steps before the current one and, last, at the current one
     float xw[K][V], gw[K][V];
-    uint32_t seq[K];
     {
       const auto H = rows_before<IO, V, K>(p, at.b, at.t0);
-      uint32_t mask = 0;
-      if (PACKED) mask = starts_mask(p, at.b, at.t0 - (K - 1), K - 1);
-      uint32_t s = 0;
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {
         const auto raw = H.load(col + j * row);
-        if (PACKED) s += mask >> j & 1;
-        seq[j] = s;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           xw[j][v] = L::get(raw, v);
           gw[j][v] = 0.0f;
         }
       }
-      seq[K - 1] = s;
     }
     const bool prev = at.t0 == 0 && p.dx_prev;
     const auto DP = rows_of<IO, V>(p.dx_prev, prev ? at.b * (K - 1) * p.d_inner : 0,
                                    prev ? (K - 1) * row : 0);
     typename L::raw xn[kStride], gn[kStride];
+    uint32_t begins = 0;                      // starts at the K - 1 steps before s0, then from s0 on
+    if (PACKED) begins = starts_mask(p, at.b, at.t0 - (K - 1), K - 1);
     uint32_t starts = 0;
     // rows are addressed kStride at a time, so that 32-bit offsets reach for any d_inner
     auto fetch = [&](int s0) {
@@ -187,18 +182,19 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
         xr[j] = xn[j];
         gr[j] = gn[j];
       }
-      const uint32_t now = starts;
+      if (PACKED) begins |= starts << (K - 1);  // bit j + K - 1: a sequence starts at step s0 + j
+      const uint32_t now = begins;
       // dx trails by K - 1 steps
       static_assert(kStride >= K, "the first rows hold a whole window");
       const int skip = s0 ? 0 : K - 1, r0 = s0 ? s0 - (K - 1) : 0;
       const int rest = n - r0 < 0 ? 0 : n - r0 < kStride ? n - r0 : kStride;
       const auto DX = rows_of<IO, V>(p.dx, first + (rest ? r0 * p.d_inner : 0), rest * row);
       if (s0 + kStride < all) fetch(s0 + kStride);
-#pragma unroll
-      for (int j = 0; j < kStride; ++j) {
+      // Step s0 + j.  PLAIN: all of the kStride steps are the wave's own and no sequence starts
+      // among them or in the window, so that nothing in them branches.
+      auto step = [&](int j, auto plain) {
+        constexpr bool kPlain = decltype(plain)::value;
         const int s = s0 + j;
-        if (s >= all) break;
-        if (PACKED) seq[K - 1] += now >> j & 1;
         float g[V], pre[V], dx[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -206,9 +202,13 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
           g[v] = L::get(gr[j], v);
           pre[v] = taps.bias[v];
         }
+        // whether a start cuts tap q (the row K - 1 - q steps back) off from this step, and this
+        // step's g (q steps after it) from the step K - 1 back
+        auto tap_cut = [&](int q) { return now & (((1u << (K - 1 - q)) - 1) << (j + q + 1)); };
+        auto dx_cut = [&](int q) { return now & (((1u << q) - 1) << (j + 1)); };
 #pragma unroll
         for (int q = 0; q < K; ++q) {
-          if (PACKED && seq[q] != seq[K - 1]) continue;
+          if (!kPlain && tap_cut(q)) continue;
 #pragma unroll
           for (int v = 0; v < V; ++v) pre[v] = fmaf(taps.w[q][v], xw[q][v], pre[v]);
         }
@@ -219,16 +219,16 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
             g[v] *= sg * fmaf(pre[v], 1.0f - sg, 1.0f);
           }
         }
-        if (s >= have) {  // past the end of the sequence: no gradient, whatever silu' gave
+        if (!kPlain && s >= have) {  // past the end: no gradient, whatever silu' gave
 #pragma unroll
           for (int v = 0; v < V; ++v) g[v] = 0.0f;
         }
-        if (s < n) {
+        if (kPlain || s < n) {
 #pragma unroll
           for (int v = 0; v < V; ++v) db[v] += g[v];
 #pragma unroll
           for (int q = 0; q < K; ++q) {
-            if (PACKED && seq[q] != seq[K - 1]) continue;
+            if (!kPlain && tap_cut(q)) continue;
 #pragma unroll
             for (int v = 0; v < V; ++v) dw[q][v] = fmaf(g[v], xw[q][v], dw[q][v]);
           }
@@ -241,24 +241,33 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
         }
 #pragma unroll
         for (int q = 0; q < K; ++q) {
-          if (PACKED && seq[q] != seq[0]) continue;
+          if (!kPlain && dx_cut(q)) continue;
 #pragma unroll
           for (int v = 0; v < V; ++v) dx[v] = fmaf(taps.w[K - 1 - q][v], gw[q][v], dx[v]);
         }
-        if (s >= K - 1)
+        if (j >= K - 1 || s0)
           DX.store(dx, col + (j - skip) * row);
         else if (prev)
           DP.store(dx, col + s * row);
 #pragma unroll
         for (int q = 0; q + 1 < K; ++q) {
-          seq[q] = seq[q + 1];
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             xw[q][v] = xw[q + 1][v];
             gw[q][v] = gw[q + 1][v];
           }
         }
+      };
+      if (s0 + kStride <= n && now == 0) {
+#pragma unroll
+        for (int j = 0; j < kStride; ++j) step(j, std::true_type{});
+      } else {
+#pragma unroll
+        for (int j = 0; j < kStride; ++j) {
+          if (s0 + j < all) step(j, std::false_type{});
+        }
       }
+      if (PACKED) begins = now >> kStride;
     }
   }
 #pragma unroll
