@@ -321,12 +321,14 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs p, int64_t lane
                             c) = x[j + 1];
 }
 
-// Steps per wave of the backward.
-constexpr int kBwdSteps = 64;
-
-int64_t lines_of(int64_t batch, int64_t seqlen) {
-  const int64_t runs = (seqlen + kBwdSteps - 1) / kBwdSteps;
-  return (batch * runs + kWaves - 1) / kWaves;
+// Steps per wave of the backward: long runs walk the k - 1 steps after them the fewest times, as
+// long as there are enough of them for one per SIMD (1024).
+int64_t bwd_steps(int64_t batch, int64_t seqlen, int64_t d_inner) {
+  const int64_t runs = (seqlen + 63) / 64, groups = (d_inner + 127) / 128;
+  return batch * runs * groups >= 1024 ? 64 : 16;
+}
+int64_t lines_of(int64_t batch, int64_t seqlen, int64_t steps) {
+  return (batch * ((seqlen + steps - 1) / steps) + kWaves - 1) / kWaves;
 }
 
 template <class F>
@@ -357,18 +359,19 @@ hipError_t launch_fwd(const ConvArgs& a, hipStream_t stream) {
 template <class IO, int V>
 hipError_t launch_bwd(const ConvArgs& a, hipStream_t stream) {
   const int64_t groups = (a.d_inner + 64 * V - 1) / (64 * V);
-  const int64_t runs = (a.seqlen + kBwdSteps - 1) / kBwdSteps;
-  const int64_t lines = lines_of(a.batch, a.seqlen);
+  const int32_t steps = static_cast<int32_t>(bwd_steps(a.batch, a.seqlen, a.d_inner));
+  const int64_t runs = (a.seqlen + steps - 1) / steps;
+  const int64_t lines = lines_of(a.batch, a.seqlen, steps);
   const dim3 grid(static_cast<unsigned>(lines * groups)), block(64 * kWaves);
   const uint32_t g = static_cast<uint32_t>(groups);
   float* part = static_cast<float*>(a.workspace);
   with_width(a.k, [&](auto k) {
     if (a.starts)
       hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, true>), grid, block, 0, stream, a, g, runs,
-                         kBwdSteps, part);
+                         steps, part);
     else
       hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, false>), grid, block, 0, stream, a, g, runs,
-                         kBwdSteps, part);
+                         steps, part);
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -403,7 +406,8 @@ bool lanes_of(const ConvArgs& a, int v) {
 }  // namespace
 
 size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int32_t k, bool) {
-  return static_cast<size_t>(lines_of(batch, seqlen) * (k + 1) * d_inner) * sizeof(float);
+  const int64_t lines = lines_of(batch, seqlen, bwd_steps(batch, seqlen, d_inner));
+  return static_cast<size_t>(lines * (k + 1) * d_inner) * sizeof(float);
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf16, hipStream_t stream) {

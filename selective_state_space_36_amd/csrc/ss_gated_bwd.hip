@@ -20,9 +20,9 @@ constexpr int kTile = kSteps * kWaves;
 static_assert(kTile == SS_GATED_CHUNK, "a tile starts at a saved state");
 
 template <class IO, bool GATE>
-__global__ __launch_bounds__(64 * kWaves) void gated_bwd_kernel(GatedArgs p, const float* states,
-                                                                float* part, int32_t groups,
-                                                                int32_t nseg) {
+__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t groups,
+                      int32_t nseg) {
   using elem = typename IO::elem;
   using R = Rows<IO, 1>;
   using F = Rows<F32, 1>;
@@ -30,6 +30,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_bwd_kernel(GatedArgs p, con
   __shared__ float back[kWaves][64];
   __shared__ float after[64];
   __shared__ float sums[3][kWaves][64];
+  __shared__ slot_t far[kFar * 64];
   __shared__ uint32_t drawn;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_bwd_kernel(GatedArgs p, con
           whole = then(whole, Piece{pieces[k][lane].P, back[k][lane]});
         if (pos) publish(slots + pos * stride, whole);
       }
-      if (pos) carry = look_back(slots, stride, pos);
+      if (pos) carry = look_back(slots, stride, pos, far);
       if (seg) publish(slots + pos * stride, Piece{0.0f, advance(whole, carry)});
       after[lane] = carry;
     }

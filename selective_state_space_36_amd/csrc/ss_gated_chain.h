@@ -13,8 +13,14 @@
 // 64-bit atomic at device scope carries value and validity together, so no fence is needed (a
 // device-scope release would write back the XCD's whole L2).
 //
-// One wave of the workgroup reads the kWindow tiles before its own at once, until there is an end
+// One wave of the workgroup reads the kNear tiles before its own at once, until there is an end
 // state among them and a piece in every slot nearer than it, then runs forward from that state.
+// Where all of them hold pieces but none an end state twice over (few chains, and so many tiles of
+// each at work at the same time), it reaches up to kFar tiles back, kMore at a time, through LDS.
+// Measured: 4 near tiles against 8 or 12 read every time, 67 against 68 and 69 us at 8 x 2048 x
+// 1536 and 702 against 743 and 760 us at 1 x 262144 x 1536; the far ones with and without, 91 and
+// 176 us at 1 x 131072 x 64 (one chain of 1024 tiles), 168 and 220 us at 1 x 131072 x 512, and
+// asked for at once, 769 us at 1 x 262144 x 1536.
 // Every tile's end state is formed as advance(piece, state before) whoever forms it, so the result
 // does not depend on timing: two runs agree bit for bit.
 //
@@ -62,24 +68,53 @@ __device__ __forceinline__ uint32_t draw_tile(uint32_t* counter, uint32_t* lds) 
 }
 
 // The state before tile `pos` >= 1 of a chain, for this lane's channel.  `slots` points at the
-// channel in tile 0 of the chain and `stride` slots lie between tiles.  For one wave.
-constexpr int kWindow = 4;
-__device__ __forceinline__ float look_back(const slot_t* slots, int64_t stride, int64_t pos) {
+// channel in tile 0 of the chain and `stride` slots lie between tiles.  For one wave; `far` is LDS
+// of its own, kFar rows of 64.
+constexpr int kNear = 4, kMore = 8, kFar = kNear + 4 * kMore;
+__device__ __forceinline__ float look_back(const slot_t* slots, int64_t stride, int64_t pos,
+                                           slot_t* far) {
+  const int lane = threadIdx.x & 63;
   const slot_t* nearest = slots + (pos - 1) * stride;
+  // slot of the tile k + 1 tiles back (past tile 0, tile 0: its slot only ever holds an end state)
+  auto slot = [&](int64_t k) { return peek(nearest - (k < pos ? k : pos - 1) * stride); };
   for (int poll = 0; poll < kMaxPolls; ++poll) {
-    // (with fewer tiles before it, tile 0 repeatedly: its slot only ever holds an end state)
-    slot_t s[kWindow];
+    slot_t s[kNear];
 #pragma unroll
-    for (int k = 0; k < kWindow; ++k) s[k] = peek(nearest - (k < pos ? k : pos - 1) * stride);
-    bool known = false;
+    for (int k = 0; k < kNear; ++k) s[k] = slot(k);
+    bool known = false, full = true;
     float state = 0.0f;
 #pragma unroll
-    for (int k = kWindow - 1; k >= 0; --k) {
+    for (int k = kNear - 1; k >= 0; --k) {
       const Piece p = unpack(s[k]);
       known = s[k] != 0 && (known || p.P == 0.0f);
+      full &= s[k] != 0;
       state = advance(p, state);
     }
     if (__all(known)) return state;
+    if (poll >= 2 && __all(full)) {
+#pragma unroll
+      for (int k = 0; k < kNear; ++k) far[k * 64 + lane] = s[k];
+      int depth = kNear;
+      while (depth < kFar && depth < pos) {
+        slot_t f[kMore];
+#pragma unroll
+        for (int k = 0; k < kMore; ++k) f[k] = slot(depth + k);
+        bool gap = false;  // an empty slot before any end state
+#pragma unroll
+        for (int k = 0; k < kMore; ++k) {
+          far[(depth + k) * 64 + lane] = f[k];
+          gap |= f[k] == 0 && !known;
+          known |= !gap && unpack(f[k]).P == 0.0f;
+        }
+        depth += kMore;
+        if (__any(gap)) break;
+        if (__all(known)) {
+          float h = 0.0f;
+          for (int k = depth - 1; k >= 0; --k) h = advance(unpack(far[k * 64 + lane]), h);
+          return h;
+        }
+      }
+    }
     __builtin_amdgcn_s_sleep(1);
   }
   return __builtin_nanf("");

@@ -340,7 +340,7 @@ int threads_per_row(int64_t dim, int v) {
 
 // Lines of partial sums, and with them workgroups of the backward: enough to fill the card, few
 // enough that the lines stay a small part of the traffic.
-constexpr int64_t kStrands = 1024;
+constexpr int64_t kStrands = 512;
 int64_t strands_of(int64_t rows, int rows_per_group) {
   const int64_t n = (rows + rows_per_group - 1) / rows_per_group;
   return n < kStrands ? n : kStrands;

@@ -550,18 +550,18 @@ def _gated_fwd(x, r, i, A, r_bias, i_bias, z, starts, h0, out, h_last, states, w
     batch, L, d = shape = _shape("x", x, 3)
     dev = x.device
     f32 = torch.float32
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if want_last and h_last is None:
-        h_last = torch.empty((batch, d), dtype=f32, device=dev)
     nct = (L + SS_GATED_CHUNK - 1) // SS_GATED_CHUNK
-    if want_states and states is None:
-        states = torch.empty((batch, nct, d), dtype=f32, device=dev)
     _expect(dev, x.dtype, shape, ("x", x), ("r", r), ("i", i), ("z", z), ("out", out))
     _expect(dev, f32, (d,), ("A", A), ("r_bias", r_bias), ("i_bias", i_bias))
     _expect(dev, f32, (batch, d), ("h0", h0), ("h_last", h_last))
     _expect(dev, f32, (batch, nct, d), ("states", states))
     _expect_starts(starts, dev, (batch, L))
+    if out is None:
+        out = torch.empty_like(x)
+    if want_last and h_last is None:
+        h_last = A.new_empty((batch, d)) if h0 is None else torch.empty_like(h0)
+    if want_states and states is None:
+        states = A.new_empty((batch, nct, d))
     l = lib()
     nbytes = l.ss_gated_scan_fwd_workspace_bytes(batch, L, d, code)
     ws, ws_len, keep = _scratch(workspace, nbytes, dev)
@@ -634,12 +634,11 @@ def gated_scan_bwd(x, r, i, A, dout, r_bias=None, i_bias=None, z=None, starts=No
     _expect(dev, f32, (batch, d), ("h0", h0), ("dh_last", dh_last))
     _expect(dev, f32, (batch, nct, d), ("states", states))
     _expect_starts(starts, dev, (batch, L))
-    e = lambda s, t: torch.empty(s, dtype=t, device=dev)  # noqa: E731
-    g = dict(dx=e(shape, x.dtype), dr=e(shape, x.dtype), di=e(shape, x.dtype),
-             dz=e(shape, x.dtype) if z is not None else None, dA=e((d,), f32),
-             dr_bias=e((d,), f32) if want_dbias else None,
-             di_bias=e((d,), f32) if want_dbias else None,
-             dh0=e((batch, d), f32) if want_dh0 else None)
+    like = torch.empty_like
+    g = dict(dx=like(x), dr=like(x), di=like(x), dz=like(x) if z is not None else None,
+             dA=like(A), dr_bias=like(A) if want_dbias else None,
+             di_bias=like(A) if want_dbias else None,
+             dh0=(A.new_empty((batch, d)) if h0 is None else like(h0)) if want_dh0 else None)
     l = lib()
     nbytes = l.ss_gated_scan_bwd_workspace_bytes(batch, L, d, code, states is not None)
     ws, ws_len, keep = _scratch(workspace, nbytes, dev)
@@ -662,11 +661,11 @@ def gated_state_update(state, x, r, i, A, r_bias=None, i_bias=None, z=None, out=
     code = _io_code(x)
     batch, d = shape = _shape("x", x, 2)
     dev = x.device
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     _expect(dev, x.dtype, shape, ("x", x), ("r", r), ("i", i), ("z", z), ("out", out))
     _expect(dev, torch.float32, (d,), ("A", A), ("r_bias", r_bias), ("i_bias", i_bias))
     _expect(dev, torch.float32, shape, ("state", state))
+    if out is None:
+        out = torch.empty_like(x)
     _check(lib().ss_gated_state_update(
         state.data_ptr(), x.data_ptr(), r.data_ptr(), i.data_ptr(), A.data_ptr(), _ptr(r_bias),
         _ptr(i_bias), _ptr(z), out.data_ptr(), batch, d, code, _raw_stream(x.device)))
@@ -694,17 +693,18 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, return_su
     rows = x.numel() // dim if dim else 0
     if return_sum is None:
         return_sum = residual is not None
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    if return_sum and sum_out is None:
-        sum_out = torch.empty(shape, dtype=f32, device=dev)
-    mean = rstd = None
-    if return_stats:
-        mean = torch.empty(shape[:-1], dtype=f32, device=dev)
-        rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
     _expect(dev, x.dtype, shape, ("x", x), ("out", out))
     _expect(dev, f32, shape, ("residual", residual), ("sum_out", sum_out))
     _expect(dev, f32, (dim,), ("weight", weight), ("bias", bias))
+    if out is None:
+        out = torch.empty_like(x)
+    if return_sum and sum_out is None:
+        sum_out = (torch.empty_like(residual) if residual is not None
+                   else torch.empty_like(x, dtype=f32))
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+        rstd = torch.empty_like(mean)
     _check(lib().ss_layer_norm_fwd(
         x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias), eps, out.data_ptr(),
         _ptr(sum_out), _ptr(mean), _ptr(rstd), rows, dim, code, _raw_stream(x.device)))
@@ -735,11 +735,10 @@ def layer_norm_bwd(dout, s, weight, mean, rstd, dsum=None, want_dx=True, want_dr
     _expect(dev, f32, shape, ("dsum", dsum))
     _expect(dev, f32, (dim,), ("weight", weight))
     _expect(dev, f32, shape[:-1], ("mean", mean), ("rstd", rstd))
-    e = lambda shp, t: torch.empty(shp, dtype=t, device=dev)  # noqa: E731
-    g = dict(dx=e(shape, dout.dtype) if want_dx else None,
-             dresidual=e(shape, f32) if want_dresidual else None,
-             dweight=e((dim,), f32) if want_dparams else None,
-             dbias=e((dim,), f32) if want_dparams else None)
+    g = dict(dx=torch.empty_like(dout) if want_dx else None,
+             dresidual=torch.empty_like(dout, dtype=f32) if want_dresidual else None,
+             dweight=mean.new_empty((dim,)) if want_dparams else None,
+             dbias=mean.new_empty((dim,)) if want_dparams else None)
     l = lib()
     nbytes = l.ss_layer_norm_bwd_workspace_bytes(rows, dim) if want_dparams else 0
     ws, ws_len, keep = _scratch(workspace, nbytes, dev)
@@ -773,9 +772,9 @@ def causal_conv_fwd(x, weight, bias=None, x_prev=None, starts=None, silu=True, o
                       dict(bias=bias, x_prev=x_prev, starts=starts, silu=silu, out=out))
     code = _io_code(x)
     shape, k = _conv_sizes(x, weight, x_prev, starts, bias, 3)
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     _expect(x.device, x.dtype, shape, ("x", x), ("out", out))
+    if out is None:
+        out = torch.empty_like(x)
     _check(lib().ss_causal_conv_fwd(
         x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(x_prev), _ptr(starts),
         1 if silu else 0, out.data_ptr(), *shape, k, code, _raw_stream(x.device)))
@@ -793,12 +792,12 @@ def causal_conv_bwd(x, weight, dout, bias=None, x_prev=None, starts=None, silu=T
                            want_dbias=want_dbias, workspace=workspace))
     code = _io_code(x)
     shape, k = _conv_sizes(x, weight, x_prev, starts, bias, 3)
-    dev, f32 = x.device, torch.float32
+    dev = x.device
     _expect(dev, x.dtype, shape, ("x", x), ("dout", dout))
-    e = lambda s, t: torch.empty(s, dtype=t, device=dev)  # noqa: E731
-    g = dict(dx=e(shape, x.dtype), dweight=e(weight.shape, f32),
-             dbias=e(shape[2:], f32) if want_dbias else None,
-             dx_prev=e(x_prev.shape, x.dtype) if x_prev is not None else None)
+    like = torch.empty_like
+    g = dict(dx=like(x), dweight=like(weight),
+             dbias=weight.new_empty(shape[2:]) if want_dbias else None,
+             dx_prev=like(x_prev) if x_prev is not None else None)
     l = lib()
     nbytes = l.ss_causal_conv_bwd_workspace_bytes(*shape, k, code)
     ws, ws_len, keep = _scratch(workspace, nbytes, dev)
@@ -817,9 +816,9 @@ def causal_conv_update(conv_state, x, weight, bias=None, silu=True, out=None, st
                       dict(bias=bias, silu=silu, out=out))
     code = _io_code(x)
     shape, k = _conv_sizes(x, weight, None, None, bias, 2)
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     _expect(x.device, x.dtype, shape, ("x", x), ("out", out))
+    if out is None:
+        out = torch.empty_like(x)
     _expect(x.device, x.dtype, (shape[0], max(k - 1, 0), shape[1]), ("conv_state", conv_state))
     _check(lib().ss_causal_conv_update(
         conv_state.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), 1 if silu else 0,
