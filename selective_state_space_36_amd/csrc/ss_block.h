@@ -39,6 +39,9 @@ struct GatedArgs {
   int64_t n_chunks;        // ceil(seqlen / SS_GATED_CHUNK)
 };
 
+// Steps of a wave, and of a workgroup's tile, of the forward; steps of a wave of the backward,
+// whose tile is SS_GATED_CHUNK.
+constexpr int kGatedFwdSteps = 16, kGatedFwdTile = 128, kGatedBwdSteps = 8;
 size_t gated_fwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool bf16);
 size_t gated_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool bf16,
                           bool states_given);

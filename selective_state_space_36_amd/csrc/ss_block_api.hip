@@ -85,11 +85,18 @@ bool sizes_ok(int64_t batch, int64_t seqlen, int64_t d_inner) {
          mul_ok(batch, d_inner, &n) && mul_ok(n, seqlen + 8, &n) && n / 64 < kMaxGrid;
 }
 
-// The sequence operators launch at most one workgroup per 16 steps and 64 channels of a batch row.
-ss_status check_tiles(int64_t batch, int64_t seqlen, int64_t d_inner) {
-  if (batch * ((d_inner + 63) / 64) * ((seqlen + 15) / 16) > kMaxGrid)
-    return fail(SS_ERR_INVALID_ARG, "too many tiles (batch * seqlen * d_inner)");
+// A launch counts its threads in 32 bits.
+ss_status check_grid(int64_t blocks, int64_t threads) {
+  if (blocks > 0xffffffffll / threads)
+    return fail(SS_ERR_INVALID_ARG, "too many elements for one launch");
   return SS_OK;
+}
+// The recurrence: one workgroup per tile and 64 channels, one wave per `per_wave` steps in it.
+ss_status check_tiles(int64_t batch, int64_t seqlen, int64_t d_inner, int64_t tile,
+                      int64_t per_wave) {
+  const int64_t waves = seqlen > tile ? tile / per_wave : (seqlen + per_wave - 1) / per_wave;
+  return check_grid(batch * ((d_inner + 63) / 64) * ((seqlen + tile - 1) / tile),
+                    64 * (waves > 0 ? waves : 1));
 }
 
 int64_t chunks_of(int64_t seqlen) { return (seqlen + SS_GATED_CHUNK - 1) / SS_GATED_CHUNK; }
@@ -128,7 +135,8 @@ ss_status ss_gated_scan_fwd(const void* x, const void* r, const void* i, const f
     if ((s = check_arrays(in, 1, out1, 1)) != SS_OK) return s;
     return launched(h0 ? ss::launch_copy(h_last, h0, rows, st) : ss::launch_zero(h_last, rows, st));
   }
-  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
+  if ((s = check_tiles(batch, seqlen, d_inner, ss::kGatedFwdTile, ss::kGatedFwdSteps)) != SS_OK)
+    return s;
   const size_t need = ss::gated_fwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16);
   const Arr in[] = {{"x", x, n, es, true}, {"r", r, n, es, true}, {"i", i, n, es, true},
                     {"A", A, d_inner, 4, true}, {"r_bias", r_bias, d_inner, 4, false},
@@ -169,7 +177,8 @@ ss_status ss_gated_scan_bwd(const void* x, const void* r, const void* i, const f
   if (s != SS_OK) return s;
   if ((s = check_sizes(batch, seqlen, d_inner, &n)) != SS_OK) return s;
   if (d_inner == 0) return ok();
-  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
+  if ((s = check_tiles(batch, seqlen, d_inner, SS_GATED_CHUNK, ss::kGatedBwdSteps)) != SS_OK)
+    return s;
   const int64_t rows = batch * d_inner;
   const bool some = n > 0;
   const size_t need = some ? ss::gated_bwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16,
@@ -219,6 +228,7 @@ ss_status ss_gated_state_update(float* state, const void* x, const void* r, cons
   if (s != SS_OK) return s;
   if ((s = check_sizes(batch, 1, d_inner, &n)) != SS_OK) return s;
   if (n == 0) return ok();
+  if ((s = check_grid((n + 255) / 256, 256)) != SS_OK) return s;
   const Arr in[] = {{"x", x, n, es, true}, {"r", r, n, es, true}, {"i", i, n, es, true},
                     {"A", A, d_inner, 4, true}, {"r_bias", r_bias, d_inner, 4, false},
                     {"i_bias", i_bias, d_inner, 4, false}, {"z", z, n, es, false}};
@@ -319,6 +329,11 @@ ss_status ss_layer_norm_bwd(const void* dout, const void* x, ss_dtype s_dtype,
 
 // ----------------------------------------------------------------------------------- convolution
 
+// One wave per at least 16 steps and 64 channels, four to a workgroup.
+static ss_status check_conv_grid(int64_t batch, int64_t seqlen, int64_t d_inner) {
+  return check_grid((batch * ((seqlen + 15) / 16) + 3) / 4 * ((d_inner + 63) / 64), 256);
+}
+
 static ss_status check_width(int32_t k) {
   return k >= 1 && k <= 4 ? SS_OK : fail(SS_ERR_UNSUPPORTED, "k=%d outside 1..4", k);
 }
@@ -333,7 +348,7 @@ ss_status ss_causal_conv_fwd(const void* x, const float* weight, const float* bi
   if ((s = check_width(k)) != SS_OK) return s;
   if ((s = check_sizes(batch, seqlen, d_inner, &n)) != SS_OK) return s;
   if (n == 0) return ok();
-  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
+  if ((s = check_conv_grid(batch, seqlen, d_inner)) != SS_OK) return s;
   const Arr in[] = {{"x", x, n, es, true}, {"weight", weight, d_inner * k, 4, true},
                     {"bias", bias, d_inner, 4, false},
                     {"x_prev", x_prev, batch * (k - 1) * d_inner, es, false},
@@ -365,7 +380,7 @@ ss_status ss_causal_conv_bwd(const void* x, const float* weight, const float* bi
   if ((s = check_width(k)) != SS_OK) return s;
   if ((s = check_sizes(batch, seqlen, d_inner, &n)) != SS_OK) return s;
   if (d_inner == 0) return ok();
-  if ((s = check_tiles(batch, seqlen, d_inner)) != SS_OK) return s;
+  if ((s = check_conv_grid(batch, seqlen, d_inner)) != SS_OK) return s;
   const bool some = n > 0;
   const int64_t prev = batch * (k - 1) * d_inner;
   if (dx_prev && !x_prev && prev > 0)
@@ -408,6 +423,7 @@ ss_status ss_causal_conv_update(void* conv_state, const void* x, const float* we
   if ((s = check_width(k)) != SS_OK) return s;
   if ((s = check_sizes(batch, 1, d_inner, &n)) != SS_OK) return s;
   if (n == 0) return ok();
+  if ((s = check_grid((n + 255) / 256, 256)) != SS_OK) return s;
   const Arr in[] = {{"x", x, n, es, true}, {"weight", weight, d_inner * k, 4, true},
                     {"bias", bias, d_inner, 4, false}};
   const Arr outs[] = {{"conv_state", k > 1 ? conv_state : nullptr, batch * (k - 1) * d_inner, es,

@@ -14,10 +14,9 @@
 namespace ss {
 namespace {
 
-constexpr int kSteps = 8;
-constexpr int kWaves = 8;
-constexpr int kTile = kSteps * kWaves;
-static_assert(kTile == SS_GATED_CHUNK, "a tile starts at a saved state");
+constexpr int kSteps = kGatedBwdSteps;
+constexpr int kTile = SS_GATED_CHUNK;  // so that a tile starts at a saved state
+constexpr int kWaves = kTile / kSteps;
 
 template <class IO, bool GATE>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))

@@ -11,9 +11,9 @@
 namespace ss {
 namespace {
 
-constexpr int kSteps = 16;
-constexpr int kWaves = 8;
-constexpr int kTile = kSteps * kWaves;
+constexpr int kSteps = kGatedFwdSteps;
+constexpr int kTile = kGatedFwdTile;
+constexpr int kWaves = kTile / kSteps;
 
 // Four waves per SIMD (two workgroups per CU) whatever the registers: told so, the compiler takes
 // up to 128 and keeps more loads in flight (708 against 730 us at 1 x 262144 x 1536).

@@ -56,75 +56,76 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(NormArgs p) {
   constexpr int kRows = kBlock<TPR> / TPR;
   const int tid = threadIdx.x % TPR;
   const int sub = kRows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub;
-  if (row >= p.rows) return;  // only where the workgroup's rows do not meet at a barrier
   const uint32_t dim = static_cast<uint32_t>(p.dim);
-  const int64_t at = row * p.dim;
-  const auto X = rows_of<IO, V>(p.x, at, dim * sizeof(typename IO::elem));
-  const auto W = rows_of<F32, V>(p.weight, 0, p.weight ? dim * 4 : 0);
-  const auto B = rows_of<F32, V>(p.bias, 0, p.bias ? dim * 4 : 0);
-  typename Lanes<IO, V>::raw xr[K];
-  typename Lanes<F32, V>::raw rr[K], wr[K], br[K];
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < p.rows; row += stride) {
+    const int64_t at = row * p.dim;
+    const auto X = rows_of<IO, V>(p.x, at, dim * sizeof(typename IO::elem));
+    const auto W = rows_of<F32, V>(p.weight, 0, p.weight ? dim * 4 : 0);
+    const auto B = rows_of<F32, V>(p.bias, 0, p.bias ? dim * 4 : 0);
+    typename Lanes<IO, V>::raw xr[K];
+    typename Lanes<F32, V>::raw rr[K], wr[K], br[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const uint32_t col = (k * TPR + tid) * V;
-    xr[k] = X.load(col * sizeof(typename IO::elem));
-  }
-  if (p.residual) {
-    const auto R = rows_of<F32, V>(p.residual, at, dim * 4);
-#pragma unroll
-    for (int k = 0; k < K; ++k) rr[k] = R.load((k * TPR + tid) * V * 4);
-  }
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    wr[k] = W.load((k * TPR + tid) * V * 4);
-    br[k] = B.load((k * TPR + tid) * V * 4);
-  }
-  float s[K][V], sum[1] = {0.0f};
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[k][v] = Lanes<IO, V>::get(xr[k], v);
-      if (p.residual) s[k][v] += Lanes<F32, V>::get(rr[k], v);
-      sum[0] += s[k][v];
+    for (int k = 0; k < K; ++k) {
+      const uint32_t col = (k * TPR + tid) * V;
+      xr[k] = X.load(col * sizeof(typename IO::elem));
     }
-  }
-  if (p.sum) {
-    const auto S = rows_of<F32, V>(p.sum, at, dim * 4);
+    if (p.residual) {
+      const auto R = rows_of<F32, V>(p.residual, at, dim * 4);
 #pragma unroll
-    for (int k = 0; k < K; ++k) S.store(s[k], (k * TPR + tid) * V * 4);
-  }
-  const float n = static_cast<float>(p.dim);
-  row_sums<TPR>(sum, lds, 0);
-  const float mu = sum[0] / n;
-  float sq[1] = {0.0f};
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const bool in = (k * TPR + tid) * V < dim;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[k][v] -= mu;
-      const float c = in ? s[k][v] : 0.0f;
-      sq[0] = fmaf(c, c, sq[0]);
+      for (int k = 0; k < K; ++k) rr[k] = R.load((k * TPR + tid) * V * 4);
     }
-  }
-  row_sums<TPR>(sq, lds, 1);
-  const float rstd = 1.0f / __builtin_sqrtf(sq[0] / n + p.eps);
-  const auto O = rows_of<IO, V>(p.out, at, dim * sizeof(typename IO::elem));
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float y[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const float w = p.weight ? Lanes<F32, V>::get(wr[k], v) : 1.0f;
-      y[v] = fmaf(s[k][v] * rstd, w, Lanes<F32, V>::get(br[k], v));
+    for (int k = 0; k < K; ++k) {
+      wr[k] = W.load((k * TPR + tid) * V * 4);
+      br[k] = B.load((k * TPR + tid) * V * 4);
     }
-    O.store(y, (k * TPR + tid) * V * sizeof(typename IO::elem));
-  }
-  if (tid == 0) {
-    if (p.mean) p.mean[row] = mu;
-    if (p.rstd) p.rstd[row] = rstd;
+    float s[K][V], sum[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[k][v] = Lanes<IO, V>::get(xr[k], v);
+        if (p.residual) s[k][v] += Lanes<F32, V>::get(rr[k], v);
+        sum[0] += s[k][v];
+      }
+    }
+    if (p.sum) {
+      const auto S = rows_of<F32, V>(p.sum, at, dim * 4);
+#pragma unroll
+      for (int k = 0; k < K; ++k) S.store(s[k], (k * TPR + tid) * V * 4);
+    }
+    const float n = static_cast<float>(p.dim);
+    row_sums<TPR>(sum, lds, 0);
+    const float mu = sum[0] / n;
+    float sq[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const bool in = (k * TPR + tid) * V < dim;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s[k][v] -= mu;
+        const float c = in ? s[k][v] : 0.0f;
+        sq[0] = fmaf(c, c, sq[0]);
+      }
+    }
+    row_sums<TPR>(sq, lds, 1);
+    const float rstd = 1.0f / __builtin_sqrtf(sq[0] / n + p.eps);
+    const auto O = rows_of<IO, V>(p.out, at, dim * sizeof(typename IO::elem));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float y[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float w = p.weight ? Lanes<F32, V>::get(wr[k], v) : 1.0f;
+        y[v] = fmaf(s[k][v] * rstd, w, Lanes<F32, V>::get(br[k], v));
+      }
+      O.store(y, (k * TPR + tid) * V * sizeof(typename IO::elem));
+    }
+    if (tid == 0) {
+      if (p.mean) p.mean[row] = mu;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
   }
 }
 
@@ -258,31 +259,33 @@ template <class IO>
 __global__ __launch_bounds__(kWide) void norm_fwd_wide_kernel(NormArgs p) {
   using elem = typename IO::elem;
   __shared__ float lds[2 * 16];
-  const int64_t row = blockIdx.x, at = row * p.dim;
-  auto value = [&](int64_t c) {
-    const float x = IO::load(static_cast<const elem*>(p.x), at + c);
-    return p.residual ? x + p.residual[at + c] : x;
-  };
-  const float n = static_cast<float>(p.dim);
-  float s[1] = {0.0f}, sq[1] = {0.0f};
-  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) s[0] += value(c);
-  row_sums<kWide>(s, lds, 0);
-  const float mu = s[0] / n;
-  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
-    const float t = value(c) - mu;
-    sq[0] = fmaf(t, t, sq[0]);
-  }
-  row_sums<kWide>(sq, lds, 1);
-  const float rstd = 1.0f / __builtin_sqrtf(sq[0] / n + p.eps);
-  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
-    const float t = value(c);
-    const float w = p.weight ? p.weight[c] : 1.0f, b = p.bias ? p.bias[c] : 0.0f;
-    static_cast<elem*>(p.out)[at + c] = IO::from_float(fmaf((t - mu) * rstd, w, b));
-    if (p.sum) p.sum[at + c] = t;
-  }
-  if (threadIdx.x == 0) {
-    if (p.mean) p.mean[row] = mu;
-    if (p.rstd) p.rstd[row] = rstd;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t at = row * p.dim;
+    auto value = [&](int64_t c) {
+      const float x = IO::load(static_cast<const elem*>(p.x), at + c);
+      return p.residual ? x + p.residual[at + c] : x;
+    };
+    const float n = static_cast<float>(p.dim);
+    float s[1] = {0.0f}, sq[1] = {0.0f};
+    for (int64_t c = threadIdx.x; c < p.dim; c += kWide) s[0] += value(c);
+    row_sums<kWide>(s, lds, 0);
+    const float mu = s[0] / n;
+    for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
+      const float t = value(c) - mu;
+      sq[0] = fmaf(t, t, sq[0]);
+    }
+    row_sums<kWide>(sq, lds, 1);
+    const float rstd = 1.0f / __builtin_sqrtf(sq[0] / n + p.eps);
+    for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
+      const float t = value(c);
+      const float w = p.weight ? p.weight[c] : 1.0f, b = p.bias ? p.bias[c] : 0.0f;
+      static_cast<elem*>(p.out)[at + c] = IO::from_float(fmaf((t - mu) * rstd, w, b));
+      if (p.sum) p.sum[at + c] = t;
+    }
+    if (threadIdx.x == 0) {
+      if (p.mean) p.mean[row] = mu;
+      if (p.rstd) p.rstd[row] = rstd;
+    }
   }
 }
 
@@ -290,26 +293,29 @@ template <class IO, class S>
 __global__ __launch_bounds__(kWide) void norm_bwd_wide_kernel(NormArgs p) {
   using elem = typename IO::elem;
   __shared__ float lds[4 * 16];
-  const int64_t row = blockIdx.x, at = row * p.dim;
-  const float mu = p.mean_in[row], rstd = p.rstd_in[row];
-  const auto* sp = static_cast<const typename S::elem*>(p.x);
-  auto hat = [&](int64_t c) { return (S::load(sp, at + c) - mu) * rstd; };
-  auto grad = [&](int64_t c) {
-    return IO::load(static_cast<const elem*>(p.dout), at + c) * (p.weight ? p.weight[c] : 1.0f);
-  };
-  float s[2] = {0.0f, 0.0f};
-  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
-    const float g = grad(c);
-    s[0] += g;
-    s[1] = fmaf(g, hat(c), s[1]);
-  }
-  row_sums<kWide>(s, lds, 0);
-  const float inv = 1.0f / static_cast<float>(p.dim);
-  const float c1 = s[0] * inv, c2 = s[1] * inv;
-  for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
-    const float ds = fmaf(rstd, grad(c) - c1 - hat(c) * c2, p.dsum ? p.dsum[at + c] : 0.0f);
-    if (p.dx) static_cast<elem*>(p.dx)[at + c] = IO::from_float(ds);
-    if (p.dresidual) p.dresidual[at + c] = ds;
+  int phase = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++phase) {
+    const int64_t at = row * p.dim;
+    const float mu = p.mean_in[row], rstd = p.rstd_in[row];
+    const auto* sp = static_cast<const typename S::elem*>(p.x);
+    auto hat = [&](int64_t c) { return (S::load(sp, at + c) - mu) * rstd; };
+    auto grad = [&](int64_t c) {
+      return IO::load(static_cast<const elem*>(p.dout), at + c) * (p.weight ? p.weight[c] : 1.0f);
+    };
+    float s[2] = {0.0f, 0.0f};
+    for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
+      const float g = grad(c);
+      s[0] += g;
+      s[1] = fmaf(g, hat(c), s[1]);
+    }
+    row_sums<kWide>(s, lds, phase);
+    const float inv = 1.0f / static_cast<float>(p.dim);
+    const float c1 = s[0] * inv, c2 = s[1] * inv;
+    for (int64_t c = threadIdx.x; c < p.dim; c += kWide) {
+      const float ds = fmaf(rstd, grad(c) - c1 - hat(c) * c2, p.dsum ? p.dsum[at + c] : 0.0f);
+      if (p.dx) static_cast<elem*>(p.dx)[at + c] = IO::from_float(ds);
+      if (p.dresidual) p.dresidual[at + c] = ds;
+    }
   }
 }
 
@@ -346,11 +352,17 @@ int64_t strands_of(int64_t rows, int rows_per_group) {
   return n < kStrands ? n : kStrands;
 }
 
+// A workgroup per group of rows, up to `most` (a launch counts its threads in 32 bits); then they
+// loop.
+unsigned blocks_of(int64_t rows, int64_t rows_per_group, int64_t most) {
+  const int64_t n = (rows + rows_per_group - 1) / rows_per_group;
+  return static_cast<unsigned>(n < most ? n : most);
+}
+
 template <class IO, int V, int TPR, int K>
 void fwd(const NormArgs& a, hipStream_t stream) {
   constexpr int kRows = kBlock<TPR> / TPR;
-  hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K>),
-                     dim3(static_cast<unsigned>((a.rows + kRows - 1) / kRows)),
+  hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K>), dim3(blocks_of(a.rows, kRows, 1 << 21)),
                      dim3(kBlock<TPR>), 0, stream, a);
 }
 
@@ -402,7 +414,7 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
   const bool quads = a.dim % 4 == 0 && wide % 16 == 0 && io % (4 * sizeof(typename IO::elem)) == 0;
   const int tpr = threads_per_row(a.dim, quads ? 4 : 1);
   if (!tpr)
-    hipLaunchKernelGGL((norm_fwd_wide_kernel<IO>), dim3(static_cast<unsigned>(a.rows)),
+    hipLaunchKernelGGL((norm_fwd_wide_kernel<IO>), dim3(blocks_of(a.rows, 1, 4096)),
                        dim3(kWide), 0, stream, a);
   else
     with_shape(a.dim, quads, tpr, [&](auto v, auto t, auto k) { fwd<IO, v, t, k>(a, stream); });
@@ -422,7 +434,7 @@ hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
   float* part = a.dweight || a.dbias ? static_cast<float*>(a.workspace) : nullptr;
   int64_t lines = 0;
   if (!tpr) {
-    hipLaunchKernelGGL((norm_bwd_wide_kernel<IO, S>), dim3(static_cast<unsigned>(a.rows)),
+    hipLaunchKernelGGL((norm_bwd_wide_kernel<IO, S>), dim3(blocks_of(a.rows, 1, 4096)),
                        dim3(kWide), 0, stream, a);
     if (part) {
       const int64_t cols = (a.dim + 255) / 256;

@@ -68,6 +68,11 @@ REFUSED = [
     ("ss_gated_scan_fwd", FWD, dict(L=1 << 31), UNS, b"seqlen"),
     ("ss_gated_scan_fwd", FWD, dict(batch=1 << 40, L=1 << 30, d=1 << 20), BAD, b"overflow"),
     ("ss_gated_scan_fwd", FWD, dict(batch=1 << 20, L=1 << 20, d=1 << 10), BAD, b"too many"),
+    ("ss_gated_scan_fwd", FWD, dict(batch=1 << 24, L=100, d=64), BAD, b"one launch"),
+    ("ss_gated_scan_bwd", BWD, dict(batch=1 << 24, L=100, d=64), BAD, b"one launch"),
+    ("ss_gated_state_update", STEP, dict(batch=1 << 26, d=64), BAD, b"one launch"),
+    ("ss_causal_conv_fwd", CFWD, dict(batch=1 << 26, L=1, d=1), BAD, b"one launch"),
+    ("ss_causal_conv_update", CSTEP, dict(batch=1 << 26, d=64), BAD, b"one launch"),
     ("ss_gated_scan_fwd", FWD, dict(L=0, h0=G, hl=G + 4), BAD, b"overlaps"),
     ("ss_gated_scan_bwd", BWD, dict(dtype=9), UNS, b"dtype"),
     ("ss_gated_scan_bwd", BWD, dict(dout=None), BAD, b"dout is NULL"),

@@ -86,6 +86,24 @@ def test_a_mean_far_from_zero_does_not_cost_the_variance(dim):
     Case(4, 4, dim, "f32", False, shift=300.0).check()
 
 
+@pytest.mark.parametrize("rows,dim", [((1 << 23) + 7, 2), ((1 << 21) + 3, 513), (4100, 8193)])
+def test_more_rows_than_workgroups(rows, dim):
+    """The workgroups loop over the rows: those of the second round equal a call on them alone."""
+    o = ops()
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x = torch.randn(rows, dim, device="cuda", generator=g).bfloat16()
+    out, mean, rstd = o.layer_norm_fwd(x, return_stats=True)
+    for a, b in ((0, 9), (rows // 2, rows // 2 + 9), (rows - 9, rows)):
+        alone, m, r = o.layer_norm_fwd(x[a:b].contiguous(), return_stats=True)
+        assert torch.equal(out[a:b], alone)
+        assert torch.equal(mean[a:b], m) and torch.equal(rstd[a:b], r)
+    dx = o.layer_norm_bwd(x, x, None, mean, rstd, want_dparams=False)["dx"]
+    tail = slice(rows - 9, rows)
+    alone = o.layer_norm_bwd(x[tail].contiguous(), x[tail].contiguous(), None, mean[tail].clone(),
+                             rstd[tail].clone(), want_dparams=False)["dx"]
+    assert torch.equal(dx[tail], alone)
+
+
 def test_a_constant_row():
     o = ops()
     x = torch.full((3, 700), 2.5, device="cuda")
