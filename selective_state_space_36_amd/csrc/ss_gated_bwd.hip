@@ -83,7 +83,7 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
 
   // Decays and gates of every step.  Rows past the end were read as zeros; their steps are made
   // to change nothing.
-  float a[kSteps], rg[kSteps], ig[kSteps], y = 0.0f;
+  float a[kSteps], s[kSteps], rs[kSteps], rg[kSteps], ig[kSteps], y = 0.0f;
   float hp[kSteps];  // the input term, then the state before the step
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
@@ -91,8 +91,12 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
     ig[j] = sigmoid_biased(IO::widen(ir[j]), ib);
     const float l = A * rg[j];
     a[j] = exp2_hw(l);
-    hp[j] = decay_scale(l, a[j]) * ig[j] * IO::widen(xr[j]);
-    if (j < n) y += l;
+    // 1 / s from one reciprocal root, and s from it; both 0 where s is (not where it is NaN)
+    const float v = one_minus_square(l, a[j]);
+    rs[j] = v != 0.0f ? rsq_hw(v) : 0.0f;
+    s[j] = v * rs[j];
+    hp[j] = s[j] * ig[j] * IO::widen(xr[j]);
+    y += l;
   }
   // Starts and the end of the sequence are the exception: one test for the whole wave.
   const bool plain = fresh == 0 && n == kSteps;
@@ -103,12 +107,17 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
       hp[j] = j < n ? hp[j] : 0.0f;
     }
   }
-  // the product of the decays as 2 to the sum of their exponents
-  Piece piece{fresh ? 0.0f : fmaxf(exp2_hw(y), kTinyDecay), 0.0f};
+  Piece piece{0.0f, 0.0f};
   if (plain) {
+    piece.P = fmaxf(exp2_hw(y), kTinyDecay);  // the decays' product: 2 to the sum of exponents
 #pragma unroll
     for (int j = 0; j < kSteps; ++j) piece.H = fmaf(a[j], piece.H, hp[j]);
   } else {
+    if (!fresh) {
+      piece.P = 1.0f;
+#pragma unroll
+      for (int j = 0; j < kSteps; ++j) piece.P = fmaxf(piece.P * a[j], kTinyDecay);
+    }
 #pragma unroll
     for (int j = 0; j < kSteps; ++j)
       piece.H = fresh >> j & 1 ? hp[j] : fmaf(a[j], piece.H, hp[j]);
@@ -128,9 +137,10 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
     g[j] = IO::widen(gr[j]);
     if (GATE) {
       const float z = IO::widen(zr[j]), sg = sigmoid_f(z);
-      const float dz = g[j] * h * (sg * fmaf(z, 1.0f - sg, 1.0f));
+      const float silu = z * sg;
+      const float dz = g[j] * h * fmaf(silu, 1.0f - sg, sg);
       dzr.store(&dz, col + j * row);
-      g[j] *= z * sg;
+      g[j] *= silu;
     }
   };
   if (plain) {
@@ -176,12 +186,10 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
     const float x = IO::widen(xr[j]);
     const float lam = g[j] + carry;
     carry = drop ? 0.0f : a[j] * lam;
-    const float s = decay_scale(A * rg[j], a[j]);
-    // a^2 / s, 0 where s = 0: there a = 1 and dx, di vanish too
-    const float slope = s > 0.0f ? a[j] * a[j] * rcp_hw(s) : 0.0f;
     const float w = ig[j] * x;
-    const float dl = lam * fmaf(a[j], hp[j], -w * slope);
-    const float ls = lam * s, q = dl * rg[j];
+    // a h - ig x a^2 / s, whose second term is 0 where s = 0: there a = 1, and dx, di vanish too
+    const float dl = lam * (a[j] * fmaf(-w * rs[j], a[j], hp[j]));
+    const float ls = lam * s[j], q = dl * rg[j];
     const float dx = ls * ig[j];
     const float dr = q * (kLn2 * A) * (1.0f - rg[j]);
     const float di = ls * w * (1.0f - ig[j]);
