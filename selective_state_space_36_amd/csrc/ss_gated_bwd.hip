@@ -21,7 +21,7 @@ constexpr int kWaves = kTile / kSteps;
 template <class IO, bool GATE>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t groups,
-                      int32_t nseg) {
+                      int32_t nseg, uint32_t sets) {
   using elem = typename IO::elem;
   using R = Rows<IO, 1>;
   using F = Rows<F32, 1>;
@@ -35,9 +35,10 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int waves = blockDim.x >> 6;
   const uint32_t chains = static_cast<uint32_t>(p.batch) * groups;
-  const uint32_t tile =
-      nseg > 1 ? draw_tile(static_cast<uint32_t*>(p.workspace), &drawn) : blockIdx.x;
-  const uint32_t pos = tile / chains, chain = tile % chains;  // pos 0 is the last segment
+  const Draw drawn_tile =
+      draw_tile(static_cast<uint32_t*>(p.workspace), &drawn, chains, nseg, sets);
+  if (!drawn_tile.some) return;
+  const uint32_t pos = drawn_tile.pos, chain = drawn_tile.chain;  // pos 0 is the last segment
   const uint32_t seg = nseg - 1 - pos;
   const int64_t b = chain / groups;
   const int64_t c = static_cast<int64_t>(chain % groups) * 64 + lane;
@@ -254,14 +255,15 @@ hipError_t launch(const GatedArgs& a, const Layout& l, const float* states, floa
   }
   // a sequence shorter than a tile needs fewer waves
   const int waves = nseg > 1 ? kWaves : static_cast<int>((a.seqlen + kSteps - 1) / kSteps);
-  const dim3 grid(static_cast<unsigned>(a.batch * groups * nseg)), block(64 * waves);
+  const ChainGrid cg = chain_grid(a.batch * groups, nseg);
+  const dim3 grid(cg.workgroups), block(64 * waves);
   const int32_t g = static_cast<int32_t>(groups), n = static_cast<int32_t>(nseg);
   if (a.z)
-    hipLaunchKernelGGL((gated_bwd_kernel<IO, true>), grid, block, 0, stream, a, states, part, g,
-                       n);
+    hipLaunchKernelGGL((gated_bwd_kernel<IO, true>), grid, block, 0, stream, a, states, part, g, n,
+                       cg.sets);
   else
-    hipLaunchKernelGGL((gated_bwd_kernel<IO, false>), grid, block, 0, stream, a, states, part, g,
-                       n);
+    hipLaunchKernelGGL((gated_bwd_kernel<IO, false>), grid, block, 0, stream, a, states, part, g, n,
+                       cg.sets);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t tiles = a.batch * nseg, plane = tiles * a.d_inner;

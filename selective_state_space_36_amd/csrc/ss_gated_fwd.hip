@@ -19,7 +19,7 @@ constexpr int kWaves = kTile / kSteps;
 // up to 128 and keeps more loads in flight (708 against 730 us at 1 x 262144 x 1536).
 template <class IO, bool GATE>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
-void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg) {
+void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg, uint32_t sets) {
   using elem = typename IO::elem;
   using R = Rows<IO, 1>;
   using F = Rows<F32, 1>;
@@ -30,9 +30,10 @@ void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t chains = static_cast<uint32_t>(p.batch) * groups;
-  uint32_t* counter = static_cast<uint32_t*>(p.workspace);
-  const uint32_t tile = nseg > 1 ? draw_tile(counter, &drawn) : blockIdx.x;
-  const uint32_t seg = tile / chains, chain = tile % chains;
+  const Draw drawn_tile =
+      draw_tile(static_cast<uint32_t*>(p.workspace), &drawn, chains, nseg, sets);
+  if (!drawn_tile.some) return;
+  const uint32_t seg = drawn_tile.pos, chain = drawn_tile.chain;
   const int64_t b = chain / groups;
   const int64_t c = static_cast<int64_t>(chain % groups) * 64 + lane;
   const bool active = c < p.d_inner;
@@ -168,12 +169,13 @@ hipError_t launch(const GatedArgs& a, hipStream_t stream) {
   }
   // a sequence shorter than a tile needs fewer waves
   const int waves = nseg > 1 ? kWaves : static_cast<int>((a.seqlen + kSteps - 1) / kSteps);
-  const dim3 grid(static_cast<unsigned>(a.batch * groups * nseg)), block(64 * waves);
+  const ChainGrid cg = chain_grid(a.batch * groups, nseg);
+  const dim3 grid(cg.workgroups), block(64 * waves);
   const int32_t g = static_cast<int32_t>(groups), n = static_cast<int32_t>(nseg);
   if (a.z)
-    hipLaunchKernelGGL((gated_fwd_kernel<IO, true>), grid, block, 0, stream, a, g, n);
+    hipLaunchKernelGGL((gated_fwd_kernel<IO, true>), grid, block, 0, stream, a, g, n, cg.sets);
   else
-    hipLaunchKernelGGL((gated_fwd_kernel<IO, false>), grid, block, 0, stream, a, g, n);
+    hipLaunchKernelGGL((gated_fwd_kernel<IO, false>), grid, block, 0, stream, a, g, n, cg.sets);
   return hipGetLastError();
 }
 
