@@ -20,7 +20,8 @@ hipError_t fill(T* dst, const T* src, int64_t n, hipStream_t stream) {
 }
 
 // One workgroup sums 32 columns of one job: 32 strands of lines, eight lines in flight each, then
-// the strands in order.  The order of the additions depends on the number of lines alone.
+// the strands in order.  The order of the additions depends on the number of lines alone.  (With 16
+// strands and one line in flight 1024 lines of 2 x 2560 took 24 us, with these 7.5.)
 constexpr int kCols = 32, kStrands = 32, kAhead = 8;
 __global__ __launch_bounds__(kCols * kStrands) void column_sums_kernel(ColumnSums p) {
   __shared__ float lds[kStrands][kCols + 1];

@@ -5,6 +5,10 @@
 // come from the same registers.  Sums run over the lanes of a wave by DPP, over the waves through
 // LDS.  Rows too wide for that (over 16384 columns, or 8192 that are not groups of four) are read
 // again for each pass by the wide kernels.
+//
+// What bounds it: memory.  16384 x 2560 bfloat16 with the residual stream: forward 503 MB in 92 us
+// (5.5 TB/s), backward 671 MB in 130 us and 4 us for the parameters' sums (5.0 TB/s); a copy of
+// 1 GB reaches 5.0 TB/s.  The backward asks for a row's successor before it sums the row.
 #include "ss_block.h"
 #include "ss_rows.h"
 
@@ -344,8 +348,9 @@ int threads_per_row(int64_t dim, int v) {
   return dim <= 64 * each ? 64 : dim <= 256 * each ? 256 : dim <= 1024 * each ? 1024 : 0;
 }
 
-// Lines of partial sums, and with them workgroups of the backward: enough to fill the card, few
-// enough that the lines stay a small part of the traffic.
+// Lines of partial sums, and with them workgroups of the backward: two per CU fill the card as the
+// registers let them, and more lines are more traffic (16384 x 2560: 512 lines 225.7, 768 229.7,
+// 1024 233.4, 1536 235.9 us for forward and backward).
 constexpr int64_t kStrands = 512;
 int64_t strands_of(int64_t rows, int rows_per_group) {
   const int64_t n = (rows + rows_per_group - 1) / rows_per_group;
