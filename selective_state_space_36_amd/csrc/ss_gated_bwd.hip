@@ -99,9 +99,10 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
     ig[j] = sigmoid_biased(IO::widen(ir[j]), ib);
     const float l = A * rg[j];
     a[j] = exp2_hw(l);
-    // 1 / s from one reciprocal root, and s from it; both 0 where s is (not where it is NaN)
+    // 1 / s from one reciprocal root, and s from it; both 0 where s^2 is 0 or too small for the
+    // root's unit (which takes it for 0 and returns infinity), but not where it is NaN
     const float v = one_minus_square(l, a[j]);
-    rs[j] = v != 0.0f ? rsq_hw(v) : 0.0f;
+    rs[j] = fabsf(v) < kTinyDecay ? 0.0f : rsq_hw(v);
     s[j] = v * rs[j];
     hp[j] = s[j] * ig[j] * IO::widen(xr[j]);
     y += l;

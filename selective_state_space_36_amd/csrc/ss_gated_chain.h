@@ -1,8 +1,8 @@
 // ss_gated_chain.h -- how the workgroups of the gated recurrence hand the state from tile to tile.
 //
-// A workgroup owns one tile: T steps of one batch row and 64 channels, one per lane.  The sequence is a chain
-// of tiles per (batch row, channel group); a tile needs the state at its start, which depends on
-// every tile before it.  Two passes (summaries, then outputs) would read the inputs twice; here
+// A workgroup owns one tile: T steps of one batch row and 64 channels, one per lane.  The sequence
+// is a chain of tiles per (batch row, channel group); a tile needs the state at its start, which
+// depends on every tile before it.  Two passes (summaries, then outputs) would read the inputs twice; here
 // each tile is read once: it reduces its steps to a Piece, publishes it, picks up the pieces and
 // end states of the tiles before it, and only then runs its steps, which are still in registers.
 //

@@ -43,7 +43,7 @@ __device__ __forceinline__ float decay_scale(float y, float a) {
 // a sequence starts inside the piece, so that nothing before it may pass, not even an infinity or
 // a NaN; a product that is only too small for float32 is held at the smallest normal number
 // instead (an error below 2^-126 of the state), so that a NaN before it is not lost.
-constexpr float kTinyDecay = 1.17549435e-38f;
+constexpr float kTinyDecay = 1.17549435e-38f;  // 2^-126
 struct Piece {
   float P, H;
 };

@@ -120,6 +120,29 @@ def test_long_sequence(io):
     c.check_bwd(c.check_fwd())
 
 
+def test_one_chain_of_many_tiles():
+    """A single chain, so that most tiles of it are at work at the same time and look far back."""
+    c = Case(7, 1, 40000, 8, "f32", packed=False, h0=True)
+    c.check_bwd(c.check_fwd())
+
+
+def test_more_tiles_than_run_at_once():
+    """A call of 768 (backward 1504) tiles equals its rows one by one, of a quarter as many."""
+    c = Case(16, 4, 3000, 512, "bf16", gate=True, packed=True, h0=True)
+    out, states, last = c.fwd()
+    g = c.bwd(states)
+    for b in range(4):
+        row = {k: (t[b:b + 1].contiguous() if t is not None and t.dim() > 1 else t)
+               for k, t in c.g.items()}
+        o, s, l = ops().gated_scan_fwd_states(*c.args(row), **c.kw(row), return_last_state=True)
+        assert torch.equal(out[b:b + 1], o) and torch.equal(states[b:b + 1], s)
+        assert torch.equal(last[b:b + 1], l)
+        r = ops().gated_scan_bwd(*c.args(row), row["dout"], **c.kw(row), dh_last=row["dh_last"],
+                                 states=s)
+        for name in ("dx", "dr", "di", "dz", "dh0"):
+            assert torch.equal(g[name][b:b + 1], r[name]), name
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("offset", [1, 2, 3])
 def test_arrays_that_start_inside_a_wider_alignment(offset, io):
@@ -202,7 +225,8 @@ def test_a_nan_stays_in_its_channel_to_the_end_of_its_sequence():
 
 
 @pytest.mark.parametrize("A,r", [(0.0, 0.0), (-1e-30, 0.0), (-1e-4, 3.0), (-40.0, 5.0),
-                                 (-200.0, 9.0), (-1.0, -200.0), (-1.0, 200.0), (-0.5, -15.0)])
+                                 (-200.0, 9.0), (-1.0, -200.0), (-1.0, 200.0), (-0.5, -15.0),
+                                 (-0.01, -84.0), (-0.5, -87.0), (-0.01, -88.0)])
 def test_extreme_gates(A, r):
     """Decays of exactly 1, nearly 1, underflowing, and gates that saturate."""
     rng = np.random.default_rng(10)
@@ -217,6 +241,7 @@ def test_extreme_gates(A, r):
     want = bt.gated_bwd(*vs[:4], vs[4], h0=vs[5])
     for name in ("dx", "dr", "di", "dh0"):
         check(g[name], want[name], "f32", name, SPLIT)
+        assert torch.isfinite(g[name]).all(), name
     assert torch.isfinite(g["dA"]).all()
 
 
