@@ -38,11 +38,21 @@ struct Taps {
   }
 };
 
-// Bit j: a sequence starts at step t + j of row b, for j < n.
-__device__ __forceinline__ uint32_t starts_mask(const ConvArgs& p, int64_t b, int64_t t, int n) {
+// What lane j needs of the starts at steps t .. t + n - 1 of row b, n < 64 (steps outside the
+// sequence have none; without starts the resource is empty and nothing is read).
+__device__ __forceinline__ uint8_t starts_at(const ConvArgs& p, int64_t b, int64_t t, int n) {
   const int lane = threadIdx.x & 63;
-  const bool in = lane < n && t + lane >= 0 && t + lane < p.seqlen;
-  return static_cast<uint32_t>(__ballot(in && p.starts[b * p.seqlen + (in ? t + lane : 0)]));
+  const int64_t skip = t < 0 ? -t : 0;             // steps before the sequence
+  int64_t rest = p.seqlen - (t + skip);
+  rest = rest < 0 || !p.starts ? 0 : rest < n - skip ? rest : n - skip;
+  const rsrc_t r = make_buf(p.starts + (rest > 0 ? b * p.seqlen + t + skip : 0),
+                            rest > 0 ? static_cast<uint32_t>(rest) : 0);
+  // (lanes before the sequence have offsets past every range)
+  return __builtin_amdgcn_raw_buffer_load_b8(r, lane - static_cast<int>(skip), 0, 0);
+}
+// Bit j: a sequence starts at the step of lane j.
+__device__ __forceinline__ uint32_t starts_mask(uint8_t at) {
+  return static_cast<uint32_t>(__ballot(at != 0));
 }
 
 // Where a wave works: a run of steps of one batch row and 64 V channels.
@@ -66,7 +76,7 @@ __device__ __forceinline__ Rows<IO, V> rows_before(const ConvArgs& p, int64_t b,
   return rows_of<IO, V>(p.x_prev, p.x_prev ? b * (K - 1) * p.d_inner : 0, p.x_prev ? bytes : 0);
 }
 
-template <class IO, int V, int K, bool PACKED>
+template <class IO, int V, int K, bool SILU>
 __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs p, uint32_t groups,
                                                                int64_t runs) {
   using elem = typename IO::elem;
@@ -81,19 +91,17 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs p, uint3
   const int64_t first = (at.b * p.seqlen + at.t0) * p.d_inner;
   const auto H = rows_before<IO, V, K>(p, at.b, at.t0);
   const auto X = rows_of<IO, V>(p.x, first, n * row);
+  const uint8_t begins = starts_at(p, at.b, at.t0 - (K - 1), kFwdSteps + K - 1);
   typename Lanes<IO, V>::raw x[kFwdSteps + K - 1];
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) x[j] = H.load(col + j * row);
 #pragma unroll
   for (int j = 0; j < kFwdSteps; ++j) x[K - 1 + j] = X.load(col + j * row);
-  // seq[j]: starts up to the row of x[j]; the first row's own start does not matter
-  uint32_t mask = 0;
-  if (PACKED) mask = starts_mask(p, at.b, at.t0 - (K - 1), kFwdSteps + K - 1);
   Taps<V, K> taps;
   taps.load(p, at.c);
+  const uint32_t mask = starts_mask(begins);  // bit j: a sequence starts at the row of x[j]
   const auto O = rows_of<IO, V>(p.out, first, n * row);
-#pragma unroll
-  for (int j = 0; j < kFwdSteps; ++j) {
+  auto step = [&](int j, auto plain) {
     float y[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) y[v] = taps.bias[v];
@@ -101,23 +109,30 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs p, uint3
     for (int q = 0; q < K; ++q) {  // x[j + q] is K - 1 - q steps back
       // a start at one of the steps after that row, up to this one, cuts it off
       const uint32_t between = ((1u << (K - 1 - q)) - 1) << (j + q + 1);
-      if (PACKED && (mask & between)) continue;
+      if (!decltype(plain)::value && (mask & between)) continue;
 #pragma unroll
       for (int v = 0; v < V; ++v)
         y[v] = fmaf(taps.w[q][v], Lanes<IO, V>::get(x[j + q], v), y[v]);
     }
-    if (p.silu) {
+    if (SILU) {
 #pragma unroll
       for (int v = 0; v < V; ++v) y[v] = silu_f(y[v]);
     }
     O.store(y, col + j * row);
+  };
+  if (mask == 0) {
+#pragma unroll
+    for (int j = 0; j < kFwdSteps; ++j) step(j, std::true_type{});
+  } else {
+#pragma unroll
+    for (int j = 0; j < kFwdSteps; ++j) step(j, std::false_type{});
   }
 }
 
 // One wave walks `steps` steps from t0 and the k - 1 after them (whose g the last dx need; their
 // own dx and sums belong to the next wave), kStride rows in flight.  The rows of sums of a
 // workgroup's waves are added in LDS into part[workgroup][K + 1][d_inner].
-template <class IO, int V, int K, bool PACKED>
+template <class IO, int V, int K, bool SILU>
 __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint32_t groups,
                                                                int64_t runs, int32_t steps,
                                                                float* part) {
@@ -166,9 +181,9 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
     const auto DP = rows_of<IO, V>(p.dx_prev, prev ? at.b * (K - 1) * p.d_inner : 0,
                                    prev ? (K - 1) * row : 0);
     typename L::raw xn[kStride], gn[kStride];
-    uint32_t begins = 0;                      // starts at the K - 1 steps before s0, then from s0 on
-    if (PACKED) begins = starts_mask(p, at.b, at.t0 - (K - 1), K - 1);
-    uint32_t starts = 0;
+    // starts at the K - 1 steps before s0, then from s0 on
+    uint32_t begins = starts_mask(starts_at(p, at.b, at.t0 - (K - 1), K - 1));
+    uint8_t starts = 0;
     // rows are addressed kStride at a time, so that 32-bit offsets reach for any d_inner
     auto fetch = [&](int s0) {
       const int more = have - s0 < 0 ? 0 : have - s0 < kStride ? have - s0 : kStride;
@@ -180,7 +195,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
         xn[j] = X.load(col + j * row);
         gn[j] = G.load(col + j * row);
       }
-      if (PACKED) starts = starts_mask(p, at.b, at.t0 + s0, kStride);
+      starts = starts_at(p, at.b, at.t0 + s0, kStride);
     };
     fetch(0);
     for (int s0 = 0; s0 < all; s0 += kStride) {
@@ -190,7 +205,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
         xr[j] = xn[j];
         gr[j] = gn[j];
       }
-      if (PACKED) begins |= starts << (K - 1);  // bit j + K - 1: a sequence starts at step s0 + j
+      begins |= starts_mask(starts) << (K - 1);  // bit j + K - 1: a sequence starts at step s0 + j
       const uint32_t now = begins;
       // dx trails by K - 1 steps
       static_assert(kStride >= K, "the first rows hold a whole window");
@@ -220,7 +235,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
 #pragma unroll
           for (int v = 0; v < V; ++v) pre[v] = fmaf(taps.w[q][v], xw[q][v], pre[v]);
         }
-        if (p.silu) {
+        if (SILU) {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const float sg = sigmoid_f(pre[v]);
@@ -275,7 +290,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
           if (s0 + j < all) step(j, std::false_type{});
         }
       }
-      if (PACKED) begins = now >> kStride;
+      begins = now >> kStride;
     }
   }
 #pragma unroll
@@ -356,7 +371,7 @@ hipError_t launch_fwd(const ConvArgs& a, hipStream_t stream) {
   const dim3 block(64 * kWaves);
   const uint32_t g = static_cast<uint32_t>(groups);
   with_width(a.k, [&](auto k) {
-    if (a.starts)
+    if (a.silu)
       hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, true>), grid, block, 0, stream, a, g, runs);
     else
       hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, false>), grid, block, 0, stream, a, g, runs);
@@ -374,7 +389,7 @@ hipError_t launch_bwd(const ConvArgs& a, hipStream_t stream) {
   const uint32_t g = static_cast<uint32_t>(groups);
   float* part = static_cast<float*>(a.workspace);
   with_width(a.k, [&](auto k) {
-    if (a.starts)
+    if (a.silu)
       hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, true>), grid, block, 0, stream, a, g, runs,
                          steps, part);
     else
