@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ss_scan.h"
 
 namespace ss {
@@ -135,5 +137,17 @@ struct ColumnSums {
   }
 };
 hipError_t launch_column_sums(const ColumnSums& p, hipStream_t stream);
+
+// Calls f with the truth values as compile-time constants.
+template <class F>
+void with_bools(F f, bool a, bool b) {
+  using std::bool_constant;
+  if (a)
+    b ? f(bool_constant<true>{}, bool_constant<true>{})
+      : f(bool_constant<true>{}, bool_constant<false>{});
+  else
+    b ? f(bool_constant<false>{}, bool_constant<true>{})
+      : f(bool_constant<false>{}, bool_constant<false>{});
+}
 
 }  // namespace ss

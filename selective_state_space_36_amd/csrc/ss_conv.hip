@@ -76,7 +76,7 @@ __device__ __forceinline__ Rows<IO, V> rows_before(const ConvArgs& p, int64_t b,
   return rows_of<IO, V>(p.x_prev, p.x_prev ? b * (K - 1) * p.d_inner : 0, p.x_prev ? bytes : 0);
 }
 
-template <class IO, int V, int K, bool SILU>
+template <class IO, int V, int K, bool SILU, bool PAST>
 __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs p, uint32_t groups,
                                                                int64_t runs) {
   using elem = typename IO::elem;
@@ -100,7 +100,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs p, uint3
   Taps<V, K> taps;
   taps.load(p, at.c);
   const uint32_t mask = starts_mask(begins);  // bit j: a sequence starts at the row of x[j]
-  const auto O = rows_of<IO, V>(p.out, first, n * row);
+  const auto O = rows_of<IO, V, PAST>(p.out, first, n * row);
   auto step = [&](int j, auto plain) {
     float y[V];
 #pragma unroll
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_fwd_kernel(ConvArgs p, uint3
 // One wave walks `steps` steps from t0 and the k - 1 after them (whose g the last dx need; their
 // own dx and sums belong to the next wave), kStride rows in flight.  The rows of sums of a
 // workgroup's waves are added in LDS into part[workgroup][K + 1][d_inner].
-template <class IO, int V, int K, bool SILU>
+template <class IO, int V, int K, bool SILU, bool PAST>
 __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint32_t groups,
                                                                int64_t runs, int32_t steps,
                                                                float* part) {
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
       static_assert(kStride >= K, "the first rows hold a whole window");
       const int skip = s0 ? 0 : K - 1, r0 = s0 ? s0 - (K - 1) : 0;
       const int rest = n - r0 < 0 ? 0 : n - r0 < kStride ? n - r0 : kStride;
-      const auto DX = rows_of<IO, V>(p.dx, first + (rest ? r0 * p.d_inner : 0), rest * row);
+      const auto DX = rows_of<IO, V, PAST>(p.dx, first + (rest ? r0 * p.d_inner : 0), rest * row);
       if (s0 + kStride < all) fetch(s0 + kStride);
       // Step s0 + j.  PLAIN: all of the kStride steps are the wave's own and no sequence starts
       // among them or in the window, so that nothing in them branches.
@@ -370,11 +370,13 @@ hipError_t launch_fwd(const ConvArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.batch * runs + kWaves - 1) / kWaves * groups));
   const dim3 block(64 * kWaves);
   const uint32_t g = static_cast<uint32_t>(groups);
+  const int64_t bytes = a.batch * a.seqlen * a.d_inner * sizeof(typename IO::elem);
   with_width(a.k, [&](auto k) {
-    if (a.silu)
-      hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, true>), grid, block, 0, stream, a, g, runs);
-    else
-      hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, false>), grid, block, 0, stream, a, g, runs);
+    auto go = [&](auto silu, auto past) {
+      hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, silu, past>), grid, block, 0, stream, a, g,
+                         runs);
+    };
+    with_bools(go, a.silu, stores_pass_cache(2 * bytes));
   });
   return hipGetLastError();
 }
@@ -387,14 +389,14 @@ hipError_t launch_bwd(const ConvArgs& a, hipStream_t stream) {
   const int64_t lines = lines_of(a.batch, a.seqlen, steps);
   const dim3 grid(static_cast<unsigned>(lines * groups)), block(64 * kWaves);
   const uint32_t g = static_cast<uint32_t>(groups);
+  const int64_t bytes = a.batch * a.seqlen * a.d_inner * sizeof(typename IO::elem);
   float* part = static_cast<float*>(a.workspace);
   with_width(a.k, [&](auto k) {
-    if (a.silu)
-      hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, true>), grid, block, 0, stream, a, g, runs,
-                         steps, part);
-    else
-      hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, false>), grid, block, 0, stream, a, g, runs,
-                         steps, part);
+    auto go = [&](auto silu, auto past) {
+      hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, silu, past>), grid, block, 0, stream, a, g,
+                         runs, steps, part);
+    };
+    with_bools(go, a.silu, stores_pass_cache(3 * bytes));
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

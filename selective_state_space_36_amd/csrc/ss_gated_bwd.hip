@@ -25,7 +25,7 @@ constexpr int kSteps = kGatedBwdSteps;
 constexpr int kTile = SS_GATED_CHUNK;  // so that a tile starts at a saved state
 constexpr int kWaves = kTile / kSteps;
 
-template <class IO, bool GATE>
+template <class IO, bool GATE, bool PAST>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t groups,
                       int32_t nseg, uint32_t sets) {
@@ -137,7 +137,8 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
 
   // the states before each step, the gated upstream gradient, dz, and the adjoint's piece
   float g[kSteps], M = 0.0f;
-  const R dzr = rows(p.dz);
+  auto outs = [&](void* base) { return rows_of<IO, 1, PAST>(base, first, n * row); };
+  const auto dzr = outs(p.dz);
   auto forward = [&](int j, bool drop) {
     if (drop) h = 0.0f;
     const float in = hp[j];
@@ -189,7 +190,7 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
   for (int k = waves - 1; k > wave; --k)
     carry = advance(Piece{pieces[k][lane].P, back[k][lane]}, carry);
 
-  const R dxr = rows(p.dx), drr = rows(p.dr), dir = rows(p.di);
+  const auto dxr = outs(p.dx), drr = outs(p.dr), dir = outs(p.di);
   float sum_A = 0.0f, sum_r = 0.0f, sum_i = 0.0f;
   auto gradients = [&](int j, bool drop) {
     const float x = IO::widen(xr[j]);
@@ -266,12 +267,12 @@ hipError_t launch(const GatedArgs& a, const Layout& l, const float* states, floa
   const ChainGrid cg = chain_grid(a.batch * groups, nseg);
   const dim3 grid(cg.workgroups), block(64 * waves);
   const int32_t g = static_cast<int32_t>(groups), n = static_cast<int32_t>(nseg);
-  if (a.z)
-    hipLaunchKernelGGL((gated_bwd_kernel<IO, true>), grid, block, 0, stream, a, states, part, g, n,
-                       cg.sets);
-  else
-    hipLaunchKernelGGL((gated_bwd_kernel<IO, false>), grid, block, 0, stream, a, states, part, g, n,
-                       cg.sets);
+  const int64_t bytes = a.batch * a.seqlen * a.d_inner * sizeof(typename IO::elem);
+  auto go = [&](auto gate, auto past) {
+    hipLaunchKernelGGL((gated_bwd_kernel<IO, gate, past>), grid, block, 0, stream, a, states, part,
+                       g, n, cg.sets);
+  };
+  with_bools(go, a.z != nullptr, stores_pass_cache(bytes * (a.z ? 9 : 7)));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t tiles = a.batch * nseg, plane = tiles * a.d_inner;

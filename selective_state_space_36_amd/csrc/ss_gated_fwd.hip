@@ -28,7 +28,7 @@ constexpr int kWaves = kTile / kSteps;
 
 // Four waves per SIMD (two workgroups per CU) whatever the registers: told so, the compiler takes
 // up to 128 and keeps more loads in flight (708 against 730 us at 1 x 262144 x 1536).
-template <class IO, bool GATE>
+template <class IO, bool GATE, bool PAST>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg, uint32_t sets) {
   using elem = typename IO::elem;
@@ -140,7 +140,7 @@ void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg, uint32_t sets) 
   }
   for (int k = 0; k < wave; ++k) h = advance(pieces[k][lane], h);
 
-  const R o = rows(p.out);
+  const auto o = rows_of<IO, 1, PAST>(p.out, first, n * row);
   auto finish = [&](int j) {  // out of step j from its state
     const float out = GATE ? h * silu_f(IO::widen(zr[j])) : h;
     if (p.out) o.store(&out, col + j * row);
@@ -183,10 +183,12 @@ hipError_t launch(const GatedArgs& a, hipStream_t stream) {
   const ChainGrid cg = chain_grid(a.batch * groups, nseg);
   const dim3 grid(cg.workgroups), block(64 * waves);
   const int32_t g = static_cast<int32_t>(groups), n = static_cast<int32_t>(nseg);
-  if (a.z)
-    hipLaunchKernelGGL((gated_fwd_kernel<IO, true>), grid, block, 0, stream, a, g, n, cg.sets);
-  else
-    hipLaunchKernelGGL((gated_fwd_kernel<IO, false>), grid, block, 0, stream, a, g, n, cg.sets);
+  const int64_t bytes = a.batch * a.seqlen * a.d_inner * sizeof(typename IO::elem);
+  auto go = [&](auto gate, auto past) {
+    hipLaunchKernelGGL((gated_fwd_kernel<IO, gate, past>), grid, block, 0, stream, a, g, n,
+                       cg.sets);
+  };
+  with_bools(go, a.z != nullptr, stores_pass_cache(bytes * (a.z ? 5 : 4)));
   return hipGetLastError();
 }
 

@@ -54,7 +54,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* lds, int phase) {
 template <int TPR>
 constexpr int kBlock = TPR < 256 ? 256 : TPR;  // threads of a workgroup
 
-template <class IO, int V, int TPR, int K>
+template <class IO, int V, int TPR, int K, bool PAST>
 __global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(NormArgs p) {
   __shared__ float lds[2 * 16];
   constexpr int kRows = kBlock<TPR> / TPR;
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(NormArgs p) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kRows;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + sub; row < p.rows; row += stride) {
     const int64_t at = row * p.dim;
-    const auto X = rows_of<IO, V>(p.x, at, dim * sizeof(typename IO::elem));
+    const auto X = rows_of<IO, V, PAST>(p.x, at, dim * sizeof(typename IO::elem));
     const auto W = rows_of<F32, V>(p.weight, 0, p.weight ? dim * 4 : 0);
     const auto B = rows_of<F32, V>(p.bias, 0, p.bias ? dim * 4 : 0);
     typename Lanes<IO, V>::raw xr[K];
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(NormArgs p) {
       xr[k] = X.load(col * sizeof(typename IO::elem));
     }
     if (p.residual) {
-      const auto R = rows_of<F32, V>(p.residual, at, dim * 4);
+      const auto R = rows_of<F32, V, PAST>(p.residual, at, dim * 4);
 #pragma unroll
       for (int k = 0; k < K; ++k) rr[k] = R.load((k * TPR + tid) * V * 4);
     }
@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_fwd_kernel(NormArgs p) {
 
 // Each row group of the launch walks the rows with the launch's stride and adds dweight and dbias
 // in its registers; part[strand][2][dim] takes one line per workgroup.
-template <class IO, class S, int V, int TPR, int K>
+template <class IO, class S, int V, int TPR, int K, bool PAST>
 __global__ __launch_bounds__(kBlock<TPR>) void norm_bwd_kernel(NormArgs p, float* part) {
   constexpr int kRows = kBlock<TPR> / TPR;
   __shared__ float lds[4 * 16];
@@ -164,15 +164,15 @@ __global__ __launch_bounds__(kBlock<TPR>) void norm_bwd_kernel(NormArgs p, float
   auto fetch = [&](int64_t row) {
     const bool in = row < p.rows;
     const int64_t at = in ? row * p.dim : 0;
-    const auto G = rows_of<IO, V>(p.dout, at, in ? dim * sizeof(typename IO::elem) : 0);
-    const auto X = rows_of<S, V>(p.x, at, in ? dim * sizeof(typename S::elem) : 0);
+    const auto G = rows_of<IO, V, PAST>(p.dout, at, in ? dim * sizeof(typename IO::elem) : 0);
+    const auto X = rows_of<S, V, PAST>(p.x, at, in ? dim * sizeof(typename S::elem) : 0);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       gr[k] = G.load((k * TPR + tid) * V * sizeof(typename IO::elem));
       sr[k] = X.load((k * TPR + tid) * V * sizeof(typename S::elem));
     }
     if (p.dsum) {
-      const auto U = rows_of<F32, V>(p.dsum, at, in ? dim * 4 : 0);
+      const auto U = rows_of<F32, V, PAST>(p.dsum, at, in ? dim * 4 : 0);
 #pragma unroll
       for (int k = 0; k < K; ++k) ur[k] = U.load((k * TPR + tid) * V * 4);
     }
@@ -367,15 +367,26 @@ unsigned blocks_of(int64_t rows, int64_t rows_per_group, int64_t most) {
 template <class IO, int V, int TPR, int K>
 void fwd(const NormArgs& a, hipStream_t stream) {
   constexpr int kRows = kBlock<TPR> / TPR;
-  hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K>), dim3(blocks_of(a.rows, kRows, 1 << 21)),
-                     dim3(kBlock<TPR>), 0, stream, a);
+  const dim3 grid(blocks_of(a.rows, kRows, 1 << 21)), block(kBlock<TPR>);
+  const int64_t each = 2 * sizeof(typename IO::elem) + (a.residual ? 4 : 0) + (a.sum ? 4 : 0);
+  if (loads_pass_cache(a.rows * a.dim * each))
+    hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K, true>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K, false>), grid, block, 0, stream, a);
 }
 
 template <class IO, class S, int V, int TPR, int K>
 void bwd(const NormArgs& a, float* part, int64_t* lines, hipStream_t stream) {
   *lines = strands_of(a.rows, kBlock<TPR> / TPR);
-  hipLaunchKernelGGL((norm_bwd_kernel<IO, S, V, TPR, K>), dim3(static_cast<unsigned>(*lines)),
-                     dim3(kBlock<TPR>), 0, stream, a, part);
+  const dim3 grid(static_cast<unsigned>(*lines)), block(kBlock<TPR>);
+  const int64_t es = sizeof(typename IO::elem);
+  const int64_t each = es + sizeof(typename S::elem) + (a.dsum ? 4 : 0) + (a.dx ? es : 0) +
+                       (a.dresidual ? 4 : 0);
+  if (loads_pass_cache(a.rows * a.dim * each))
+    hipLaunchKernelGGL((norm_bwd_kernel<IO, S, V, TPR, K, true>), grid, block, 0, stream, a, part);
+  else
+    hipLaunchKernelGGL((norm_bwd_kernel<IO, S, V, TPR, K, false>), grid, block, 0, stream, a,
+                       part);
 }
 
 // Calls f with the instance's V, TPR and K: groups of four columns (V = 4) in up to four rounds,

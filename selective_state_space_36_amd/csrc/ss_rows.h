@@ -74,38 +74,53 @@ struct Lanes<F32, 4> {
 // pass kOffNone and do neither, and an access costs one 32-bit offset register that all arrays
 // share.  The whole offset is in that register: the range check subtracts a scalar offset from
 // the size, which is no check where the difference would be negative.
-template <class IO, int V>
+//
+// PAST: the access is marked non-temporal, so that it does not keep a place in the caches.  That is
+// for calls that move more than the 256 MB Infinity Cache holds (below), where nobody
+// finds their rows there again: stores of the recurrence and the convolution (4 x 4096 x 5120
+// training 548 -> 536 and 185 -> 173 us, 8 x 2048 x 1536 167 -> 160), loads of the layer norm
+// (16384 x 2560 training 227 -> 208).  Below that it costs (the norm at 16384 x 768 65 -> 68 us,
+// the recurrence in float32 at 3 x 1111 x 1027 50.9 -> 51.9).
+template <class IO, int V, bool PAST = false>
 struct Rows {
   using raw = typename Lanes<IO, V>::raw;
+  static constexpr int kAux = PAST ? 2 : 0;  // the instruction's nt bit
   rsrc_t r;
   __device__ __forceinline__ raw load(uint32_t off) const {
     if constexpr (sizeof(raw) == 2)
-      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, kAux));
     else if constexpr (sizeof(raw) == 4)
-      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kAux));
     else if constexpr (sizeof(raw) == 8)
-      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, kAux));
     else
-      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, kAux));
   }
   __device__ __forceinline__ void store(const float* f, uint32_t off) const {
     const raw v = Lanes<IO, V>::put(f);
     using v2u = __attribute__((ext_vector_type(2))) unsigned int;
     using v4u = __attribute__((ext_vector_type(4))) unsigned int;
     if constexpr (sizeof(raw) == 2)
-      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, kAux);
     else if constexpr (sizeof(raw) == 4)
-      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, kAux);
     else if constexpr (sizeof(raw) == 8)
-      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, v), r, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(v2u, v), r, off, 0, kAux);
     else
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, off, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, v), r, off, 0, kAux);
   }
 };
 // `first`: the first row's element offset in the array, `bytes`: of the whole run (below 2^31).
-template <class IO, int V>
-__device__ __forceinline__ Rows<IO, V> rows_of(const void* base, int64_t first, uint32_t bytes) {
-  return Rows<IO, V>{make_buf(static_cast<const typename IO::elem*>(base) + first, bytes)};
+template <class IO, int V, bool PAST = false>
+__device__ __forceinline__ Rows<IO, V, PAST> rows_of(const void* base, int64_t first,
+                                                     uint32_t bytes) {
+  return Rows<IO, V, PAST>{make_buf(static_cast<const typename IO::elem*>(base) + first, bytes)};
 }
+
+// Whether a call that moves `bytes` outgrows the Infinity Cache, for its stores; its loads, which
+// may find what an earlier call left there, count as passing it from half as much again (the norm
+// at 4096 x 5120, 335 MB a backward pass: 121 us, 124 with non-temporal loads).
+inline bool stores_pass_cache(int64_t bytes) { return bytes >= (int64_t(256) << 20); }
+inline bool loads_pass_cache(int64_t bytes) { return bytes >= (int64_t(384) << 20); }
 
 }  // namespace ss
