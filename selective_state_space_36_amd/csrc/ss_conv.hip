@@ -178,8 +178,8 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
       }
     }
     const bool prev = at.t0 == 0 && p.dx_prev;
-    const auto DP = rows_of<IO, V>(p.dx_prev, prev ? at.b * (K - 1) * p.d_inner : 0,
-                                   prev ? (K - 1) * row : 0);
+    const auto DP = rows_of<IO, V, PAST>(p.dx_prev, prev ? at.b * (K - 1) * p.d_inner : 0,
+                                         prev ? (K - 1) * row : 0);
     typename L::raw xn[kStride], gn[kStride];
     // starts at the K - 1 steps before s0, then from s0 on
     uint32_t begins = starts_mask(starts_at(p, at.b, at.t0 - (K - 1), K - 1));
@@ -188,8 +188,8 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
     auto fetch = [&](int s0) {
       const int more = have - s0 < 0 ? 0 : have - s0 < kStride ? have - s0 : kStride;
       const int64_t f = more ? first + s0 * p.d_inner : 0;
-      const auto X = rows_of<IO, V>(p.x, f, more * row);
-      const auto G = rows_of<IO, V>(p.dout, f, more * row);
+      const auto X = rows_of<IO, V, PAST>(p.x, f, more * row);
+      const auto G = rows_of<IO, V, PAST>(p.dout, f, more * row);
 #pragma unroll
       for (int j = 0; j < kStride; ++j) {
         xn[j] = X.load(col + j * row);
@@ -376,7 +376,7 @@ hipError_t launch_fwd(const ConvArgs& a, hipStream_t stream) {
       hipLaunchKernelGGL((conv_fwd_kernel<IO, V, k, silu, past>), grid, block, 0, stream, a, g,
                          runs);
     };
-    with_bools(go, a.silu, stores_pass_cache(2 * bytes));
+    with_bools(go, a.silu, passes_cache(2 * bytes));
   });
   return hipGetLastError();
 }
@@ -396,7 +396,7 @@ hipError_t launch_bwd(const ConvArgs& a, hipStream_t stream) {
       hipLaunchKernelGGL((conv_bwd_kernel<IO, V, k, silu, past>), grid, block, 0, stream, a, g,
                          runs, steps, part);
     };
-    with_bools(go, a.silu, stores_pass_cache(3 * bytes));
+    with_bools(go, a.silu, passes_cache(3 * bytes));
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

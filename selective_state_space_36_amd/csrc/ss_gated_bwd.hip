@@ -30,7 +30,7 @@ __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 
 void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t groups,
                       int32_t nseg, uint32_t sets) {
   using elem = typename IO::elem;
-  using R = Rows<IO, 1>;
+  using R = Rows<IO, 1, PAST>;
   using F = Rows<F32, 1>;
   __shared__ Piece pieces[kWaves][64];
   __shared__ float back[kWaves][64];
@@ -58,7 +58,7 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
   const int64_t first = n ? (row0 + t0) * p.d_inner : 0;
   const uint32_t row = static_cast<uint32_t>(p.d_inner) * sizeof(elem);
   const uint32_t col = active ? static_cast<uint32_t>(c) * sizeof(elem) : kOffNone;
-  auto rows = [&](const void* base) { return rows_of<IO, 1>(base, first, n * row); };
+  auto rows = [&](const void* base) { return rows_of<IO, 1, PAST>(base, first, n * row); };
   // Parameters and starts are asked for first: what is waited for last is then the rows, once.
   // (An absent array is an empty resource and reads as zeros, without a branch to wait at.)
   const uint32_t wide = static_cast<uint32_t>(p.d_inner) * 4;
@@ -137,8 +137,7 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
 
   // the states before each step, the gated upstream gradient, dz, and the adjoint's piece
   float g[kSteps], M = 0.0f;
-  auto outs = [&](void* base) { return rows_of<IO, 1, PAST>(base, first, n * row); };
-  const auto dzr = outs(p.dz);
+  const R dzr = rows(p.dz);
   auto forward = [&](int j, bool drop) {
     if (drop) h = 0.0f;
     const float in = hp[j];
@@ -190,7 +189,7 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
   for (int k = waves - 1; k > wave; --k)
     carry = advance(Piece{pieces[k][lane].P, back[k][lane]}, carry);
 
-  const auto dxr = outs(p.dx), drr = outs(p.dr), dir = outs(p.di);
+  const R dxr = rows(p.dx), drr = rows(p.dr), dir = rows(p.di);
   float sum_A = 0.0f, sum_r = 0.0f, sum_i = 0.0f;
   auto gradients = [&](int j, bool drop) {
     const float x = IO::widen(xr[j]);
@@ -272,7 +271,7 @@ hipError_t launch(const GatedArgs& a, const Layout& l, const float* states, floa
     hipLaunchKernelGGL((gated_bwd_kernel<IO, gate, past>), grid, block, 0, stream, a, states, part,
                        g, n, cg.sets);
   };
-  with_bools(go, a.z != nullptr, stores_pass_cache(bytes * (a.z ? 9 : 7)));
+  with_bools(go, a.z != nullptr, passes_cache(bytes * (a.z ? 9 : 7)));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t tiles = a.batch * nseg, plane = tiles * a.d_inner;

@@ -32,7 +32,7 @@ template <class IO, bool GATE, bool PAST>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg, uint32_t sets) {
   using elem = typename IO::elem;
-  using R = Rows<IO, 1>;
+  using R = Rows<IO, 1, PAST>;
   using F = Rows<F32, 1>;
   __shared__ Piece pieces[kWaves][64];
   __shared__ float before[64];
@@ -56,7 +56,7 @@ void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg, uint32_t sets) 
   const int64_t first = n ? (row0 + t0) * p.d_inner : 0;
   const uint32_t row = static_cast<uint32_t>(p.d_inner) * sizeof(elem);
   const uint32_t col = active ? static_cast<uint32_t>(c) * sizeof(elem) : kOffNone;
-  auto rows = [&](const void* base) { return rows_of<IO, 1>(base, first, n * row); };
+  auto rows = [&](const void* base) { return rows_of<IO, 1, PAST>(base, first, n * row); };
   // Parameters and starts are asked for first: what is waited for last is then the rows, once.
   // (An absent array is an empty resource and reads as zeros, without a branch to wait at.)
   const uint32_t wide = static_cast<uint32_t>(p.d_inner) * 4;
@@ -140,7 +140,7 @@ void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg, uint32_t sets) 
   }
   for (int k = 0; k < wave; ++k) h = advance(pieces[k][lane], h);
 
-  const auto o = rows_of<IO, 1, PAST>(p.out, first, n * row);
+  const R o = rows(p.out);
   auto finish = [&](int j) {  // out of step j from its state
     const float out = GATE ? h * silu_f(IO::widen(zr[j])) : h;
     if (p.out) o.store(&out, col + j * row);
@@ -188,7 +188,7 @@ hipError_t launch(const GatedArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((gated_fwd_kernel<IO, gate, past>), grid, block, 0, stream, a, g, n,
                        cg.sets);
   };
-  with_bools(go, a.z != nullptr, stores_pass_cache(bytes * (a.z ? 5 : 4)));
+  with_bools(go, a.z != nullptr, passes_cache(bytes * (a.z ? 5 : 4)));
   return hipGetLastError();
 }
 

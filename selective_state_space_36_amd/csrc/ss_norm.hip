@@ -369,7 +369,7 @@ void fwd(const NormArgs& a, hipStream_t stream) {
   constexpr int kRows = kBlock<TPR> / TPR;
   const dim3 grid(blocks_of(a.rows, kRows, 1 << 21)), block(kBlock<TPR>);
   const int64_t each = 2 * sizeof(typename IO::elem) + (a.residual ? 4 : 0) + (a.sum ? 4 : 0);
-  if (loads_pass_cache(a.rows * a.dim * each))
+  if (passes_cache(a.rows * a.dim * each))
     hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K, true>), grid, block, 0, stream, a);
   else
     hipLaunchKernelGGL((norm_fwd_kernel<IO, V, TPR, K, false>), grid, block, 0, stream, a);
@@ -382,7 +382,7 @@ void bwd(const NormArgs& a, float* part, int64_t* lines, hipStream_t stream) {
   const int64_t es = sizeof(typename IO::elem);
   const int64_t each = es + sizeof(typename S::elem) + (a.dsum ? 4 : 0) + (a.dx ? es : 0) +
                        (a.dresidual ? 4 : 0);
-  if (loads_pass_cache(a.rows * a.dim * each))
+  if (passes_cache(a.rows * a.dim * each))
     hipLaunchKernelGGL((norm_bwd_kernel<IO, S, V, TPR, K, true>), grid, block, 0, stream, a, part);
   else
     hipLaunchKernelGGL((norm_bwd_kernel<IO, S, V, TPR, K, false>), grid, block, 0, stream, a,

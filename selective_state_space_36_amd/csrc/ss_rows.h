@@ -76,11 +76,11 @@ struct Lanes<F32, 4> {
 // the size, which is no check where the difference would be negative.
 //
 // PAST: the access is marked non-temporal, so that it does not keep a place in the caches.  That is
-// for calls that move more than the 256 MB Infinity Cache holds (below), where nobody
-// finds their rows there again: stores of the recurrence and the convolution (4 x 4096 x 5120
-// training 548 -> 536 and 185 -> 173 us, 8 x 2048 x 1536 167 -> 160), loads of the layer norm
-// (16384 x 2560 training 227 -> 208).  Below that it costs (the norm at 16384 x 768 65 -> 68 us,
-// the recurrence in float32 at 3 x 1111 x 1027 50.9 -> 51.9).
+// for calls that move more than the 256 MB Infinity Cache holds (passes_cache), where nobody finds
+// their rows there again.  Training steps, never / always: recurrence 4 x 4096 x 5120 551 / 527 us,
+// 8 x 2048 x 1536 189 / 179, 2 x 2048 x 1536 (63 and 113 MB) 60.4 / 65.4; norm (loads only)
+// 16384 x 2560 227 / 206, 10000 x 2560 142 / 123, 16384 x 768 (151 and 201 MB) 64 / 68;
+// convolution (its forward's loads apart, which neighbours share) 4 x 4096 x 5120 191 / 170.
 template <class IO, int V, bool PAST = false>
 struct Rows {
   using raw = typename Lanes<IO, V>::raw;
@@ -117,10 +117,7 @@ __device__ __forceinline__ Rows<IO, V, PAST> rows_of(const void* base, int64_t f
   return Rows<IO, V, PAST>{make_buf(static_cast<const typename IO::elem*>(base) + first, bytes)};
 }
 
-// Whether a call that moves `bytes` outgrows the Infinity Cache, for its stores; its loads, which
-// may find what an earlier call left there, count as passing it from half as much again (the norm
-// at 4096 x 5120, 335 MB a backward pass: 121 us, 124 with non-temporal loads).
-inline bool stores_pass_cache(int64_t bytes) { return bytes >= (int64_t(256) << 20); }
-inline bool loads_pass_cache(int64_t bytes) { return bytes >= (int64_t(384) << 20); }
+// Whether a call that moves `bytes` outgrows the Infinity Cache.
+inline bool passes_cache(int64_t bytes) { return bytes > (int64_t(256) << 20); }
 
 }  // namespace ss

@@ -165,6 +165,31 @@ def test_two_runs_agree_and_writes_stay_inside():
     assert out.intact() and ws.intact()
 
 
+@pytest.mark.parametrize("io,d,k,silu", [("bf16", 8200, 4, True), ("f32", 4101, 3, False)])
+def test_a_call_that_outgrows_the_cache(io, d, k, silu):
+    """Above 256 MB rows are accessed non-temporally: the call equals its batch rows one by one,
+    which stay below."""
+    o, dt = ops(), torch.bfloat16 if io == "bf16" else torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    r = lambda *s: torch.randn(s, device="cuda", generator=gen)  # noqa: E731
+    x, dout, w, b = r(4, 2100, d).to(dt), r(4, 2100, d).to(dt), r(d, k), r(d)
+    starts = torch.rand((4, 2100), device="cuda", generator=gen) < 0.01
+    moved = x.numel() * x.element_size()
+    assert 2 * moved > 256 << 20 > 3 * moved // 4
+    out = o.causal_conv_fwd(x, w, b, starts=starts, silu=silu)
+    g = o.causal_conv_bwd(x, w, dout, b, starts=starts, silu=silu)
+    dw = torch.zeros_like(w)
+    for k_ in range(4):
+        c = lambda t: t[k_:k_ + 1].contiguous()  # noqa: E731
+        assert torch.equal(out[k_:k_ + 1], o.causal_conv_fwd(c(x), w, b, starts=c(starts),
+                                                             silu=silu))
+        one = o.causal_conv_bwd(c(x), w, c(dout), b, starts=c(starts), silu=silu)
+        assert torch.equal(g["dx"][k_:k_ + 1], one["dx"])
+        dw += one["dweight"]
+    # sums of 8400 products of unit size in another order: 2^-24 a step of at most a few hundred
+    torch.testing.assert_close(g["dweight"], dw, rtol=1e-4, atol=2e-2)
+
+
 def test_empty_sizes():
     o = ops()
     e = lambda *s: torch.empty(s, device="cuda")  # noqa: E731

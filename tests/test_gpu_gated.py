@@ -143,6 +143,34 @@ def test_more_tiles_than_run_at_once():
             assert torch.equal(g[name][b:b + 1], r[name]), name
 
 
+@pytest.mark.parametrize("io,gate", [("bf16", True), ("f32", False)])
+def test_a_call_that_outgrows_the_cache(io, gate):
+    """Above 256 MB rows are accessed non-temporally: the call equals its batch rows one by one,
+    which stay below."""
+    o, dt = ops(), torch.bfloat16 if io == "bf16" else torch.float32
+    shape = (4, 2049, 3402 if gate else 2303)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda: torch.randn(shape, device="cuda", generator=gen).to(dt)  # noqa: E731
+    x, rr, ii, z, dout = r(), r(), r(), r() if gate else None, r()
+    A = -torch.rand(shape[2], device="cuda", generator=gen)
+    starts = torch.rand(shape[:2], device="cuda", generator=gen) < 0.003
+    moved = x.numel() * x.element_size()
+    assert moved * (5 if gate else 4) > 256 << 20 > moved * (9 if gate else 7) // 4
+    out, states, last = o.gated_scan_fwd_states(x, rr, ii, A, z=z, starts=starts,
+                                                return_last_state=True)
+    g = o.gated_scan_bwd(x, rr, ii, A, dout, z=z, starts=starts, states=states)
+    for b in range(4):
+        c = lambda t: None if t is None else t[b:b + 1].contiguous()  # noqa: E731
+        p = o.gated_scan_fwd_states(c(x), c(rr), c(ii), A, z=c(z), starts=c(starts),
+                                    return_last_state=True)
+        q = o.gated_scan_bwd(c(x), c(rr), c(ii), A, c(dout), z=c(z), starts=c(starts),
+                             states=p[1])
+        for whole, alone in zip((out, states, last), p):
+            assert torch.equal(whole[b:b + 1], alone)
+        for name in ("dx", "dr", "di", "dh0") + (("dz",) if gate else ()):
+            assert torch.equal(g[name][b:b + 1], q[name]), name
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("offset", [1, 2, 3])
 def test_arrays_that_start_inside_a_wider_alignment(offset, io):

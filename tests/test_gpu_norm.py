@@ -104,6 +104,26 @@ def test_more_rows_than_workgroups(rows, dim):
     assert torch.equal(dx[tail], alone)
 
 
+@pytest.mark.parametrize("io,dim", [("bf16", 2564), ("f32", 1027), ("bf16", 300)])
+def test_a_call_that_outgrows_the_cache(io, dim):
+    """Above 256 MB rows are read non-temporally: the call equals pieces of it, which stay below."""
+    o, dt = ops(), torch.bfloat16 if io == "bf16" else torch.float32
+    rows = (48 << 20) // dim
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    r = lambda *s: torch.randn(s, device="cuda", generator=gen)  # noqa: E731
+    x, res, w, b, dout = r(rows, dim).to(dt), r(rows, dim), r(dim), r(dim), r(rows, dim).to(dt)
+    out, s, mean, rstd = o.layer_norm_fwd(x, w, b, residual=res, return_stats=True)
+    g = o.layer_norm_bwd(dout, s, w, mean, rstd, dsum=res, want_dresidual=True)
+    for k in range(4):
+        c = slice(k * rows // 4, (k + 1) * rows // 4)
+        p, q, m, t = o.layer_norm_fwd(x[c], w, b, residual=res[c], return_stats=True)
+        assert torch.equal(out[c], p) and torch.equal(s[c], q)
+        assert torch.equal(mean[c], m) and torch.equal(rstd[c], t)
+        h = o.layer_norm_bwd(dout[c], q, w, m, t, dsum=res[c], want_dresidual=True)
+        assert torch.equal(g["dx"][c], h["dx"]) and torch.equal(g["dresidual"][c],
+                                                                h["dresidual"])
+
+
 def test_a_constant_row():
     o = ops()
     x = torch.full((3, 700), 2.5, device="cuda")
