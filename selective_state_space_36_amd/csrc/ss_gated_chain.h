@@ -60,8 +60,9 @@ __device__ __forceinline__ slot_t peek(const slot_t* s) {
   return __hip_atomic_load(s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The chains are dealt to `sets` counters, chain c to counter c mod sets, and so are the
-// workgroups; a set's tiles are numbered segment by segment.  A single counter serves workgroups
+// The chains are dealt to `sets` counters in runs of neighbours, the workgroups in turn (so that the
+// sets are the XCDs' and neighbours, which share cache lines where rows are not whole lines, meet
+// in one L2); a set's tiles are numbered segment by segment.  A single counter serves workgroups
 // that start together one after the other, the last of 512 some 3 us late.
 struct Draw {
   uint32_t pos, chain;  // the tile's place in its chain, and the chain
@@ -71,14 +72,16 @@ struct Draw {
 __device__ __forceinline__ Draw draw_tile(uint32_t* counters, uint32_t* lds, uint32_t chains,
                                           uint32_t segments, uint32_t sets) {
   if (segments == 1) return Draw{0, blockIdx.x, true};
-  const uint32_t set = blockIdx.x % sets;
+  const uint32_t set = sets == 1 ? 0 : blockIdx.x % kMaxSets;
   if (threadIdx.x == 0)
     *lds = __hip_atomic_fetch_add(counters + set * kCounterStep, 1u, __ATOMIC_RELAXED,
                                   __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   const uint32_t tile = __builtin_amdgcn_readfirstlane(*lds);
-  const uint32_t mine = (chains - set + sets - 1) / sets;
-  return Draw{tile / mine, set + sets * (tile % mine), tile < mine * segments};
+  const uint32_t first = set * chains / kMaxSets;  // (several sets: at most 512 chains)
+  const uint32_t mine = sets == 1 ? chains : (set + 1) * chains / kMaxSets - first;
+  if (tile >= mine * segments) return Draw{0, 0, false};
+  return Draw{tile / mine, first + tile % mine, true};
 }
 // Sets and workgroups of a launch: kMaxSets where all tiles start at once (two workgroups per CU;
 // 50.6 against 53.4 us for a training step at 3 x 1111 x 1027), else one, since sets that drift
