@@ -95,8 +95,7 @@ ss_status check_grid(int64_t blocks, int64_t threads) {
 ss_status check_tiles(int64_t batch, int64_t seqlen, int64_t d_inner, int64_t tile,
                       int64_t per_wave) {
   const int64_t waves = seqlen > tile ? tile / per_wave : (seqlen + per_wave - 1) / per_wave;
-  // (rounded up to whole sets of chains)
-  return check_grid((batch * ((d_inner + 63) / 64) + 7) * ((seqlen + tile - 1) / tile),
+  return check_grid(batch * ((d_inner + 63) / 64) * ((seqlen + tile - 1) / tile),
                     64 * (waves > 0 ? waves : 1));
 }
 

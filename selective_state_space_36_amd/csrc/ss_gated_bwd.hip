@@ -28,7 +28,7 @@ constexpr int kWaves = kTile / kSteps;
 template <class IO, bool GATE, bool PAST>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t groups,
-                      int32_t nseg, uint32_t sets) {
+                      int32_t nseg, uint32_t log_sets) {
   using elem = typename IO::elem;
   using R = Rows<IO, 1, PAST>;
   using F = Rows<F32, 1>;
@@ -43,7 +43,7 @@ void gated_bwd_kernel(GatedArgs p, const float* states, float* part, int32_t gro
   const int waves = blockDim.x >> 6;
   const uint32_t chains = static_cast<uint32_t>(p.batch) * groups;
   const Draw drawn_tile =
-      draw_tile(static_cast<uint32_t*>(p.workspace), &drawn, chains, nseg, sets);
+      draw_tile(static_cast<uint32_t*>(p.workspace), &drawn, chains, nseg, log_sets);
   if (!drawn_tile.some) return;
   const uint32_t pos = drawn_tile.pos, chain = drawn_tile.chain;  // pos 0 is the last segment
   const uint32_t seg = nseg - 1 - pos;
@@ -263,15 +263,16 @@ hipError_t launch(const GatedArgs& a, const Layout& l, const float* states, floa
   }
   // a sequence shorter than a tile needs fewer waves
   const int waves = nseg > 1 ? kWaves : static_cast<int>((a.seqlen + kSteps - 1) / kSteps);
-  const ChainGrid cg = chain_grid(a.batch * groups, nseg);
-  const dim3 grid(cg.workgroups), block(64 * waves);
+  const dim3 grid(static_cast<unsigned>(a.batch * groups * nseg)), block(64 * waves);
   const int32_t g = static_cast<int32_t>(groups), n = static_cast<int32_t>(nseg);
-  const int64_t bytes = a.batch * a.seqlen * a.d_inner * sizeof(typename IO::elem);
+  const int64_t row = a.d_inner * sizeof(typename IO::elem);
+  const uint32_t log_sets = chain_log_sets(a.batch * groups, nseg, row);
+  const int64_t bytes = a.batch * a.seqlen * row;
   auto go = [&](auto gate, auto past) {
     hipLaunchKernelGGL((gated_bwd_kernel<IO, gate, past>), grid, block, 0, stream, a, states, part,
-                       g, n, cg.sets);
+                       g, n, log_sets);
   };
-  with_bools(go, a.z != nullptr, passes_cache(bytes * (a.z ? 9 : 7)));
+  with_bools(go, a.z != nullptr, passes_cache(bytes * (a.z ? 9 : 7), row));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t tiles = a.batch * nseg, plane = tiles * a.d_inner;

@@ -39,7 +39,7 @@ using slot_t = unsigned long long;
 // Workspace of a launch: the counters (in the first kChainHead bytes, a cache line each), then the
 // slots [segment][batch row][channel group][64].  All of it is cleared before the launch.
 constexpr int64_t kChainHead = 1024;
-constexpr int kMaxSets = 8, kCounterStep = 32;
+constexpr int kLogSets = 3, kCounterStep = 32;
 inline int64_t chain_bytes(int64_t batch, int64_t segments, int64_t d_inner) {
   if (segments <= 1) return 0;
   return kChainHead + batch * segments * ((d_inner + 63) / 64 * 64) * 8;
@@ -60,41 +60,53 @@ __device__ __forceinline__ slot_t peek(const slot_t* s) {
   return __hip_atomic_load(s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The chains are dealt to `sets` counters in runs of neighbours, the workgroups in turn (so that the
-// sets are the XCDs' and neighbours, which share cache lines where rows are not whole lines, meet
-// in one L2); a set's tiles are numbered segment by segment.  A single counter serves workgroups
-// that start together one after the other, the last of 512 some 3 us late.
+// The chains are dealt to one counter or to eight (sets), in runs of neighbours, and a set's tiles
+// are numbered segment by segment.  Workgroups start at the sets in turn, so that a set is an
+// XCD's and neighbours, which share cache lines where rows are not whole lines, meet in one L2; one
+// whose set has no tile left goes on to the next.  There are as many workgroups as tiles.
 struct Draw {
   uint32_t pos, chain;  // the tile's place in its chain, and the chain
-  bool some;            // false: the set has no tile left for this workgroup
+  bool some;            // false: none was left (the counters were not clear)
 };
+// The chains before set `s`.
+__device__ __forceinline__ uint32_t share(uint32_t chains, uint32_t s, uint32_t log_sets) {
+  return static_cast<uint32_t>(static_cast<uint64_t>(chains) * s >> log_sets);
+}
 // `lds` is written by the first thread and read after a barrier.
 __device__ __forceinline__ Draw draw_tile(uint32_t* counters, uint32_t* lds, uint32_t chains,
-                                          uint32_t segments, uint32_t sets) {
+                                          uint32_t segments, uint32_t log_sets) {
   if (segments == 1) return Draw{0, blockIdx.x, true};
-  const uint32_t set = sets == 1 ? 0 : blockIdx.x % kMaxSets;
-  if (threadIdx.x == 0)
-    *lds = __hip_atomic_fetch_add(counters + set * kCounterStep, 1u, __ATOMIC_RELAXED,
-                                  __HIP_MEMORY_SCOPE_AGENT);
-  __syncthreads();
-  const uint32_t tile = __builtin_amdgcn_readfirstlane(*lds);
-  const uint32_t first = set * chains / kMaxSets;  // (several sets: at most 512 chains)
-  const uint32_t mine = sets == 1 ? chains : (set + 1) * chains / kMaxSets - first;
-  if (tile >= mine * segments) return Draw{0, 0, false};
-  return Draw{tile / mine, first + tile % mine, true};
+  const uint32_t last = (1u << log_sets) - 1;
+  uint32_t set = blockIdx.x & last;
+  for (uint32_t tries = 0;;) {
+    if (threadIdx.x == 0)
+      *lds = __hip_atomic_fetch_add(counters + set * kCounterStep, 1u, __ATOMIC_RELAXED,
+                                    __HIP_MEMORY_SCOPE_AGENT);
+    uint32_t first = 0, mine = chains;
+    if (log_sets) {
+      first = share(chains, set, log_sets);
+      mine = share(chains, set + 1, log_sets) - first;
+    }
+    __syncthreads();
+    const uint32_t tile = __builtin_amdgcn_readfirstlane(*lds);
+    if (__builtin_expect(tile < mine * segments, 1))
+      return Draw{tile / mine, first + tile % mine, true};
+    if (tries++ == last) return Draw{0, 0, false};
+    set = (set + 1) & last;
+    __syncthreads();
+  }
 }
-// Sets and workgroups of a launch: kMaxSets where all tiles start at once (two workgroups per CU;
-// 50.6 against 53.4 us for a training step at 3 x 1111 x 1027), else one, since sets that drift
-// apart take the rows of one step at different times and DRAM pages with them (861 against 716 us
-// at 1 x 262144 x 1536).
-struct ChainGrid {
-  uint32_t sets, workgroups;
-};
-inline ChainGrid chain_grid(int64_t chains, int64_t segments) {
-  if (segments == 1) return ChainGrid{1, static_cast<uint32_t>(chains)};
-  const int64_t sets = chains * segments <= 512 ? kMaxSets : 1;
-  return ChainGrid{static_cast<uint32_t>(sets),
-                   static_cast<uint32_t>((chains + sets - 1) / sets * sets * segments)};
+// Sets of a launch, as a power of two.  Eight where all tiles start at once, two workgroups per CU
+// (a single counter serves them one after the other, the last of 512 some 3 us late), and where
+// chains are short (one / eight, forward: 8 x 2048 x 1536 63.9 / 60.2 us, 4 x 4096 x 5120 186 /
+// 182; training step: 3 x 1111 x 1027 51.4 / 45.5).  In long ones the sets drift apart and take the
+// rows of one step at different times, and DRAM pages with them (1 x 262144 x 1536 695 / 797 us;
+// 2 x 16384 x 1536 float32 172 / 175), which rows that are not whole lines outweigh a little longer
+// (2 x 16384 x 1601 153 / 145, 1 x 65536 x 1537 279 / 297).
+inline uint32_t chain_log_sets(int64_t chains, int64_t segments, int64_t row) {
+  if (chains < 1 << kLogSets) return 0;
+  const int64_t longest = row % 128 == 0 ? 32 : 128;
+  return chains * segments <= 512 || segments <= longest ? kLogSets : 0;
 }
 
 // The state before tile `pos` >= 1 of a chain, for this lane's channel.  `slots` points at the

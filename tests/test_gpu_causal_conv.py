@@ -165,10 +165,11 @@ def test_two_runs_agree_and_writes_stay_inside():
     assert out.intact() and ws.intact()
 
 
-@pytest.mark.parametrize("io,d,k,silu", [("bf16", 8200, 4, True), ("f32", 4101, 3, False)])
+@pytest.mark.parametrize("io,d,k,silu", [("bf16", 8200, 4, True), ("f32", 4101, 3, False),
+                                          ("bf16", 8192, 4, True), ("f32", 4096, 3, False)])
 def test_a_call_that_outgrows_the_cache(io, d, k, silu):
-    """Above 256 MB rows are accessed non-temporally: the call equals its batch rows one by one,
-    which stay below."""
+    """Above 256 MB rows of whole cache lines are accessed non-temporally: the call equals its
+    batch rows one by one, which stay below."""
     o, dt = ops(), torch.bfloat16 if io == "bf16" else torch.float32
     gen = torch.Generator(device="cuda").manual_seed(d)
     r = lambda *s: torch.randn(s, device="cuda", generator=gen)  # noqa: E731

@@ -126,9 +126,11 @@ def test_one_chain_of_many_tiles():
     c.check_bwd(c.check_fwd())
 
 
-def test_more_tiles_than_run_at_once():
-    """A call of 768 (backward 1504) tiles equals its rows one by one, of a quarter as many."""
-    c = Case(16, 4, 3000, 512, "bf16", gate=True, packed=True, h0=True)
+@pytest.mark.parametrize("d", [512, 1090])
+def test_more_tiles_than_run_at_once(d):
+    """A call of 768 (backward 1504) tiles, and one of 1728 in 72 chains, equal their rows one by
+    one, of a quarter as many."""
+    c = Case(16, 4, 3000, d, "bf16", gate=True, packed=True, h0=True)
     out, states, last = c.fwd()
     g = c.bwd(states)
     for b in range(4):
@@ -143,12 +145,13 @@ def test_more_tiles_than_run_at_once():
             assert torch.equal(g[name][b:b + 1], r[name]), name
 
 
-@pytest.mark.parametrize("io,gate", [("bf16", True), ("f32", False)])
-def test_a_call_that_outgrows_the_cache(io, gate):
-    """Above 256 MB rows are accessed non-temporally: the call equals its batch rows one by one,
-    which stay below."""
+@pytest.mark.parametrize("io,gate,d", [("bf16", True, 3402), ("f32", False, 2303),
+                                       ("bf16", True, 3392), ("f32", False, 2304)])
+def test_a_call_that_outgrows_the_cache(io, gate, d):
+    """Above 256 MB rows of whole cache lines are accessed non-temporally: the call equals its
+    batch rows one by one, which stay below."""
     o, dt = ops(), torch.bfloat16 if io == "bf16" else torch.float32
-    shape = (4, 2049, 3402 if gate else 2303)
+    shape = (4, 2049, d)
     gen = torch.Generator(device="cuda").manual_seed(3)
     r = lambda: torch.randn(shape, device="cuda", generator=gen).to(dt)  # noqa: E731
     x, rr, ii, z, dout = r(), r(), r(), r() if gate else None, r()
