@@ -60,7 +60,9 @@ class Case:
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("rows,dim", [(1, 1), (1, 2560), (3, 2), (5, 63), (4, 64), (7, 100),
                                       (2, 768), (33, 130), (9, 1027), (300, 96), (3, 4096),
-                                      (2, 5121), (5, 8200), (2, 20001)])
+                                      (2, 5121), (5, 8200), (2, 20001), (3, 641), (6, 1022),
+                                      (4, 1601), (5, 2049), (600, 3601), (3, 4093), (2, 4098),
+                                      (3, 5126), (3, 8194), (2, 16382), (2, 8193), (2, 16386)])
 def test_forward_and_gradients(rows, dim, residual, io):
     Case(rows * 10 + dim, rows, dim, io, residual).check()
 
@@ -104,9 +106,11 @@ def test_more_rows_than_workgroups(rows, dim):
     assert torch.equal(dx[tail], alone)
 
 
-@pytest.mark.parametrize("io,dim", [("bf16", 2564), ("f32", 1027), ("bf16", 300)])
+@pytest.mark.parametrize("io,dim", [("bf16", 2564), ("f32", 1027), ("bf16", 300),
+                                    ("bf16", 2560), ("f32", 1024)])
 def test_a_call_that_outgrows_the_cache(io, dim):
-    """Above 256 MB rows are read non-temporally: the call equals pieces of it, which stay below."""
+    """Above 256 MB rows of whole cache lines are read non-temporally: the call equals pieces of it,
+    which stay below."""
     o, dt = ops(), torch.bfloat16 if io == "bf16" else torch.float32
     rows = (48 << 20) // dim
     gen = torch.Generator(device="cuda").manual_seed(dim)
