@@ -5,13 +5,14 @@
 // start inside a row, a mask of the starts, the same for the whole wave (a scalar register), says
 // which taps would cross one; steps without a start run without a branch.
 //
-// What bounds it: memory.  4 x 4096 x 5120 bfloat16, four taps: forward 336 MB in 63 us (5.3 TB/s),
-// backward 503 MB in 125 us (4.0 TB/s) and 5 us for the parameters' sums.
-// Why these runs: the forward takes a wave's 16 rows and the 3 before them at once, which neighbours
-// find in the cache (8 rows: 3 us more).  The backward needs 3 rows on either side of its own, so it
-// walks 64 steps with 8 rows in flight (16 to 128 steps and 4 rows: 2 to 20 us more; four channels
-// per lane 10 us more, one 45).  Its branches per step cost 20 us before steps without a start
-// got a path of their own.
+// What bounds it: memory.  4 x 4096 x 5120 bfloat16, four taps: forward 336 MB in 64 us (5.3 TB/s),
+// backward 503 MB in 105 us (4.8 TB/s, the VALU issuing in nine tenths of the cycles: 39 operations
+// per element) and 5 us for the parameters' sums.
+// Why these runs: the forward takes a wave's 16 rows and the 3 before them at once, which
+// neighbours find in the cache (8 rows: 3 us more).  The backward needs 3 rows on either side of
+// its own, so it walks 64 steps with 8 rows in flight (16 to 128 steps and 4 rows: 2 to 20 us more;
+// four channels per lane 10 us more, one 45).  Its branches per step cost 20 us before steps
+// without a start got a path of their own.
 #include "ss_block.h"
 #include "ss_gated_math.h"
 

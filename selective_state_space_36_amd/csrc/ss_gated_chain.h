@@ -2,9 +2,10 @@
 //
 // A workgroup owns one tile: T steps of one batch row and 64 channels, one per lane.  The sequence
 // is a chain of tiles per (batch row, channel group); a tile needs the state at its start, which
-// depends on every tile before it.  Two passes (summaries, then outputs) would read the inputs twice; here
-// each tile is read once: it reduces its steps to a Piece, publishes it, picks up the pieces and
-// end states of the tiles before it, and only then runs its steps, which are still in registers.
+// depends on every tile before it.  Two passes (summaries, then outputs) would read the inputs
+// twice; here each tile is read once: it reduces its steps to a Piece, publishes it, picks up the
+// pieces and end states of the tiles before it, and only then runs its steps, which are still in
+// registers.
 //
 // A slot holds one channel's Piece of one tile in 64 bits: H in the low half, P in the high half
 // with the sign bit set (P is never negative).  An empty slot is 0.  An end state is published

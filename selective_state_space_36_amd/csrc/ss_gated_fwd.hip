@@ -6,16 +6,16 @@
 // to the chain (ss_gated_chain.h), and with the state before its first step every wave runs its
 // steps again from the registers and stores.  Inputs are read once and outputs written once.
 //
-// What bounds it: memory.  1 x 262144 x 1536 bfloat16 without a gate moves 3.2 GB in 710 us
-// (4.5 TB/s; a copy of that size reaches 4.7), 671 us without the wait for the chain; 4 x 4096 x
-// 5120 with a gate 0.84 GB in 190 us (4.4 TB/s), the VALU issuing in three quarters of the cycles
+// What bounds it: memory.  1 x 262144 x 1536 bfloat16 without a gate moves 3.2 GB in 689 us
+// (4.7 TB/s, what a copy of that size reaches); 4 x 4096 x 5120 with a gate 0.84 GB in 182 us
+// (4.6 TB/s), the VALU issuing in four fifths of the cycles
 // (44 operations per element, six of them transcendental).
 // Why this tile: a tile pays for the chain, the parameters and the waves' pieces once, so long ones
-// are better, as far as registers let two workgroups share a CU.  64 steps in four or eight waves
-// took 93 and 85 us at 8 x 2048 x 1536 against 66 (two channels per lane 69), 96 steps 79, 192 in
-// twelve waves 71, 256 in sixteen 67; 32 steps per wave gain 3 % at 1 x 262144 x 1536 and lose 4 %
-// in float32.  Workgroups that stay and draw their next tile early took 780 against 710 us at
-// 1 x 262144 x 1536.
+// are better, as far as registers let two workgroups share a CU.  At 8 x 2048 x 1536, 60 us now, 64
+// steps in four or eight waves took 93 and 85 us when 128 took 66 (with two channels per lane 69),
+// 96 steps 79, 192 in twelve waves 71, 256 in sixteen 67; 32 steps per wave gained 3 % at
+// 1 x 262144 x 1536 and lost 4 % in float32.  Workgroups that stay and draw their next tile early
+// took 780 us there, at 710 without.
 #include "ss_block.h"
 #include "ss_gated_chain.h"
 
@@ -27,7 +27,7 @@ constexpr int kTile = kGatedFwdTile;
 constexpr int kWaves = kTile / kSteps;
 
 // Four waves per SIMD (two workgroups per CU) whatever the registers: told so, the compiler takes
-// up to 128 and keeps more loads in flight (708 against 730 us at 1 x 262144 x 1536).
+// up to 128 and keeps more loads in flight (708 against 730 us at 1 x 262144 x 1536 when tried).
 template <class IO, bool GATE, bool PAST>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void gated_fwd_kernel(GatedArgs p, int32_t groups, int32_t nseg, uint32_t log_sets) {

@@ -6,9 +6,10 @@
 // LDS.  Rows too wide for that (over 16384 columns, or 8192 that are not groups of four) are read
 // again for each pass by the wide kernels.
 //
-// What bounds it: memory.  16384 x 2560 bfloat16 with the residual stream: forward 503 MB in 92 us
-// (5.5 TB/s), backward 671 MB in 130 us and 4 us for the parameters' sums (5.0 TB/s); a copy of
-// 1 GB reaches 5.0 TB/s.  The backward asks for a row's successor before it sums the row.
+// What bounds it: memory.  16384 x 2560 bfloat16 with the residual stream: forward 503 MB in 93 us
+// (5.4 TB/s), backward 671 MB in 105 us and 4 us for the parameters' sums (6.4 TB/s, some of it
+// from the 256 MB cache); a copy of 1 GB reaches 5.0 TB/s.  The backward asks for a row's successor
+// before it sums the row.
 #include "ss_block.h"
 #include "ss_rows.h"
 
