@@ -120,16 +120,22 @@ def test_long_sequence(io):
     c.check_bwd(c.check_fwd())
 
 
+@pytest.mark.parametrize("batch", [8, 11, 15])
+def test_chains_that_the_counters_share_unevenly(batch):
+    c = Case(batch, batch, 700, 40, "bf16", gate=True, packed=True, h0=True)
+    c.check_bwd(c.check_fwd())
+
+
 def test_one_chain_of_many_tiles():
     """A single chain, so that most tiles of it are at work at the same time and look far back."""
     c = Case(7, 1, 40000, 8, "f32", packed=False, h0=True)
     c.check_bwd(c.check_fwd())
 
 
-@pytest.mark.parametrize("d", [512, 1090])
+@pytest.mark.parametrize("d", [512, 1090, 1030])
 def test_more_tiles_than_run_at_once(d):
-    """A call of 768 (backward 1504) tiles, and one of 1728 in 72 chains, equal their rows one by
-    one, of a quarter as many."""
+    """A call of 768 (backward 1504) tiles, one of 1728 in 72 chains and one of 1632 in 68, which
+    eight counters do not share evenly, equal their rows one by one, of a quarter as many."""
     c = Case(16, 4, 3000, d, "bf16", gate=True, packed=True, h0=True)
     out, states, last = c.fwd()
     g = c.bwd(states)
