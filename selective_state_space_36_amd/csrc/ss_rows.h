@@ -22,7 +22,10 @@ struct Lanes<BF16, 2> {
     return __uint_as_float(v ? r & 0xffff0000u : r << 16);
   }
   static __device__ __forceinline__ raw put(const float* f) {
-    return BF16::from_float(f[0]) | static_cast<uint32_t>(BF16::from_float(f[1])) << 16;
+    // (one conversion of both: rounded apart they are shifted and joined by three more instructions)
+    using f2 = __attribute__((ext_vector_type(2))) float;
+    using b2 = __attribute__((ext_vector_type(2))) __bf16;
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2{f[0], f[1]}), b2));
   }
 };
 template <>
