@@ -253,7 +253,8 @@ __global__ __launch_bounds__(64 * kWaves) void conv_bwd_kernel(ConvArgs p, uint3
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const float sg = sigmoid_f(pre[v]);
-            g[v] *= sg * fmaf(pre[v], 1.0f - sg, 1.0f);
+            // silu' = sg (1 + pre (1 - sg))
+            g[v] *= fmaf(sg, fmaf(-pre[v], sg, pre[v]), sg);
           }
         }
         if (!kPlain && s >= have) {  // past the end: no gradient, whatever silu' gave
