@@ -183,3 +183,89 @@ def test_empty_sizes():
     g = o.layer_norm_bwd(e, e, None, mean, rstd)
     assert not g["dweight"].any() and not g["dbias"].any() and g["dx"].shape == (0, 16)
     assert o.layer_norm_fwd(torch.empty(3, 0, device="cuda")).shape == (3, 0)
+
+
+# Whole numbers whose sums stay below 2^24: float32 holds every sum over rows and columns exactly,
+# in whatever order it is formed.
+def whole(rows, dim, seed):
+    """dout, s, weight, mean, rstd, dsum on the GPU, in float32."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, device="cuda",  # noqa: E731
+                                         generator=g).float()
+    return (n(-2, 2, rows, dim), n(-4, 4, rows, dim), n(1, 2, dim), n(-1, 1, rows),
+            2.0 ** n(-1, 0, rows), n(-9, 9, rows, dim))
+
+
+def gradients64(dout, s, weight, mean, rstd, dsum):
+    """ds with a bound on its float32 error, dweight and dbias, in float64."""
+    dy, w, rs = dout.double(), weight.double(), rstd.double()[:, None]
+    xh = (s.double() - mean.double()[:, None]) * rs
+    g = dy * w
+    c1, c2 = g.mean(1, keepdim=True), (g * xh).mean(1, keepdim=True)
+    ds = rs * (g - c1 - xh * c2) + dsum.double()
+    # The sums are exact; 1 / dim and its products with them round (2 U of c1 and c2), then
+    # g - c1, the multiply-add with xh c2, and the last one with rstd and dsum.
+    terms = rs * (g.abs() + c1.abs() + (xh * c2).abs())
+    return ds, 2.0 ** -24 * (5 * terms + ds.abs()), (dy * xh).sum(0), dy.sum(0)
+
+
+# Rows enough for every workgroup (512 of them, of one row or of four) to take several: groups of
+# four columns with 64, 256 and 1024 threads a row, single columns likewise, and the wide rows,
+# whose parameter sums 64 strands share.
+@pytest.mark.parametrize("io,sdt", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,dim", [(5003, 1000), (1501, 1540), (1501, 2560), (1030, 4096),
+                                      (1100, 5120), (1030, 12288), (1030, 16384), (5003, 333),
+                                      (1501, 2561), (1501, 3601), (1030, 4099), (1030, 8191),
+                                      (300, 8193), (200, 20000), (67, 20001)])
+def test_gradients_where_workgroups_take_many_rows(rows, dim, io, sdt):
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}
+    dout, s, w, mean, rstd, dsum = whole(rows, dim, rows + dim)
+    g = ops().layer_norm_bwd(dout.to(dt[io]), s.to(dt[sdt]), w, mean, rstd, dsum=dsum,
+                             want_dresidual=True)
+    ds, e, dw, db = gradients64(dout, s, w, mean, rstd, dsum)
+    assert torch.equal(g["dweight"].double(), dw)
+    assert torch.equal(g["dbias"].double(), db)
+    assert ((g["dresidual"].double() - ds).abs() <= e).all()
+    half = 2.0 ** -8 if io == "bf16" else 0.0
+    assert ((g["dx"].double() - ds).abs() <= e + half * (ds.abs() + e)).all()
+
+
+@pytest.mark.parametrize("io,dim", [("bf16", 2560), ("f32", 1024), ("bf16", 300), ("f32", 1027)])
+def test_parameter_sums_of_a_call_that_outgrows_the_cache(io, dim):
+    rows = (48 << 20) // dim
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    dout, s, w, mean, rstd, dsum = whole(rows, dim, dim)
+    g = ops().layer_norm_bwd(dout.to(dt), s, w, mean, rstd, dsum=dsum)
+    dw, db = torch.zeros_like(w, dtype=torch.float64), torch.zeros_like(w, dtype=torch.float64)
+    for k in range(4):
+        c = slice(k * rows // 4, (k + 1) * rows // 4)
+        ds, e, pw, pb = gradients64(dout[c], s[c], w, mean[c], rstd[c], dsum[c])
+        half = 2.0 ** -8 if io == "bf16" else 0.0
+        assert ((g["dx"][c].double() - ds).abs() <= e + half * (ds.abs() + e)).all()
+        dw += pw
+        db += pb
+    assert torch.equal(g["dweight"].double(), dw) and torch.equal(g["dbias"].double(), db)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim", [(777, 515), (5, 4099), (3, 2), (2, 20001), (9, 260)])
+def test_gradients_stay_inside_their_arrays(rows, dim, io):
+    """Every array that the backward writes, between marker bytes."""
+    o = ops()
+    c = Case(rows + dim, rows, dim, io, True)
+    _, s, mean, rstd = o.layer_norm_fwd(c.x, c.w, c.b, residual=c.res, return_stats=True)
+    want = o.layer_norm_bwd(c.dout, s, c.w, mean, rstd, dsum=c.dsum, want_dresidual=True)
+    g = dict(dx=Guarded((rows, dim), c.x.dtype), dresidual=Guarded((rows, dim), torch.float32),
+             dweight=Guarded((dim,), torch.float32), dbias=Guarded((dim,), torch.float32))
+    n = o.lib().ss_layer_norm_bwd_workspace_bytes(rows, dim)
+    ws = Guarded((n,), torch.uint8)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    o._check(o.lib().ss_layer_norm_bwd(
+        p(c.dout), p(s), o.SS_F32, p(c.w), p(mean), p(rstd), p(c.dsum),
+        *(p(g[k].t) for k in ("dx", "dresidual", "dweight", "dbias")), rows, dim,
+        o.SS_BF16 if io == "bf16" else o.SS_F32, p(ws.t), n,
+        torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    for k, buf in g.items():
+        assert torch.equal(buf.t, want[k]) and buf.intact(), k
+    assert ws.intact()
