@@ -202,3 +202,80 @@ def test_empty_sizes():
     with pytest.raises(o.SSError) as err:
         o.causal_conv_fwd(e(1, 2, 8), torch.randn(8, 5, device="cuda"))
     assert err.value.status == o.SS_ERR_UNSUPPORTED
+
+
+# The backward's waves walk 64 steps where that leaves 1024 of them (sequences in runs of 64, times
+# groups of 128 channels), else 16.
+def walks_64(batch, L, d):
+    return batch * -(-L // 64) * -(-d // 128) >= 1024
+
+
+@pytest.mark.parametrize("batch,L,d,k", [(350, 130, 6, 4), (350, 129, 5, 3), (520, 127, 3, 2),
+                                         (520, 66, 4, 4), (260, 200, 2, 1), (120, 191, 257, 4)])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_long_runs_without_silu_are_exact(batch, L, d, k, io):
+    """Small whole numbers: every product and sum is exact in float32, so each gradient equals the
+    definition's, whatever the runs, the starts among them and the windows between."""
+    assert walks_64(batch, L, d)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    gen = torch.Generator().manual_seed(L * d + k)
+    n = lambda *s: torch.randint(-3, 4, s, generator=gen).double()  # noqa: E731
+    x, dout, w, xp = n(batch, L, d), n(batch, L, d), n(d, k), n(batch, k - 1, d)
+    starts = torch.rand((batch, L), generator=gen) < 0.05
+    up = lambda t, as_=dt: t.to(as_).cuda()  # noqa: E731
+    g = ops().causal_conv_bwd(up(x), up(w, torch.float32), up(dout), x_prev=up(xp),
+                              starts=starts.cuda(), silu=False)
+    seq = torch.cumsum(starts.int(), 1)
+    whole = torch.cat([xp, x], 1)
+    dpad, dw = torch.zeros_like(whole), []
+    for j in range(k):
+        lag = k - 1 - j
+        then = torch.cat([torch.zeros(batch, lag, dtype=seq.dtype), seq[:, :L - lag]], 1)
+        m = (then == seq)[..., None] * dout
+        dpad[:, j:j + L] += m * w[:, j]
+        dw.append((m * whole[:, j:j + L]).sum((0, 1)))
+    # (gradients of bfloat16 inputs are sums of at most four products below 9: no rounding)
+    assert torch.equal(g["dx"].double().cpu(), dpad[:, k - 1:])
+    assert torch.equal(g["dx_prev"].double().cpu(), dpad[:, :k - 1])
+    assert torch.equal(g["dweight"].double().cpu(), torch.stack(dw, 1))
+    assert torch.equal(g["dbias"].double().cpu(), dout.sum((0, 1)))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,L,d,k", [(350, 130, 6, 4), (345, 131, 5, 3)])
+def test_long_runs(batch, L, d, k, io):
+    assert walks_64(batch, L, d)
+    run_case(L, batch, L, d, k, io, packed=True, prev=True)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,L,d,k", [(2, 77, 65, 4), (1, 130, 30, 3), (2, 2, 9, 4),
+                                         (350, 130, 7, 2), (3, 5, 128, 1)])
+def test_gradients_stay_inside_their_arrays(batch, L, d, k, io):
+    """Every array that the backward writes, between marker bytes; and the one-token form's."""
+    rng = np.random.default_rng(L + d)
+    n = lambda *s: gpu(rng.standard_normal(s), io)[0]  # noqa: E731
+    x, dout, xp, o = n(batch, L, d), n(batch, L, d), n(batch, k - 1, d), ops()
+    w, b = gpu(rng.standard_normal((d, k)))[0], gpu(rng.standard_normal(d))[0]
+    s = starts_gpu(draw_starts(rng, batch, L, 7))
+    want = o.causal_conv_bwd(x, w, dout, b, x_prev=xp, starts=s)
+    g = dict(dx=Guarded((batch, L, d), x.dtype), dweight=Guarded((d, k), torch.float32),
+             dbias=Guarded((d,), torch.float32), dx_prev=Guarded((batch, k - 1, d), x.dtype))
+    code = o.SS_BF16 if io == "bf16" else o.SS_F32
+    size = o.lib().ss_causal_conv_bwd_workspace_bytes(batch, L, d, k, code)
+    ws = Guarded((size,), torch.uint8)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    o._check(o.lib().ss_causal_conv_bwd(
+        p(x), p(w), p(b), p(xp) or None, p(s), 1, p(dout),
+        *(p(g[m].t) for m in ("dx", "dweight", "dbias", "dx_prev")), batch, L, d, k, code,
+        p(ws.t), size, torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    for m, buf in g.items():
+        assert torch.equal(buf.t, want[m]) and buf.intact(), m
+    assert ws.intact()
+    state, out = Guarded((batch, k - 1, d), x.dtype), Guarded((batch, d), x.dtype)
+    state.t.copy_(xp)
+    ref = o.causal_conv_update(xp, x[:, 0].contiguous(), w, b)
+    o.causal_conv_update(state.t, x[:, 0].contiguous(), w, b, out=out.t)
+    assert torch.equal(out.t, ref) and torch.equal(state.t, xp)
+    assert out.intact() and state.intact()
