@@ -386,3 +386,80 @@ def test_empty_sizes():
     assert not g["dA"].any() and g["dh0"].shape == (0, 8)
     assert o.gated_scan_fwd(e(1, 4, 0), e(1, 4, 0), e(1, 4, 0), e(0)).shape == (1, 4, 0)
     assert o.gated_state_update(e(0, 8), e(0, 8), e(0, 8), e(0, 8), A).shape == (0, 8)
+
+
+@pytest.mark.parametrize("lo,hi", [(37, 200), (64, 65), (130, 256), (0, 63)])
+@pytest.mark.parametrize("L", [100, 700])
+def test_a_channel_range_comes_out_the_same_alone(lo, hi, L):
+    """Also one that begins inside a group of 64 channels, and one that ends in another."""
+    c = Case(17, 3, L, 256, "bf16", gate=True, packed=True, h0=True)
+    whole = (*c.fwd(), c.bwd(None))
+    part = {k: t if t is None or k == "starts" else t[..., lo:hi].contiguous()
+            for k, t in c.g.items()}
+    alone = ops().gated_scan_fwd_states(*c.args(part), **c.kw(part), return_last_state=True)
+    g = ops().gated_scan_bwd(*c.args(part), part["dout"], **c.kw(part), dh_last=part["dh_last"])
+    for p, q in zip(whole, alone):
+        assert torch.equal(p[..., lo:hi], q)
+    for name in g:
+        assert torch.equal(whole[3][name][..., lo:hi], g[name]), name
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("batch,L,d", [(2, 77, 65), (1, 130, 30), (2, 5, 200), (1, 1, 1),
+                                       (3, 300, 129)])
+def test_gradients_stay_inside_their_arrays(batch, L, d, given, io):
+    """Every array that the backward writes, between marker bytes; and the one-token form's."""
+    o = ops()
+    c = Case(18, batch, L, d, io, gate=True, packed=True, h0=True)
+    states = c.fwd()[1] if given else None
+    want, v = c.bwd(states), c.g
+    dt, f32 = v["x"].dtype, torch.float32
+    g = {k: Guarded((batch, L, d), dt) for k in ("dx", "dr", "di", "dz")}
+    g.update({k: Guarded((d,), f32) for k in ("dA", "dr_bias", "di_bias")},
+             dh0=Guarded((batch, d), f32))
+    code = o.SS_BF16 if io == "bf16" else o.SS_F32
+    n = o.lib().ss_gated_scan_bwd_workspace_bytes(batch, L, d, code, given)
+    ws = Guarded((n,), torch.uint8)
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    o._check(o.lib().ss_gated_scan_bwd(
+        *(p(v[k]) for k in ("x", "r", "i", "A", "r_bias", "i_bias", "z", "starts", "h0", "dout",
+                            "dh_last")), p(states),
+        *(p(g[k].t) for k in ("dx", "dr", "di", "dz", "dA", "dr_bias", "di_bias", "dh0")),
+        batch, L, d, code, p(ws.t), n, torch.cuda.current_stream().cuda_stream))
+    torch.cuda.synchronize()
+    for k, buf in g.items():
+        assert torch.equal(buf.t, want[k]) and buf.intact(), k
+    assert ws.intact()
+    tok = {k: v[k][:, 0].contiguous() for k in ("x", "r", "i", "z")}
+    state, out = Guarded((batch, d), f32), Guarded((batch, d), dt)
+    state.t.copy_(v["h0"])
+    h = v["h0"].clone()
+    rest = (tok["x"], tok["r"], tok["i"], v["A"], v["r_bias"], v["i_bias"], tok["z"])
+    ref = o.gated_state_update(h, *rest)
+    o.gated_state_update(state.t, *rest, out=out.t)
+    assert torch.equal(out.t, ref) and torch.equal(state.t, h)
+    assert out.intact() and state.intact()
+
+
+@pytest.mark.parametrize("A,r", [(0.0, 0.0), (-1e-30, 0.0), (-1e-4, 3.0), (-40.0, 5.0),
+                                 (-200.0, 9.0), (-1.0, -200.0), (-1.0, 200.0), (-0.5, -15.0),
+                                 (-0.01, -84.0), (-0.5, -87.0), (-0.01, -88.0)])
+def test_parameter_gradients_of_extreme_gates(A, r):
+    rng = np.random.default_rng(10)
+    L, d = 150, 66
+    x, i, dout = (rng.standard_normal((2, L, d)) for _ in range(3))
+    rr = np.full((2, L, d), r) + 1e-3 * rng.standard_normal((2, L, d))
+    gs, vs = zip(*(gpu(a) for a in (x, rr, i, np.full(d, A), dout, rng.standard_normal((2, d)))))
+    g = ops().gated_scan_bwd(*gs[:4], gs[4], h0=gs[5])
+    want = bt.gated_bwd(*vs[:4], vs[4], h0=vs[5])
+    check(g["di_bias"], want["di_bias"], "f32", "di_bias", SPLIT)
+    for name in ("dA", "dr_bias"):
+        if r > -80.0:
+            check(g[name], want[name], "f32", name, SPLIT)
+            continue
+        # 1 - a^2 = 2 |A| rg nears or passes the smallest normal number, and its reciprocal root
+        # has no useful bound; but a token adds lam (a h rg - ig x a^2 rg / s) with
+        # rg / s = (rg / 2 |A|)^(1/2) < 4.1e-18, or without the second term, where |lam| < 2 L 5,
+        # |x| and |h| < 5 and rg < 4e-37: 2 L tokens of 2 L 25 4.1e-18 are below 1e-11.
+        assert abs(want[name].v).max() < 1e-11 and (g[name].abs() < 1e-11).all(), name
