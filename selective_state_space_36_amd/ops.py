@@ -679,7 +679,7 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, return_su
     x: (..., dim) float32 or bfloat16; residual: the same shape, float32 (the residual stream);
     weight, bias: (dim,) float32.  Returns out alone, or a tuple of out, then the float32 sum
     x + residual (return_sum: by default with a residual), then mean and rstd, (...) float32, with
-    return_stats (layer_norm_bwd takes them)."""
+    return_stats (layer_norm_bwd takes them; NaN, being 0 / 0, where dim is 0)."""
     if _elsewhere(x, stream):
         return _moved(layer_norm_fwd, x, stream, (x,),
                       dict(weight=weight, bias=bias, residual=residual, eps=eps,
@@ -705,6 +705,9 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, return_su
     if return_stats:
         mean = torch.empty(shape[:-1], dtype=f32, device=dev)
         rstd = torch.empty_like(mean)
+        if not dim:  # the library writes nothing then
+            mean.fill_(float("nan"))
+            rstd.fill_(float("nan"))
     _check(lib().ss_layer_norm_fwd(
         x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias), eps, out.data_ptr(),
         _ptr(sum_out), _ptr(mean), _ptr(rstd), rows, dim, code, _raw_stream(x.device)))

@@ -269,3 +269,13 @@ def test_gradients_stay_inside_their_arrays(rows, dim, io):
     for k, buf in g.items():
         assert torch.equal(buf.t, want[k]) and buf.intact(), k
     assert ws.intact()
+
+
+@pytest.mark.parametrize("shape", [(3, 0), (0,), (2, 5, 0)])
+def test_statistics_of_no_columns_are_nan(shape):
+    """They are allocated by the call: not what the memory held before."""
+    held = [torch.full((10,), 7.0, device="cuda") for _ in range(4)]
+    del held
+    out, mean, rstd = ops().layer_norm_fwd(torch.empty(shape, device="cuda"), return_stats=True)
+    assert out.shape == shape and mean.shape == rstd.shape == shape[:-1]
+    assert torch.isnan(mean).all() and torch.isnan(rstd).all()
