@@ -401,20 +401,25 @@ void bwd(const NormArgs& a, float* part, int64_t* lines, hipStream_t stream) {
 }
 
 // Calls f with the instance's V, TPR and K: groups of four columns (V = 4) in up to four rounds,
-// single columns (V = 1) in up to sixteen.
+// single columns (V = 1) in up to sixteen.  More than 64 threads take a row only when it has more
+// columns than a quarter as many hold, so the fewest rounds are for 64 alone.
 template <int V, int TPR, class F>
 void with_rounds(int64_t dim, F f) {
   const int64_t k = (dim + TPR * V - 1) / (TPR * V);
   using std::integral_constant;
   auto go = [&](auto kk) { f(integral_constant<int, V>{}, integral_constant<int, TPR>{}, kk); };
   if constexpr (V == 4) {
-    if (k <= 1) go(integral_constant<int, 1>{});
-    else if (k <= 2) go(integral_constant<int, 2>{});
+    if constexpr (TPR == 64) {
+      if (k <= 1) return go(integral_constant<int, 1>{});
+    }
+    if (k <= 2) go(integral_constant<int, 2>{});
     else if (k <= 3) go(integral_constant<int, 3>{});
     else go(integral_constant<int, 4>{});
   } else {
-    if (k <= 2) go(integral_constant<int, 2>{});
-    else if (k <= 5) go(integral_constant<int, 5>{});
+    if constexpr (TPR == 64) {
+      if (k <= 2) return go(integral_constant<int, 2>{});
+    }
+    if (k <= 5) go(integral_constant<int, 5>{});
     else if constexpr (TPR == 1024) go(integral_constant<int, 8>{});
     else if (k <= 8) go(integral_constant<int, 8>{});
     else if (k <= 12) go(integral_constant<int, 12>{});
