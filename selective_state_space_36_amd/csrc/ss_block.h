@@ -44,9 +44,8 @@ struct GatedArgs {
 // Steps of a wave, and of a workgroup's tile, of the forward; steps of a wave of the backward,
 // whose tile is SS_GATED_CHUNK.
 constexpr int kGatedFwdSteps = 16, kGatedFwdTile = 128, kGatedBwdSteps = 8;
-size_t gated_fwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool bf16);
-size_t gated_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool bf16,
-                          bool states_given);
+size_t gated_fwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner);
+size_t gated_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool states_given);
 hipError_t launch_gated_fwd(const GatedArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_gated_bwd(const GatedArgs& a, bool bf16, hipStream_t stream);
 
@@ -110,7 +109,7 @@ struct ConvArgs {
   int32_t k;
   int32_t silu;
 };
-size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int32_t k, bool bf16);
+size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int32_t k);
 hipError_t launch_conv_fwd(const ConvArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_conv_step(const ConvArgs& a, bool bf16, hipStream_t stream);

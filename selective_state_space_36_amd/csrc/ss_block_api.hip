@@ -105,10 +105,12 @@ int64_t chunks_of(int64_t seqlen) { return (seqlen + SS_GATED_CHUNK - 1) / SS_GA
 
 extern "C" {
 
+// (The workspaces hold float32 sums and states only: their sizes do not depend on the io dtype that
+// the queries take, as the scan's do.)
 size_t ss_gated_scan_fwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner,
-                                         ss_dtype dtype) {
+                                         ss_dtype) {
   if (!sizes_ok(batch, seqlen, d_inner)) return 0;
-  return ss::gated_fwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16);
+  return ss::gated_fwd_ws_bytes(batch, seqlen, d_inner);
 }
 
 size_t ss_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t d_inner) {
@@ -137,7 +139,7 @@ ss_status ss_gated_scan_fwd(const void* x, const void* r, const void* i, const f
   }
   if ((s = check_tiles(batch, seqlen, d_inner, ss::kGatedFwdTile, ss::kGatedFwdSteps)) != SS_OK)
     return s;
-  const size_t need = ss::gated_fwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16);
+  const size_t need = ss::gated_fwd_ws_bytes(batch, seqlen, d_inner);
   const Arr in[] = {{"x", x, n, es, true}, {"r", r, n, es, true}, {"i", i, n, es, true},
                     {"A", A, d_inner, 4, true}, {"r_bias", r_bias, d_inner, 4, false},
                     {"i_bias", i_bias, d_inner, 4, false}, {"z", z, n, es, false},
@@ -159,9 +161,9 @@ ss_status ss_gated_scan_fwd(const void* x, const void* r, const void* i, const f
 }
 
 size_t ss_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner,
-                                         ss_dtype dtype, int states_given) {
+                                         ss_dtype, int states_given) {
   if (!sizes_ok(batch, seqlen, d_inner)) return 0;
-  return ss::gated_bwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16, states_given != 0);
+  return ss::gated_bwd_ws_bytes(batch, seqlen, d_inner, states_given != 0);
 }
 
 ss_status ss_gated_scan_bwd(const void* x, const void* r, const void* i, const float* A,
@@ -181,9 +183,8 @@ ss_status ss_gated_scan_bwd(const void* x, const void* r, const void* i, const f
     return s;
   const int64_t rows = batch * d_inner;
   const bool some = n > 0;
-  const size_t need = some ? ss::gated_bwd_ws_bytes(batch, seqlen, d_inner, dtype == SS_BF16,
-                                                    states != nullptr)
-                           : 0;
+  const size_t need =
+      some ? ss::gated_bwd_ws_bytes(batch, seqlen, d_inner, states != nullptr) : 0;
   const Arr in[] = {{"x", x, n, es, some}, {"r", r, n, es, some}, {"i", i, n, es, some},
                     {"A", A, d_inner, 4, true}, {"r_bias", r_bias, d_inner, 4, false},
                     {"i_bias", i_bias, d_inner, 4, false}, {"z", z, n, es, false},
@@ -363,9 +364,9 @@ ss_status ss_causal_conv_fwd(const void* x, const float* weight, const float* bi
 }
 
 size_t ss_causal_conv_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t d_inner,
-                                          int32_t k, ss_dtype dtype) {
+                                          int32_t k, ss_dtype) {
   if (!sizes_ok(batch, seqlen, d_inner) || k < 1 || k > 4) return 0;
-  return ss::conv_bwd_ws_bytes(batch, seqlen, d_inner, k, dtype == SS_BF16);
+  return ss::conv_bwd_ws_bytes(batch, seqlen, d_inner, k);
 }
 
 ss_status ss_causal_conv_bwd(const void* x, const float* weight, const float* bias,
@@ -385,8 +386,7 @@ ss_status ss_causal_conv_bwd(const void* x, const float* weight, const float* bi
   const int64_t prev = batch * (k - 1) * d_inner;
   if (dx_prev && !x_prev && prev > 0)
     return fail(SS_ERR_INVALID_ARG, "dx_prev is given without x_prev");
-  const size_t need =
-      some ? ss::conv_bwd_ws_bytes(batch, seqlen, d_inner, k, dtype == SS_BF16) : 0;
+  const size_t need = some ? ss::conv_bwd_ws_bytes(batch, seqlen, d_inner, k) : 0;
   const Arr in[] = {{"x", x, n, es, some}, {"weight", weight, d_inner * k, 4, true},
                     {"bias", bias, d_inner, 4, false}, {"x_prev", x_prev, prev, es, false},
                     {"starts", starts, batch * seqlen, 1, false}, {"dout", dout, n, es, some}};

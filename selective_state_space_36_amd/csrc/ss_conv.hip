@@ -445,7 +445,7 @@ bool lanes_of(const ConvArgs& a, int v) {
 
 }  // namespace
 
-size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int32_t k, bool) {
+size_t conv_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, int32_t k) {
   const int64_t lines = lines_of(batch, seqlen, bwd_steps(batch, seqlen, d_inner));
   return static_cast<size_t>(lines * (k + 1) * d_inner) * sizeof(float);
 }

@@ -238,13 +238,13 @@ int64_t segments_of(int64_t seqlen) { return (seqlen + kTile - 1) / kTile; }
 struct Layout {
   int64_t chain, part, states, total;  // bytes of the chain to clear; byte offsets
 };
-Layout layout(int64_t batch, int64_t seqlen, int64_t d_inner, bool bf16, bool given) {
+Layout layout(int64_t batch, int64_t seqlen, int64_t d_inner, bool given) {
   const int64_t nseg = segments_of(seqlen);
   Layout l;
   l.chain = chain_bytes(batch, nseg, d_inner);
   int64_t head = l.chain;
   if (!given) {
-    const int64_t f = static_cast<int64_t>(gated_fwd_ws_bytes(batch, seqlen, d_inner, bf16));
+    const int64_t f = static_cast<int64_t>(gated_fwd_ws_bytes(batch, seqlen, d_inner));
     head = head > f ? head : f;
   }
   l.part = (head + 255) / 256 * 256;
@@ -287,13 +287,13 @@ hipError_t launch(const GatedArgs& a, const Layout& l, const float* states, floa
 
 }  // namespace
 
-size_t gated_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool bf16, bool given) {
-  return static_cast<size_t>(layout(batch, seqlen, d_inner, bf16, given).total);
+size_t gated_bwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool given) {
+  return static_cast<size_t>(layout(batch, seqlen, d_inner, given).total);
 }
 
 hipError_t launch_gated_bwd(const GatedArgs& a, bool bf16, hipStream_t stream) {
   char* ws = static_cast<char*>(a.workspace);
-  const Layout l = layout(a.batch, a.seqlen, a.d_inner, bf16, a.states != nullptr);
+  const Layout l = layout(a.batch, a.seqlen, a.d_inner, a.states != nullptr);
   const float* states = a.states;
   float* part = reinterpret_cast<float*>(ws + l.part);
   if (!states) {

@@ -195,7 +195,7 @@ hipError_t launch(const GatedArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-size_t gated_fwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner, bool) {
+size_t gated_fwd_ws_bytes(int64_t batch, int64_t seqlen, int64_t d_inner) {
   return static_cast<size_t>(chain_bytes(batch, segments_of(seqlen), d_inner));
 }
 

@@ -39,17 +39,6 @@ struct Lanes<BF16, 4> {
   }
 };
 template <>
-struct Lanes<BF16, 8> {
-  using raw = uint4;
-  static __device__ __forceinline__ float get(raw r, int v) {
-    return Lanes<BF16, 2>::get(v < 2 ? r.x : v < 4 ? r.y : v < 6 ? r.z : r.w, v & 1);
-  }
-  static __device__ __forceinline__ raw put(const float* f) {
-    return uint4{Lanes<BF16, 2>::put(f), Lanes<BF16, 2>::put(f + 2), Lanes<BF16, 2>::put(f + 4),
-                 Lanes<BF16, 2>::put(f + 6)};
-  }
-};
-template <>
 struct Lanes<F32, 1> {
   using raw = float;
   static __device__ __forceinline__ float get(raw r, int) { return r; }
