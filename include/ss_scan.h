@@ -358,8 +358,10 @@ ss_status ss_state_update_conv(float* state, void* conv_state, const void* x,
  *   workspace        : ss_gated_scan_fwd_workspace_bytes() bytes, 16-byte aligned; may be NULL
  *                      when that is 0.  Its contents need no preparation and mean nothing after
  *                      the call; calls that may run at the same time need one each.
- * 1 - a^2 is formed without cancellation (as -expm1(2 A rg)).  Results do not depend on how the
- * sequence is cut over workgroups, and two runs agree bit for bit.
+ * 1 - a^2 is formed without cancellation (as -expm1(2 A rg)).  Results do not depend on timing or
+ * on the order in which workgroups run: two runs agree bit for bit.  They do depend, by rounding,
+ * on where a step lies in its row: a sequence behind a start and the same one in a call of its own
+ * agree to a few float32 roundings per step.
  * Outputs must not overlap the inputs, each other or the workspace (SS_ERR_INVALID_ARG); d_inner
  * above 2^24 or seqlen above 2^31 - 1 -> SS_ERR_UNSUPPORTED.  Empty sizes are a no-op (with
  * seqlen == 0, h_last receives h0, or zeros).
@@ -386,7 +388,8 @@ size_t ss_gated_scan_states_bytes(int64_t batch, int64_t seqlen, int64_t d_inner
  * passes no gradient.
  *   states            : what ss_gated_scan_fwd saved for the same inputs, or NULL: the states
  *                       are then recomputed by a pass of its own (into the workspace).
- *   dx, dr, di        : (batch, seqlen, d_inner) io dtype, required; dz likewise with z.
+ *   dx, dr, di        : (batch, seqlen, d_inner) io dtype, required; dz likewise with z (without
+ *                       z it is not written).
  *   dA                : (d_inner) float32, required.  dr_bias, di_bias: (d_inner) float32, NULL:
  *                       not written.  Sums over batch rows and steps, in a fixed order: two runs
  *                       agree bit for bit.  Zeros when there are no tokens.
