@@ -3,8 +3,8 @@
 // A row lies in the registers of TPR threads (64, 256 or 1024), K groups of V consecutive columns
 // each, so it is read once: the mean, then the squared differences from it, then the output all
 // come from the same registers.  Sums run over the lanes of a wave by DPP, over the waves through
-// LDS.  Rows too wide for that (over 16384 columns, or 8192 that are not groups of four) are read
-// again for each pass by the wide kernels.
+// LDS.  Rows too wide for that (over 16384 columns, 12288 in the backward, or 8192 that are not
+// groups of four) are read again for each pass by the wide kernels.
 //
 // What bounds it: memory.  16384 x 2560 bfloat16 with the residual stream: forward 503 MB in 93 us
 // (5.4 TB/s), backward 671 MB in 105 us and 4 us for the parameters' sums (6.4 TB/s, some of it
@@ -346,8 +346,21 @@ __global__ __launch_bounds__(256) void norm_param_wide_kernel(NormArgs p, float*
 // Threads per row: the fewest that hold it in registers, 0 for a wide row.  (At most 8 single
 // columns per thread, so more threads, took 342 against 244 us for a training step at 16384 x 2561,
 // 162 against 95 at 8000 x 2049; 226 against 198 at 8000 x 4093, float32 239 against 248.)
-int threads_per_row(int64_t dim, bool quads) {
-  return dim <= 64 * 16 ? 64 : dim <= 256 * 16 ? 256 : dim <= 1024 * (quads ? 16 : 8) ? 1024 : 0;
+//
+// 1024 threads have 128 registers each and hold up to `rounds` groups of four columns, or 8 single
+// ones, per thread.  Measured in registers / by the wide kernels, us, bfloat16 with a residual and
+// float32 without: forward 4096 x 16384 154 / 403 and 104 / 221, singles 4096 x 8191 97 / 204 and
+// 4096 x 4101 58 / 97 and 29 / 47.  The backward keeps nine values per column.  In a third round it
+// spills 8 to 21 registers, which still pays (4096 x 8196 153 / 203, 4096 x 12288 192 / 270 and
+// 164 / 255; not where everything lies in the cache, 512 x 12288 58 / 35); in a fourth 50 to 62,
+// which does not (4096 x 12292 409 / 284, 4096 x 16384 442 / 346 and 445 / 327, 512 x 12292 86 /
+// 37).
+constexpr int kRoundsFwd = 4, kRoundsBwd = 3;
+int threads_per_row(int64_t dim, bool quads, int rounds) {
+  return dim <= 64 * 16 ? 64
+         : dim <= 256 * 16 ? 256
+         : dim <= 1024 * (quads ? 4 * rounds : 8) ? 1024
+                                                  : 0;
 }
 
 // Lines of partial sums, and with them workgroups of the backward: two per CU fill the card as the
@@ -400,10 +413,11 @@ void bwd(const NormArgs& a, float* part, int64_t* lines, hipStream_t stream) {
   with_past<V>(go, passes_cache(a.rows * a.dim * each));
 }
 
-// Calls f with the instance's V, TPR and K: groups of four columns (V = 4) in up to four rounds,
-// single columns (V = 1) in up to sixteen.  More than 64 threads take a row only when it has more
-// columns than a quarter as many hold, so the fewest rounds are for 64 alone.
-template <int V, int TPR, class F>
+// Calls f with the instance's V, TPR and K: groups of four columns (V = 4) in up to four rounds (up
+// to ROUNDS by 1024 threads), single columns (V = 1) in up to sixteen.  More than 64 threads take a
+// row only when it has more columns than a quarter as many hold, so the fewest rounds are for 64
+// alone.
+template <int V, int TPR, int ROUNDS, class F>
 void with_rounds(int64_t dim, F f) {
   const int64_t k = (dim + TPR * V - 1) / (TPR * V);
   using std::integral_constant;
@@ -413,6 +427,7 @@ void with_rounds(int64_t dim, F f) {
       if (k <= 1) return go(integral_constant<int, 1>{});
     }
     if (k <= 2) go(integral_constant<int, 2>{});
+    else if constexpr (TPR == 1024 && ROUNDS == 3) go(integral_constant<int, 3>{});
     else if (k <= 3) go(integral_constant<int, 3>{});
     else go(integral_constant<int, 4>{});
   } else {
@@ -426,16 +441,16 @@ void with_rounds(int64_t dim, F f) {
     else go(integral_constant<int, 16>{});
   }
 }
-template <int V, class F>
+template <int V, int ROUNDS, class F>
 void with_threads(int64_t dim, int tpr, F f) {
-  if (tpr == 64) with_rounds<V, 64>(dim, f);
-  else if (tpr == 256) with_rounds<V, 256>(dim, f);
-  else with_rounds<V, 1024>(dim, f);
+  if (tpr == 64) with_rounds<V, 64, ROUNDS>(dim, f);
+  else if (tpr == 256) with_rounds<V, 256, ROUNDS>(dim, f);
+  else with_rounds<V, 1024, ROUNDS>(dim, f);
 }
-template <class F>
+template <int ROUNDS, class F>
 void with_shape(int64_t dim, bool quads, int tpr, F f) {
-  if (quads) with_threads<4>(dim, tpr, f);
-  else with_threads<1>(dim, tpr, f);
+  if (quads) with_threads<4, ROUNDS>(dim, tpr, f);
+  else with_threads<1, ROUNDS>(dim, tpr, f);
 }
 
 template <class IO>
@@ -446,12 +461,13 @@ hipError_t launch_fwd(const NormArgs& a, hipStream_t stream) {
                          reinterpret_cast<uintptr_t>(a.bias);
   const uintptr_t io = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out);
   const bool quads = a.dim % 4 == 0 && wide % 16 == 0 && io % (4 * sizeof(typename IO::elem)) == 0;
-  const int tpr = threads_per_row(a.dim, quads);
+  const int tpr = threads_per_row(a.dim, quads, kRoundsFwd);
   if (!tpr)
     hipLaunchKernelGGL((norm_fwd_wide_kernel<IO>), dim3(blocks_of(a.rows, 1, 4096)),
                        dim3(kWide), 0, stream, a);
   else
-    with_shape(a.dim, quads, tpr, [&](auto v, auto t, auto k) { fwd<IO, v, t, k>(a, stream); });
+    with_shape<kRoundsFwd>(a.dim, quads, tpr,
+                           [&](auto v, auto t, auto k) { fwd<IO, v, t, k>(a, stream); });
   return hipGetLastError();
 }
 
@@ -464,7 +480,7 @@ hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
   const bool quads = a.dim % 4 == 0 && wide % 16 == 0 &&
                      io % (4 * sizeof(typename IO::elem)) == 0 &&
                      reinterpret_cast<uintptr_t>(a.x) % (4 * sizeof(typename S::elem)) == 0;
-  const int tpr = threads_per_row(a.dim, quads);
+  const int tpr = threads_per_row(a.dim, quads, kRoundsBwd);
   float* part = a.dweight || a.dbias ? static_cast<float*>(a.workspace) : nullptr;
   int64_t lines = 0;
   if (!tpr) {
@@ -478,8 +494,9 @@ hipError_t launch_bwd(const NormArgs& a, hipStream_t stream) {
                          dim3(256), 0, stream, a, part);
     }
   } else {
-    with_shape(a.dim, quads, tpr,
-               [&](auto v, auto t, auto k) { bwd<IO, S, v, t, k>(a, part, &lines, stream); });
+    with_shape<kRoundsBwd>(a.dim, quads, tpr, [&](auto v, auto t, auto k) {
+      bwd<IO, S, v, t, k>(a, part, &lines, stream);
+    });
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !part) return e;

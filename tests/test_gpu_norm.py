@@ -216,7 +216,7 @@ def gradients64(dout, s, weight, mean, rstd, dsum):
 @pytest.mark.parametrize("rows,dim", [(5003, 1000), (1501, 1540), (1501, 2560), (1030, 4096),
                                       (1100, 5120), (1030, 12288), (1030, 16384), (5003, 333),
                                       (1501, 2561), (1501, 3601), (1030, 4099), (1030, 8191),
-                                      (300, 8193), (200, 20000), (67, 20001)])
+                                      (300, 8193), (130, 12292), (200, 20000), (67, 20001)])
 def test_gradients_where_workgroups_take_many_rows(rows, dim, io, sdt):
     dt = {"f32": torch.float32, "bf16": torch.bfloat16}
     dout, s, w, mean, rstd, dsum = whole(rows, dim, rows + dim)
