@@ -328,3 +328,118 @@ def test_refusals_of_the_binding():
         with pytest.raises(kind):
             f()
             print("not refused:", k)
+
+
+def random_bf16(shape, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+
+
+@pytest.fixture
+def large():
+    """The test's arrays go back to the device, not to the allocator's cache."""
+    yield
+    torch.cuda.empty_cache()
+
+
+def test_recurrence_past_32_bit_offsets(large):
+    """2.2e9 elements (4.5 GB) an array.  The last steps behind a start at a tile's edge equal a
+    call on them alone, where every tile holds the same steps (gradients from the next tile on: the
+    tile with the start takes another path, whose compiler may round a sum elsewhere)."""
+    o = ops()
+    B, L, d, cut = 2, 270100, 4160, 270080 - 20 * 128
+    assert B * L * d > 1 << 31 and cut % 128 == 0
+    x, r, i, z, dout = (random_bf16((B, L, d), s) for s in range(5))
+    A = -torch.rand(d, device="cuda")
+    starts = torch.zeros(B, L, dtype=torch.bool, device="cuda")
+    starts[:, cut] = True
+    out, states, last = o.gated_scan_fwd_states(x, r, i, A, z=z, starts=starts,
+                                                return_last_state=True)
+    g = o.gated_scan_bwd(x, r, i, A, dout, z=z, starts=starts, states=states)
+    tail = lambda t: t[:, cut:].contiguous()  # noqa: E731
+    p, s, h = o.gated_scan_fwd_states(tail(x), tail(r), tail(i), A, z=tail(z),
+                                      return_last_state=True)
+    q = o.gated_scan_bwd(tail(x), tail(r), tail(i), A, tail(dout), z=tail(z), states=s)
+    assert torch.equal(out[:, cut:], p) and torch.equal(last, h)
+    assert torch.equal(states[:, cut // 64:], s)
+    for name in ("dx", "dr", "di", "dz"):
+        assert torch.equal(g[name][:, cut + 64:], q[name][:, 64:]), name
+
+
+def test_convolution_past_32_bit_offsets(large):
+    o = ops()
+    B, L, d, cut = 2, 270100, 4160, 270080 - 20 * 64
+    x, dout = random_bf16((B, L, d), 1), random_bf16((B, L, d), 2)
+    w = torch.randn(d, 4, device="cuda")
+    out, g = o.causal_conv_fwd(x, w), o.causal_conv_bwd(x, w, dout)
+    tail, prev = x[:, cut:].contiguous(), x[:, cut - 3:cut].contiguous()
+    assert torch.equal(out[:, cut:], o.causal_conv_fwd(tail, w, x_prev=prev))
+    q = o.causal_conv_bwd(tail, w, dout[:, cut:].contiguous(), x_prev=prev)
+    assert torch.equal(g["dx"][:, cut:], q["dx"])
+
+
+def test_norm_past_32_bit_offsets(large):
+    o = ops()
+    rows, dim, cut = 900001, 2560, 899900
+    assert rows * dim > 1 << 31
+    x, dout = random_bf16((rows, dim), 1), random_bf16((rows, dim), 2)
+    res = torch.randn(rows, dim, device="cuda")
+    out, s, mean, rstd = o.layer_norm_fwd(x, residual=res, return_stats=True)
+    g = o.layer_norm_bwd(dout, s, None, mean, rstd, dsum=res, want_dresidual=True)
+    p, t, m, v = o.layer_norm_fwd(x[cut:], residual=res[cut:], return_stats=True)
+    q = o.layer_norm_bwd(dout[cut:], t, None, m, v, dsum=res[cut:], want_dresidual=True)
+    for whole, alone in ((out, p), (s, t), (mean, m), (rstd, v), (g["dx"], q["dx"]),
+                         (g["dresidual"], q["dresidual"])):
+        assert torch.equal(whole[cut:], alone)
+
+
+@pytest.mark.parametrize("d", [1 << 24, (1 << 24) - 27])
+def test_the_widest_rows(d, large):
+    """Channels do not meet in the recurrence and the convolution: the last ones of the widest rows
+    equal a call on them alone.  The norm of such a row is compared with float64."""
+    o = ops()
+    L, lo = 35, (1 << 24) - 300
+    x, r, i = (torch.randn(1, L, d, device="cuda") for _ in range(3))
+    A, w = -torch.rand(d, device="cuda"), torch.randn(d, 4, device="cuda")
+    c = lambda t: t[..., lo:].contiguous()  # noqa: E731
+    last = (c(x), c(r), c(i), A[lo:].clone())
+    assert torch.equal(c(o.gated_scan_fwd(x, r, i, A)), o.gated_scan_fwd(*last))
+    g, q = o.gated_scan_bwd(x, r, i, A, x), o.gated_scan_bwd(*last, last[0])
+    for name in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dh0"):
+        assert torch.equal(c(g[name]), q[name]), name
+    del g
+    h, hl = r[:, 0].clone(), c(r[:, 0])
+    y = o.gated_state_update(h, x[:, 1].clone(), r[:, 1].clone(), i[:, 1].clone(), A)
+    z = o.gated_state_update(hl, *(t[:, 1].contiguous() for t in last[:3]), last[3])
+    assert torch.equal(c(y), z) and torch.equal(c(h), hl)
+    # (whole numbers: sums over the steps are exact however many a wave takes)
+    x, r, w = ((3 * t).clamp(-9, 9).round() for t in (x, r, w))
+    last, wl = (c(x), c(r)), w[lo:].clone()
+    assert torch.equal(c(o.causal_conv_fwd(x, w)), o.causal_conv_fwd(last[0], wl))
+    g = o.causal_conv_bwd(x, w, r, silu=False)
+    q = o.causal_conv_bwd(last[0], wl, last[1], silu=False)
+    assert torch.equal(c(g["dx"]), q["dx"]) and torch.equal(g["dweight"][lo:], q["dweight"])
+    assert torch.equal(g["dbias"][lo:], q["dbias"])
+    del g
+    win, wn = x[:, :3].clone(), last[0][:, :3].clone()
+    y = o.causal_conv_update(win, x[:, 3].clone(), w)
+    z = o.causal_conv_update(wn, last[0][:, 3].clone(), wl)
+    assert torch.equal(c(y), z) and torch.equal(c(win), wn)
+    # Small whole numbers and a power of two for rstd: sums below 2^24 are exact, so that 1 / d and
+    # six more roundings of terms of at most 6 remain.
+    dy, s = (torch.randint(-1, 2, (2, d), device="cuda").float() for _ in range(2))
+    zero, one = torch.zeros(2, device="cuda"), torch.ones(2, device="cuda")
+    g = o.layer_norm_bwd(dy, s, None, zero, one)
+    xh, gy = s.double(), dy.double()
+    ds = gy - gy.mean(1, keepdim=True) - xh * (gy * xh).mean(1, keepdim=True)
+    assert ((g["dx"].double() - ds).abs() <= 7 * 2.0 ** -24 * 3).all()
+    assert torch.equal(g["dweight"].double(), (gy * xh).sum(0))
+    assert torch.equal(g["dbias"].double(), gy.sum(0))
+    out, mean, rstd = o.layer_norm_fwd(s, return_stats=True)
+    mu = xh.mean(1)
+    # at most 2^14 products a thread, each added with a rounding, then the thread sums
+    assert ((mean.double() - mu).abs() <= 2.0 ** -24 * 2 * mu.abs()).all()
+    v = 1 / (((xh - mu[:, None]) ** 2).mean(1) + 1e-5).sqrt()
+    assert ((rstd.double() - v).abs() <= 2.0 ** -24 * (2 ** 14 + 50) * v).all()
+    assert ((out.double() - (xh - mu[:, None]) * v[:, None]).abs()
+            <= 2.0 ** -24 * (2 ** 14 + 60) * 2 * v.max()).all()
