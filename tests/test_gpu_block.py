@@ -443,3 +443,32 @@ def test_the_widest_rows(d, large):
     assert ((rstd.double() - v).abs() <= 2.0 ** -24 * (2 ** 14 + 50) * v).all()
     assert ((out.double() - (xh - mu[:, None]) * v[:, None]).abs()
             <= 2.0 ** -24 * (2 ** 14 + 60) * 2 * v.max()).all()
+
+
+@pytest.mark.parametrize("L", [1, 3, 40, 700])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), torch.finfo(torch.float32).min])
+def test_a_start_at_the_first_step_cuts_off_what_was_before(L, bad):
+    """Whatever h0 and x_prev hold then, results, sums over tokens among them, are those of a call
+    without them, and their gradients are 0."""
+    o = ops()
+    x, r, i, dout = (torch.randn(2, L, 70, device="cuda") for _ in range(4))
+    A, w = -torch.rand(70, device="cuda"), torch.randn(70, 4, device="cuda")
+    starts = torch.rand(2, L, device="cuda") < 0.05
+    starts[:, 0] = True
+    h0, xp = torch.full((2, 70), bad, device="cuda"), torch.full((2, 3, 70), bad, device="cuda")
+    want = o.gated_scan_fwd_states(x, r, i, A, starts=starts, return_last_state=True)
+    got = o.gated_scan_fwd_states(x, r, i, A, starts=starts, h0=h0, return_last_state=True)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q) and torch.isfinite(p).all()
+    g = o.gated_scan_bwd(x, r, i, A, dout, starts=starts, h0=h0)
+    v = o.gated_scan_bwd(x, r, i, A, dout, starts=starts)
+    for k in ("dx", "dr", "di", "dA", "dr_bias", "di_bias", "dh0"):
+        assert torch.equal(g[k], v[k]) and torch.isfinite(g[k]).all(), k
+    assert not g["dh0"].any()
+    assert torch.equal(o.causal_conv_fwd(x, w, x_prev=xp, starts=starts),
+                       o.causal_conv_fwd(x, w, starts=starts))
+    g = o.causal_conv_bwd(x, w, dout, x_prev=xp, starts=starts)
+    v = o.causal_conv_bwd(x, w, dout, starts=starts)
+    for k in ("dx", "dweight", "dbias"):
+        assert torch.equal(g[k], v[k]) and torch.isfinite(g[k]).all(), k
+    assert not g["dx_prev"].any()
