@@ -361,7 +361,8 @@ ss_status ss_state_update_conv(float* state, void* conv_state, const void* x,
  * 1 - a^2 is formed without cancellation (as -expm1(2 A rg)).  Results do not depend on timing or
  * on the order in which workgroups run: two runs agree bit for bit.  They do depend, by rounding,
  * on where a step lies in its row: a sequence behind a start and the same one in a call of its own
- * agree to a few float32 roundings per step.
+ * agree to a few float32 roundings per step.  A decay below 2^-126 counts as 0 and a product of
+ * decays below it as 2^-126: an error of at most 2^-126 times the state before.
  * Outputs must not overlap the inputs, each other or the workspace (SS_ERR_INVALID_ARG); d_inner
  * above 2^24 or seqlen above 2^31 - 1 -> SS_ERR_UNSUPPORTED.  Empty sizes are a no-op (with
  * seqlen == 0, h_last receives h0, or zeros).

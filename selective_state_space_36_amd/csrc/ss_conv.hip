@@ -5,9 +5,10 @@
 // start inside a row, a mask of the starts, the same for the whole wave (a scalar register), says
 // which taps would cross one; steps without a start run without a branch.
 //
-// What bounds it: memory.  4 x 4096 x 5120 bfloat16, four taps: forward 336 MB in 64 us (5.3 TB/s),
-// backward 503 MB in 102 us (4.9 TB/s, the VALU issuing in nine tenths of the cycles: 36 operations
-// per element) and 5 us for the parameters' sums.
+// What bounds it: the forward memory, the backward memory and the VALU alike.  4 x 4096 x 5120
+// bfloat16, four taps, packed: forward 336 MB in 64 us (5.2 TB/s), backward 503 MB in 108 us
+// (4.7 TB/s, the VALU issuing in nine tenths of the cycles: 36 operations per element) and 5 us for
+// the parameters' sums.
 // Why these runs: the forward takes a wave's 16 rows and the 3 before them at once, which
 // neighbours find in the cache (8 rows: 3 us more).  The backward needs 3 rows on either side of
 // its own, so it walks 64 steps with 8 rows in flight (16 to 128 steps and 4 rows: 2 to 20 us more;

@@ -10,7 +10,7 @@
 // LDS, and over the tiles by a second kernel, always in the same order.
 //
 // What bounds it: memory and its latency.  4 x 4096 x 5120 bfloat16 with a gate moves 1.55 GB in
-// 339 us (4.6 TB/s; a copy of that size reaches 4.9); without the wait for the chain it took 4 %
+// 340 us (4.6 TB/s; a copy of that size reaches 4.9); without the wait for the chain it took 4 %
 // less, with 20 % fewer VALU operations 1 % less.
 // Why eight steps per wave in eight waves: sixteen hold too many registers for two workgroups on
 // a CU, and chunks of 32 and 128 steps took 714 and 612 us a training step against then 566.  Two

@@ -18,10 +18,11 @@
 // state among them and a piece in every slot nearer than it, then runs forward from that state.
 // Where all of them hold pieces but none an end state twice over (few chains, and so many tiles of
 // each at work at the same time), it reaches up to kFar tiles back, kMore at a time, through LDS.
-// Measured: 4 near tiles against 8 or 12 read every time, 67 against 68 and 69 us at 8 x 2048 x
-// 1536 and 702 against 743 and 760 us at 1 x 262144 x 1536; the far ones with and without, 91 and
-// 176 us at 1 x 131072 x 64 (one chain of 1024 tiles), 168 and 220 us at 1 x 131072 x 512, and
-// asked for at once, 769 us at 1 x 262144 x 1536.
+// Measured (each comparison here timed in turn, with the kernels as they then stood): 4 near tiles
+// against 8 or 12 read every time, 67 against 68 and 69 us at 8 x 2048 x 1536 and 702 against 743
+// and 760 us at 1 x 262144 x 1536; the far ones with and without, 91 and 176 us at 1 x 131072 x 64
+// (one chain of 1024 tiles), 168 and 220 us at 1 x 131072 x 512, and asked for at once, 769 us at
+// 1 x 262144 x 1536.
 // Every tile's end state is formed as advance(piece, state before) whoever forms it, so the result
 // does not depend on timing: two runs agree bit for bit.
 //

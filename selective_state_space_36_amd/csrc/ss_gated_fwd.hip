@@ -6,12 +6,12 @@
 // to the chain (ss_gated_chain.h), and with the state before its first step every wave runs its
 // steps again from the registers and stores.  Inputs are read once and outputs written once.
 //
-// What bounds it: memory.  1 x 262144 x 1536 bfloat16 without a gate moves 3.2 GB in 689 us
+// What bounds it: memory.  1 x 262144 x 1536 bfloat16 without a gate moves 3.2 GB in 688 us
 // (4.7 TB/s, what a copy of that size reaches); 4 x 4096 x 5120 with a gate 0.84 GB in 182 us
-// (4.6 TB/s), the VALU issuing in four fifths of the cycles
-// (44 operations per element, six of them transcendental).
+// (4.6 TB/s), the VALU issuing in four fifths of the cycles (44 operations per element, eight of
+// them transcendental: two for each of the three sigmoids, the decay and the root).
 // Why this tile: a tile pays for the chain, the parameters and the waves' pieces once, so long ones
-// are better, as far as registers let two workgroups share a CU.  At 8 x 2048 x 1536, 60 us now, 64
+// are better, as far as registers let two workgroups share a CU.  At 8 x 2048 x 1536, 61 us now, 64
 // steps in four or eight waves took 93 and 85 us when 128 took 66 (with two channels per lane 69),
 // 96 steps 79, 192 in twelve waves 71, 256 in sixteen 67; 32 steps per wave gained 3 % at
 // 1 x 262144 x 1536 and lost 4 % in float32.  Workgroups that stay and draw their next tile early

@@ -69,10 +69,11 @@ struct Lanes<F32, 4> {
 //
 // PAST: the access is marked non-temporal, so that it does not keep a place in the caches.  That is
 // for calls that move more than the 256 MB Infinity Cache holds (passes_cache), where nobody finds
-// their rows there again.  Training steps, never / always: recurrence 4 x 4096 x 5120 551 / 527 us,
-// 8 x 2048 x 1536 189 / 179, 2 x 2048 x 1536 (63 and 113 MB) 60.4 / 65.4; norm (loads only)
-// 16384 x 2560 227 / 206, 10000 x 2560 142 / 123, 16384 x 768 (151 and 201 MB) 64 / 68;
-// convolution (its forward's loads apart, which neighbours share) 4 x 4096 x 5120 191 / 170.
+// their rows there again.  Training steps, never / always, timed in turn with the kernels as they
+// then stood: recurrence 4 x 4096 x 5120 551 / 527 us, 8 x 2048 x 1536 189 / 179, 2 x 2048 x 1536
+// (63 and 113 MB) 60.4 / 65.4; norm (loads only) 16384 x 2560 227 / 206, 10000 x 2560 142 / 123,
+// 16384 x 768 (151 and 201 MB) 64 / 68; convolution (its forward's loads apart, which neighbours
+// share) 4 x 4096 x 5120 191 / 170.
 template <class IO, int V, bool PAST = false>
 struct Rows {
   using raw = typename Lanes<IO, V>::raw;
