@@ -355,7 +355,7 @@ __global__ __launch_bounds__(256) void norm_param_wide_kernel(NormArgs p, float*
 // spills 8 to 21 registers, which still pays (4096 x 8196 153 / 203, 4096 x 12288 192 / 270 and
 // 164 / 255; not where everything lies in the cache, 512 x 12288 58 / 35); in a fourth 50 to 62,
 // which does not (4096 x 12292 409 / 284, 4096 x 16384 442 / 346 and 445 / 327, 512 x 12292 86 /
-// 37).
+// 37; one to 64 rows of 16384, which launches bound, 18 to 25 / 19 to 27).
 constexpr int kRoundsFwd = 4, kRoundsBwd = 3;
 int threads_per_row(int64_t dim, bool quads, int rounds) {
   return dim <= 64 * 16 ? 64
