@@ -518,6 +518,193 @@ ss_status ss_causal_conv_update(void* conv_state, const void* x, const float* we
                                 const float* bias, int silu, void* out, int64_t batch,
                                 int64_t d_inner, int32_t k, ss_dtype dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The block around the multi-head scan (ss_scan2_fwd): the scan's next token with the convolution
+ * in front of it, its gradients, the RMS norm in front of a block (which adds the block before to
+ * the residual stream), the gated RMS norm behind the scan, and dropout.  A block is
+ *
+ *     norm -> projection [z | x B C | dt] -> convolution -> scan -> gated norm -> projection
+ *
+ * where the projections are the caller's matrix products.  io dtype as above; parameters, states,
+ * statistics and every gradient that is a sum over tokens are float32, and so is all arithmetic.
+ * Some inputs are parts of a projection's rows: those have a `_stride`, the elements from one row
+ * to the next (at least the row's own; other arrays are contiguous).
+ * ------------------------------------------------------------------------------------------- */
+
+/*
+ * Gradients of ss_scan2_fwd for the upstream gradients dout (io dtype, required) and dh_last
+ * (float32, NULL: 0), with lam_t = dL/dS_t:
+ *
+ *     gy_t  = dout_t silu(z_t);    lam_t = C_t gy_t^T + a_{t+1} lam_{t+1};   a_t = exp(dt_t A)
+ *     dx_t  = D gy_t + dt_t lam_t^T B_t;           dz_t = dout_t y_t silu'(z_t)
+ *     dB_t  = sum over the group's heads of dt_t lam_t x_t;   dC_t = sum of S_t gy_t
+ *     dl_t  = <lam_t, a_t S_{t-1}>;   ddt_t = (A dl_t + x_t . lam_t^T B_t) softplus'(dt_t + bias)
+ *     dA = sum dt_t dl_t;   dD = sum gy_t . x_t;   ddt_bias = sum ddt_t;   dh0 = a_0 lam_0
+ *
+ *   x .. h0, sizes    : exactly as given to ss_scan2_fwd.
+ *   dx, ddt, dB, dC   : in the io dtype and the shapes of x, dt, B and C, required; dz likewise
+ *                       with z (without z it is not written).  dB and dC are added over the heads
+ *                       in float32 and rounded once: they go on as rows of the convolution's or
+ *                       the projection's upstream gradient.
+ *   dA                : (nheads) float32, required.  dD, ddt_bias: (nheads) float32, NULL: not
+ *                       written (the gradient at the given D / bias, also when those are NULL,
+ *                       i.e. 0).  Sums in a fixed order: two runs agree bit for bit.  Zeros when
+ *                       there are no tokens.
+ *   dh0               : (batch, nheads, d_state, headdim) float32, NULL: not written.
+ *   workspace         : ss_scan2_bwd_workspace_bytes() bytes, 16-byte aligned: first the states
+ *                       before and the adjoints behind every 64 steps.  Its contents need no
+ *                       preparation and mean nothing after the call; calls that may run at the
+ *                       same time need one each.
+ * d_state outside 1..256, headdim or nheads above 2^24 or seqlen above 2^31 - 1 ->
+ * SS_ERR_UNSUPPORTED.  Outputs must not overlap inputs, each other or the workspace.
+ */
+ss_status ss_scan2_bwd(const void* x, const void* dt, const float* A, const void* B,
+                       const void* C, const float* D, const void* z, const float* dt_bias,
+                       int dt_softplus, const float* h0, const void* dout, const float* dh_last,
+                       void* dx, void* ddt, void* dz, float* dA, void* dB, void* dC, float* dD,
+                       float* ddt_bias, float* dh0, int64_t batch, int64_t seqlen,
+                       int64_t nheads, int64_t headdim, int64_t ngroups, int64_t d_state,
+                       ss_dtype dtype, void* workspace, size_t workspace_bytes, void* stream);
+size_t ss_scan2_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads,
+                                    int64_t headdim, int64_t ngroups, int64_t d_state,
+                                    ss_dtype dtype);
+
+/*
+ * One token of ss_scan2_fwd: state (batch, nheads, d_state, headdim) float32 (the layout of
+ * h_last) is advanced IN PLACE; x, z, out: (batch, nheads, headdim), dt: (batch, nheads), B, C:
+ * (batch, ngroups, d_state), io dtype; the rest as in ss_scan2_fwd.  state and out must not
+ * overlap the inputs or each other.
+ */
+ss_status ss_scan2_state_update(float* state, const void* x, const void* dt, const float* A,
+                                const void* B, const void* C, const float* D, const void* z,
+                                const float* dt_bias, int dt_softplus, void* out, int64_t batch,
+                                int64_t nheads, int64_t headdim, int64_t ngroups,
+                                int64_t d_state, ss_dtype dtype, void* stream);
+
+/*
+ * The same with the convolution in front: x, B and C are what ss_causal_conv_update (with silu)
+ * makes of xbc, whose rows hold [x (nheads headdim) | B (ngroups d_state) | C (ngroups d_state)],
+ * `width` columns together; between the convolution and the scan they stay float32.
+ *   xbc        : (batch, width) io dtype, rows xbc_stride elements apart.
+ *   conv_state : (batch, conv_k - 1, width) io dtype, the window before this token (oldest
+ *                first), shifted IN PLACE.  May be NULL when conv_k == 1.
+ *   conv_weight: (width, conv_k) float32, conv_k in 1..4 (SS_ERR_UNSUPPORTED otherwise);
+ *                conv_bias: (width) float32, NULL means 0.
+ *   dt, z      : (batch, nheads) and (batch, nheads headdim), rows dt_stride and z_stride
+ *                elements apart (z_stride means nothing without z).
+ *   workspace  : ss_scan2_state_update_conv_workspace_bytes() bytes, 16-byte aligned; one per
+ *                call that may run at the same time.
+ * state, conv_state and out must not overlap the inputs, each other or the workspace.
+ */
+ss_status ss_scan2_state_update_conv(float* state, void* conv_state, const void* xbc,
+                                     int64_t xbc_stride, const float* conv_weight,
+                                     const float* conv_bias, int32_t conv_k, const void* dt,
+                                     int64_t dt_stride, const float* A, const float* D,
+                                     const void* z, int64_t z_stride, const float* dt_bias,
+                                     int dt_softplus, void* out, int64_t batch, int64_t nheads,
+                                     int64_t headdim, int64_t ngroups, int64_t d_state,
+                                     ss_dtype dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream);
+size_t ss_scan2_state_update_conv_workspace_bytes(int64_t batch, int64_t nheads, int64_t headdim,
+                                                  int64_t ngroups, int64_t d_state);
+
+/*
+ * RMS norm over the last axis, with a block's output added to the residual stream before it:
+ *
+ *     b = x, or x / sqrt(mean(x^2) + eps)  (norm_branch: the norm behind the block)
+ *     s = residual + drop(scale b);   rstd = 1 / sqrt(mean(s^2) + eps);   out = s rstd weight
+ *
+ *   x, out           : (rows, dim) io dtype.
+ *   residual, sum    : (rows, dim) float32 (as in ss_layer_norm_fwd).  residual NULL: 0.  sum
+ *                      NULL: s is not written.
+ *   weight, scale    : (dim) float32, NULL means 1.  `scale` is the block's learned residual scale
+ *                      or, with norm_branch, that norm's weight.
+ *   p, rng           : dropout as in ss_dropout; p == 0: none (rng is not read and may be NULL).
+ *   rstd, branch_rstd: (rows) float32 statistics for the backward; NULL: not written (branch_rstd
+ *                      not without norm_branch either).
+ *   eps              : not negative (SS_ERR_INVALID_ARG).
+ * Outputs must not overlap the inputs or each other.  rows == 0 or dim == 0 is a no-op.
+ * dim above 2^24 -> SS_ERR_UNSUPPORTED; rows above 2^31 - 1 -> SS_ERR_INVALID_ARG.
+ */
+ss_status ss_rms_norm_fwd(const void* x, const float* residual, const float* weight,
+                          const float* scale, int norm_branch, double p, const uint64_t* rng,
+                          float eps, void* out, float* sum, float* rstd, float* branch_rstd,
+                          int64_t rows, int64_t dim, ss_dtype dtype, void* stream);
+
+/*
+ * Gradients of ss_rms_norm_fwd, with sh = s rstd, g = dout weight and b as there:
+ *
+ *     ds = rstd (g - sh mean(g sh)) + dsum;   db = drop(ds);   dweight = sum of dout sh
+ *     dscale = sum of db b;   dx = db scale, or through the norm: branch_rstd (db scale -
+ *     b mean(db scale b))
+ *
+ *   s            : (rows, dim) in `s_dtype`: x itself (s_dtype == dtype, where the forward had
+ *                  none of residual, scale, norm_branch and dropout) or the sum it wrote.
+ *   x            : as the forward's; read for dscale and with norm_branch, else it may be NULL.
+ *   rstd, branch_rstd : as the forward wrote them (branch_rstd with norm_branch only).
+ *   weight, scale, p, rng : as the forward's.
+ *   dsum         : (rows, dim) float32 upstream gradient of sum, NULL: 0.
+ *   dx, dresidual: the gradients of x (in `dtype`) and of residual (ds, float32).  At least one is
+ *                  required.
+ *   dweight, dscale : (dim) float32, NULL: not written.  Summed in a fixed order: two runs agree
+ *                  bit for bit.  Zeros when rows == 0.
+ *   workspace    : ss_rms_norm_bwd_workspace_bytes() bytes, 16-byte aligned, with dweight or
+ *                  dscale; one per call that may run at the same time.
+ */
+ss_status ss_rms_norm_bwd(const void* dout, const void* s, ss_dtype s_dtype,
+                          const float* weight, const float* rstd, const void* x,
+                          const float* scale, int norm_branch, const float* branch_rstd,
+                          double p, const uint64_t* rng, const float* dsum, void* dx,
+                          float* dresidual, float* dweight, float* dscale, int64_t rows,
+                          int64_t dim, ss_dtype dtype, void* workspace, size_t workspace_bytes,
+                          void* stream);
+size_t ss_rms_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
+/*
+ * RMS norm with the output gate, over each of `groups` runs of dim / groups columns of a row:
+ *
+ *     gate_first: u = x silu(z);  out = u rstd weight       else: u = x;  out = u rstd weight silu(z)
+ *     rstd = 1 / sqrt(mean over the run of u^2 + eps)
+ *
+ *   x, out   : (rows, dim) io dtype.      z : the same, rows z_stride elements apart; NULL: no gate.
+ *   weight   : (dim) float32, NULL means 1.
+ *   rstd     : (rows, groups) float32 statistics for the backward; NULL: not written.
+ * dim not a multiple of groups, or rows * groups above 2^31 - 1 or groups above 2^20 ->
+ * SS_ERR_INVALID_ARG; the rest as in ss_rms_norm_fwd.
+ */
+ss_status ss_gated_norm_fwd(const void* x, const void* z, int64_t z_stride, const float* weight,
+                            int gate_first, float eps, void* out, float* rstd, int64_t rows,
+                            int64_t dim, int64_t groups, ss_dtype dtype, void* stream);
+
+/*
+ * Gradients of ss_gated_norm_fwd.  dx: (rows, dim) io dtype, required; dz likewise with z
+ * (contiguous; without z it is not written); dweight: (dim) float32, NULL: not written, summed in a
+ * fixed order, zeros when rows == 0.  rstd as the forward wrote it.  workspace:
+ * ss_gated_norm_bwd_workspace_bytes() bytes, 16-byte aligned, with dweight; one per call that may
+ * run at the same time.
+ */
+ss_status ss_gated_norm_bwd(const void* dout, const void* x, const void* z, int64_t z_stride,
+                            const float* weight, const float* rstd, int gate_first, void* dx,
+                            void* dz, float* dweight, int64_t rows, int64_t dim, int64_t groups,
+                            ss_dtype dtype, void* workspace, size_t workspace_bytes,
+                            void* stream);
+size_t ss_gated_norm_bwd_workspace_bytes(int64_t rows, int64_t dim, int64_t groups);
+
+/*
+ * Dropout: out = x / (1 - q) where the element is kept, 0 (exactly, whatever x is) where it is
+ * dropped.  q is p rounded to a multiple of 2^-16, p in 0..1 (SS_ERR_INVALID_ARG otherwise).
+ *   x, out : (rows, dim) io dtype.
+ *   rng    : two 64-bit numbers in DEVICE memory, a seed and an offset, read by the kernel (a
+ *            captured call draws anew when the caller has advanced them).  Required.
+ * The mask is not stored: it is a function of rng and of the element's row and column alone
+ * (Philox4x32-10 under the key `seed`: 16 bits per element, eight columns a counter (column / 8,
+ * row, offset)), the same in ss_dropout, ss_rms_norm_fwd and ss_rms_norm_bwd.  The gradient is this
+ * call on the upstream gradient.  Draws that are to be independent need another offset or seed.
+ * out must not overlap x.  rows == 0 or dim == 0 is a no-op; limits as in ss_rms_norm_fwd.
+ */
+ss_status ss_dropout(const void* x, void* out, double p, const uint64_t* rng, int64_t rows,
+                     int64_t dim, ss_dtype dtype, void* stream);
+
 /* Static description of a status code. */
 const char* ss_status_string(ss_status s);
 

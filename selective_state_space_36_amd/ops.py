@@ -71,6 +71,25 @@ SIGNATURES = {
     "ss_causal_conv_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32]),
     "ss_causal_conv_update": (_i32, [_vp, _vp, _vp, _vp, ctypes.c_int, _vp, _i64, _i64, _i32,
                                      _i32, _vp]),
+    "ss_scan2_bwd": (_i32, [_vp] * 8 + [ctypes.c_int] + [_vp] * 12 + [_i64] * 6
+                     + [_i32, _vp, _sz, _vp]),
+    "ss_scan2_bwd_workspace_bytes": (_sz, [_i64] * 6 + [_i32]),
+    "ss_scan2_state_update": (_i32, [_vp] * 9 + [ctypes.c_int, _vp] + [_i64] * 5 + [_i32, _vp]),
+    "ss_scan2_state_update_conv": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp,
+                                          _vp, _vp, _i64, _vp, ctypes.c_int, _vp] + [_i64] * 5
+                                   + [_i32, _vp, _sz, _vp]),
+    "ss_scan2_state_update_conv_workspace_bytes": (_sz, [_i64] * 5),
+    "ss_rms_norm_fwd": (_i32, [_vp] * 4 + [ctypes.c_int, ctypes.c_double, _vp, ctypes.c_float]
+                        + [_vp] * 4 + [_i64, _i64, _i32, _vp]),
+    "ss_rms_norm_bwd": (_i32, [_vp, _vp, _i32] + [_vp] * 4 + [ctypes.c_int, _vp, ctypes.c_double]
+                        + [_vp] * 6 + [_i64, _i64, _i32, _vp, _sz, _vp]),
+    "ss_rms_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "ss_gated_norm_fwd": (_i32, [_vp, _vp, _i64, _vp, ctypes.c_int, ctypes.c_float, _vp, _vp,
+                                 _i64, _i64, _i64, _i32, _vp]),
+    "ss_gated_norm_bwd": (_i32, [_vp, _vp, _vp, _i64, _vp, _vp, ctypes.c_int, _vp, _vp, _vp,
+                                 _i64, _i64, _i64, _i32, _vp, _sz, _vp]),
+    "ss_gated_norm_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "ss_dropout": (_i32, [_vp, _vp, ctypes.c_double, _vp, _i64, _i64, _i32, _vp]),
     "ss_status_string": (ctypes.c_char_p, [_i32]),
     "ss_last_error": (ctypes.c_char_p, []),
     "ss_version": (ctypes.c_int, []),
@@ -826,4 +845,343 @@ def causal_conv_update(conv_state, x, weight, bias=None, silu=True, out=None, st
     _check(lib().ss_causal_conv_update(
         conv_state.data_ptr(), x.data_ptr(), weight.data_ptr(), _ptr(bias), 1 if silu else 0,
         out.data_ptr(), *shape, k, code, _raw_stream(x.device)))
+    return out
+
+
+# ---------------------------------------------------------------------------------------------
+# The block around the multi-head scan.  Streams, devices and workspaces as above.
+
+
+def _row_stride(name, t, device, dtype, shape) -> int:
+    """Elements from one row of the (rows, width) tensor t to the next; its rows may be parts of
+    longer ones."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    rows, width = shape
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    if rows <= 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def _rng(p, rng, device):
+    """The pointer to the generator's (seed, offset), or None where nothing is dropped."""
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p={p} is not a probability")
+    if rng is None:
+        if p:
+            raise ValueError("dropout needs rng, the generator's seed and offset")
+        return None
+    _expect(device, torch.int64, (2,), ("rng", rng))
+    return rng.data_ptr()
+
+
+def scan2_bwd(x, dt, A, B, C, dout, D=None, z=None, dt_bias=None, dt_softplus=True, h0=None,
+              dh_last=None, want_dD=True, want_ddt_bias=True, want_dh0=True, workspace=None,
+              stream=None):
+    """Gradients of scan2_fwd (ss_scan2_bwd) for the upstream gradient dout (shape and dtype of
+    out) and optionally dh_last ((batch, nheads, d_state, headdim) float32).  Returns a dict: dx,
+    ddt, dz, dB, dC (io dtype, the shapes of x, dt, z, B, C; dz None without z), dA, dD, ddt_bias
+    ((nheads,) float32) and dh0 (float32), None where not wanted.  workspace: uint8 device buffer of
+    ss_scan2_bwd_workspace_bytes bytes (allocated here when None); calls that may overlap need one
+    each."""
+    if _elsewhere(x, stream):
+        return _moved(scan2_bwd, x, stream, (x, dt, A, B, C, dout),
+                      dict(D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, h0=h0,
+                           dh_last=dh_last, want_dD=want_dD, want_ddt_bias=want_ddt_bias,
+                           want_dh0=want_dh0, workspace=workspace))
+    code = _io_code(x)
+    batch, L, H, P = shape = _shape("x", x, 4)
+    G, N = _shape("B", B, 4)[2:]
+    dev, f32 = x.device, torch.float32
+    _expect(dev, x.dtype, shape, ("x", x), ("z", z), ("dout", dout))
+    _expect(dev, x.dtype, (batch, L, H), ("dt", dt))
+    _expect(dev, x.dtype, (batch, L, G, N), ("B", B), ("C", C))
+    _expect(dev, f32, (H,), ("A", A), ("D", D), ("dt_bias", dt_bias))
+    _expect(dev, f32, (batch, H, N, P), ("h0", h0), ("dh_last", dh_last))
+    like = torch.empty_like
+    g = dict(dx=like(x), ddt=like(dt), dz=like(x) if z is not None else None, dA=like(A),
+             dB=like(B), dC=like(C), dD=like(A) if want_dD else None,
+             ddt_bias=like(A) if want_ddt_bias else None,
+             dh0=A.new_empty((batch, H, N, P)) if want_dh0 else None)
+    l = lib()
+    nbytes = l.ss_scan2_bwd_workspace_bytes(batch, L, H, P, G, N, code)
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_scan2_bwd(
+        x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z),
+        _ptr(dt_bias), 1 if dt_softplus else 0, _ptr(h0), dout.data_ptr(), _ptr(dh_last),
+        _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dz"]), _ptr(g["dA"]), _ptr(g["dB"]), _ptr(g["dC"]),
+        _ptr(g["dD"]), _ptr(g["ddt_bias"]), _ptr(g["dh0"]), batch, L, H, P, G, N, code, ws,
+        ws_len, _raw_stream(dev)))
+    return g
+
+
+def scan2_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True,
+                       out=None, stream=None):
+    """One token of the multi-head scan (ss_scan2_state_update); `state` (batch, nheads, d_state,
+    headdim) float32, scan2_fwd's h_last, is advanced in place.  x, z: (batch, nheads, headdim);
+    dt: (batch, nheads); B, C: (batch, ngroups, d_state), one io dtype.  Returns out."""
+    if _elsewhere(x, stream):
+        return _moved(scan2_state_update, x, stream, (state, x, dt, A, B, C),
+                      dict(D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus, out=out))
+    code = _io_code(x)
+    batch, H, P = shape = _shape("x", x, 3)
+    G, N = _shape("B", B, 3)[1:]
+    dev, f32 = x.device, torch.float32
+    _expect(dev, x.dtype, shape, ("x", x), ("z", z), ("out", out))
+    _expect(dev, x.dtype, (batch, H), ("dt", dt))
+    _expect(dev, x.dtype, (batch, G, N), ("B", B), ("C", C))
+    _expect(dev, f32, (H,), ("A", A), ("D", D), ("dt_bias", dt_bias))
+    _expect(dev, f32, (batch, H, N, P), ("state", state))
+    if out is None:
+        out = torch.empty_like(x)
+    _check(lib().ss_scan2_state_update(
+        state.data_ptr(), x.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(),
+        _ptr(D), _ptr(z), _ptr(dt_bias), 1 if dt_softplus else 0, out.data_ptr(), batch, H, P, G,
+        N, code, _raw_stream(dev)))
+    return out
+
+
+def scan2_state_update_conv(state, conv_state, xbc, conv_weight, conv_bias, dt, A, ngroups=1,
+                            D=None, z=None, dt_bias=None, dt_softplus=True, out=None,
+                            workspace=None, stream=None):
+    """One token through the convolution and the multi-head scan (ss_scan2_state_update_conv):
+    state (batch, nheads, d_state, headdim) float32 and conv_state (batch, k-1, width) io dtype are
+    advanced in place.  xbc: (batch, width) with width = nheads headdim + 2 ngroups d_state, the
+    columns [x | B | C] before the convolution; conv_weight: (width, k) float32, k in 1..4;
+    conv_bias: (width,) float32 or None; dt: (batch, nheads); z: (batch, nheads headdim) or None.
+    The rows of xbc, dt and z may be parts of one projection's.  Returns out (batch, nheads,
+    headdim)."""
+    if _elsewhere(xbc, stream):
+        return _moved(scan2_state_update_conv, xbc, stream,
+                      (state, conv_state, xbc, conv_weight, conv_bias, dt, A),
+                      dict(ngroups=ngroups, D=D, z=z, dt_bias=dt_bias, dt_softplus=dt_softplus,
+                           out=out, workspace=workspace))
+    code = _io_code(xbc)
+    batch, H, N, P = _shape("state", state, 4)
+    k = _shape("conv_weight", conv_weight, 2)[1]
+    width = H * P + 2 * ngroups * N
+    dev, f32, io = xbc.device, torch.float32, xbc.dtype
+    _expect(dev, f32, state.shape, ("state", state))
+    _expect(dev, f32, (width, k), ("conv_weight", conv_weight))
+    _expect(dev, f32, (width,), ("conv_bias", conv_bias))
+    _expect(dev, io, (batch, max(k - 1, 0), width), ("conv_state", conv_state))
+    _expect(dev, f32, (H,), ("A", A), ("D", D), ("dt_bias", dt_bias))
+    _expect(dev, io, (batch, H, P), ("out", out))
+    xs = _row_stride("xbc", xbc, dev, io, (batch, width))
+    ds = _row_stride("dt", dt, dev, io, (batch, H))
+    zs = _row_stride("z", z, dev, io, (batch, H * P)) if z is not None else 0
+    if out is None:
+        out = xbc.new_empty((batch, H, P))
+    l = lib()
+    nbytes = l.ss_scan2_state_update_conv_workspace_bytes(batch, H, P, ngroups, N)
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_scan2_state_update_conv(
+        state.data_ptr(), _ptr(conv_state), xbc.data_ptr(), xs, conv_weight.data_ptr(),
+        _ptr(conv_bias), k, dt.data_ptr(), ds, A.data_ptr(), _ptr(D), _ptr(z), zs, _ptr(dt_bias),
+        1 if dt_softplus else 0, out.data_ptr(), batch, H, P, ngroups, N, code, ws, ws_len,
+        _raw_stream(dev)))
+    return out
+
+
+def rms_norm_fwd(x, weight=None, residual=None, scale=None, norm_branch=False, p=0.0, rng=None,
+                 eps=1e-5, return_sum=None, return_stats=False, out=None, sum_out=None,
+                 stream=None):
+    """RMS norm over the last axis of s = residual + dropout(scale * x) (ss_rms_norm_fwd); with
+    norm_branch x is RMS-normalised first (the norm behind a block; scale is its weight then).
+
+    x: (..., dim) float32 or bfloat16; residual: the same shape, float32 (the residual stream);
+    weight, scale: (dim,) float32; p, rng: as in dropout.  Returns out alone, or a tuple of out,
+    then the float32 sum s (return_sum: by default wherever s is not x), then with return_stats the
+    statistics rstd and branch_rstd, (...) float32, that rms_norm_bwd takes (branch_rstd None
+    without norm_branch; NaN, being 0 / 0, where dim is 0)."""
+    if _elsewhere(x, stream):
+        return _moved(rms_norm_fwd, x, stream, (x,),
+                      dict(weight=weight, residual=residual, scale=scale, norm_branch=norm_branch,
+                           p=p, rng=rng, eps=eps, return_sum=return_sum,
+                           return_stats=return_stats, out=out, sum_out=sum_out))
+    code = _io_code(x)
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    shape, dev, f32 = x.shape, x.device, torch.float32
+    dim = shape[-1]
+    rows = x.numel() // dim if dim else 0
+    if return_sum is None:
+        return_sum = residual is not None or scale is not None or norm_branch or p > 0
+    _expect(dev, x.dtype, shape, ("x", x), ("out", out))
+    _expect(dev, f32, shape, ("residual", residual), ("sum_out", sum_out))
+    _expect(dev, f32, (dim,), ("weight", weight), ("scale", scale))
+    seed = _rng(p, rng, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    if return_sum and sum_out is None:
+        sum_out = torch.empty_like(x, dtype=f32)
+    rstd = branch_rstd = None
+    if return_stats:
+        rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
+        branch_rstd = torch.empty_like(rstd) if norm_branch else None
+        if not dim:  # the library writes nothing then
+            for t in (rstd, branch_rstd):
+                if t is not None:
+                    t.fill_(float("nan"))
+    _check(lib().ss_rms_norm_fwd(
+        x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(scale), 1 if norm_branch else 0, p, seed,
+        eps, out.data_ptr(), _ptr(sum_out), _ptr(rstd), _ptr(branch_rstd), rows, dim, code,
+        _raw_stream(dev)))
+    res = (out, *((sum_out,) if return_sum else ()),
+           *((rstd, branch_rstd) if return_stats else ()))
+    return res if len(res) > 1 else out
+
+
+def rms_norm_bwd(dout, s, weight, rstd, x=None, scale=None, norm_branch=False, branch_rstd=None,
+                 p=0.0, rng=None, dsum=None, want_dx=True, want_dresidual=False,
+                 want_dparams=True, workspace=None, stream=None):
+    """Gradients of rms_norm_fwd (ss_rms_norm_bwd) for the upstream gradient dout of out and
+    optionally dsum (float32) of the sum.  s: what was normalised, the float32 sum or, where the
+    forward had none, x itself; rstd, branch_rstd: the forward's statistics; weight, scale,
+    norm_branch, p, rng: as the forward's; x: as the forward's, needed with scale or norm_branch.
+    Returns a dict: dx (dout's dtype), dresidual (float32), dweight, dscale ((dim,) float32; dscale
+    None without scale), None where not wanted."""
+    if _elsewhere(dout, stream):
+        return _moved(rms_norm_bwd, dout, stream, (dout, s, weight, rstd),
+                      dict(x=x, scale=scale, norm_branch=norm_branch, branch_rstd=branch_rstd, p=p,
+                           rng=rng, dsum=dsum, want_dx=want_dx, want_dresidual=want_dresidual,
+                           want_dparams=want_dparams, workspace=workspace))
+    code = _io_code(dout)
+    if dout.dim() < 1:
+        raise ValueError("dout needs at least one dimension")
+    shape, dev, f32 = dout.shape, dout.device, torch.float32
+    dim = shape[-1]
+    rows = dout.numel() // dim if dim else 0
+    s_dtype = f32 if s.dtype is f32 else dout.dtype
+    _expect(dev, dout.dtype, shape, ("dout", dout), ("x", x))
+    _expect(dev, s_dtype, shape, ("s", s))
+    _expect(dev, f32, shape, ("dsum", dsum))
+    _expect(dev, f32, (dim,), ("weight", weight), ("scale", scale))
+    _expect(dev, f32, shape[:-1], ("rstd", rstd), ("branch_rstd", branch_rstd))
+    want_dscale = want_dparams and scale is not None
+    if x is None and (want_dscale or norm_branch):
+        raise ValueError("x is needed for the gradient of scale and with norm_branch")
+    if norm_branch and branch_rstd is None:
+        raise ValueError("branch_rstd is needed with norm_branch")
+    seed = _rng(p, rng, dev)
+    g = dict(dx=torch.empty_like(dout) if want_dx else None,
+             dresidual=torch.empty_like(dout, dtype=f32) if want_dresidual else None,
+             dweight=rstd.new_empty((dim,)) if want_dparams else None,
+             dscale=rstd.new_empty((dim,)) if want_dscale else None)
+    l = lib()
+    nbytes = l.ss_rms_norm_bwd_workspace_bytes(rows, dim) if want_dparams else 0
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_rms_norm_bwd(
+        dout.data_ptr(), s.data_ptr(), _IO[s_dtype], _ptr(weight), rstd.data_ptr(), _ptr(x),
+        _ptr(scale), 1 if norm_branch else 0, _ptr(branch_rstd), p, seed, _ptr(dsum),
+        _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]), _ptr(g["dscale"]), rows, dim,
+        code, ws, ws_len, _raw_stream(dev)))
+    return g
+
+
+def _gated_norm_z(x, z):
+    """(rows, dim, z's row stride): z has x's shape, its rows may be parts of longer ones."""
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    if z is None:
+        return rows, dim, 0
+    if z.shape != x.shape:
+        raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(x.shape)}")
+    if rows and z.dim() != 2:
+        # the leading axes have to be one run of rows
+        try:
+            z = z.view(rows, dim)
+        except RuntimeError:
+            raise ValueError("z must have equally spaced rows") from None
+    return rows, dim, _row_stride("z", z, x.device, x.dtype, (rows, dim)) if rows else dim
+
+
+def gated_norm_fwd(x, z=None, weight=None, groups=1, gate_first=True, eps=1e-5,
+                   return_stats=False, out=None, stream=None):
+    """RMS norm with an output gate, over each of `groups` runs of the last axis
+    (ss_gated_norm_fwd): norm(x silu(z)) * weight, or norm(x) * weight * silu(z) with
+    gate_first=False; without z no gate.  x: (..., dim) float32 or bfloat16; z: the same shape (its
+    rows may be parts of longer ones); weight: (dim,) float32.  Returns out, or (out, rstd) with
+    return_stats: the statistics, (..., groups) float32, that gated_norm_bwd takes."""
+    if _elsewhere(x, stream):
+        return _moved(gated_norm_fwd, x, stream, (x,),
+                      dict(z=z, weight=weight, groups=groups, gate_first=gate_first, eps=eps,
+                           return_stats=return_stats, out=out))
+    code = _io_code(x)
+    rows, dim, zs = _gated_norm_z(x, z)
+    dev = x.device
+    _expect(dev, x.dtype, x.shape, ("x", x), ("out", out))
+    _expect(dev, torch.float32, (dim,), ("weight", weight))
+    if out is None:
+        out = torch.empty_like(x)
+    rstd = None
+    if return_stats:
+        rstd = torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=dev)
+        if not dim:  # the library writes nothing then
+            rstd.fill_(float("nan"))
+    _check(lib().ss_gated_norm_fwd(
+        x.data_ptr(), _ptr(z), zs, _ptr(weight), 1 if gate_first else 0, eps, out.data_ptr(),
+        _ptr(rstd), rows, dim, groups, code, _raw_stream(dev)))
+    return (out, rstd) if return_stats else out
+
+
+def gated_norm_bwd(dout, x, z, weight, rstd, groups=1, gate_first=True, want_dweight=True,
+                   workspace=None, stream=None):
+    """Gradients of gated_norm_fwd (ss_gated_norm_bwd); x, z, weight, groups and gate_first as the
+    forward's, rstd its statistics.  Returns a dict: dx, dz (io dtype; dz None without z) and
+    dweight ((dim,) float32, None when not wanted)."""
+    if _elsewhere(dout, stream):
+        return _moved(gated_norm_bwd, dout, stream, (dout, x, z, weight, rstd),
+                      dict(groups=groups, gate_first=gate_first, want_dweight=want_dweight,
+                           workspace=workspace))
+    code = _io_code(dout)
+    rows, dim, zs = _gated_norm_z(x, z)
+    dev = dout.device
+    _expect(dev, dout.dtype, dout.shape, ("dout", dout), ("x", x))
+    _expect(dev, torch.float32, (dim,), ("weight", weight))
+    _expect(dev, torch.float32, (*dout.shape[:-1], groups), ("rstd", rstd))
+    g = dict(dx=torch.empty_like(dout), dz=torch.empty_like(dout) if z is not None else None,
+             dweight=rstd.new_empty((dim,)) if want_dweight else None)
+    l = lib()
+    nbytes = l.ss_gated_norm_bwd_workspace_bytes(rows, dim, groups) if want_dweight else 0
+    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
+    _check(l.ss_gated_norm_bwd(
+        dout.data_ptr(), x.data_ptr(), _ptr(z), zs, _ptr(weight), rstd.data_ptr(),
+        1 if gate_first else 0, _ptr(g["dx"]), _ptr(g["dz"]), _ptr(g["dweight"]), rows, dim,
+        groups, code, ws, ws_len, _raw_stream(dev)))
+    return g
+
+
+def dropout(x, p, rng, out=None, stream=None):
+    """Dropout with a mask that is never stored (ss_dropout): out is x / (1 - p) where the element
+    is kept and 0 where it is dropped, each with probability p (rounded to a multiple of 2^-16).
+    x: (..., dim) float32 or bfloat16; rng: (2,) int64 on the device, a seed and an offset, read
+    when the kernel runs.  The mask depends on rng and the element's place alone: the gradient is
+    dropout(dout, p, rng), and rms_norm_fwd with the same rng drops the same elements.  Advance the
+    offset between draws that are to be independent."""
+    if _elsewhere(x, stream):
+        return _moved(dropout, x, stream, (x, p, rng), dict(out=out))
+    code = _io_code(x)
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    dim = x.shape[-1]
+    rows = x.numel() // dim if dim else 0
+    _expect(x.device, x.dtype, x.shape, ("x", x), ("out", out))
+    if rng is None:
+        raise ValueError("dropout needs rng, the generator's seed and offset")
+    seed = _rng(p, rng, x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    _check(lib().ss_dropout(x.data_ptr(), out.data_ptr(), p, seed, rows, dim, code,
+                            _raw_stream(x.device)))
     return out

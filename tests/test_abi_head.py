@@ -1,0 +1,187 @@
+"""CPU checks of the entry points around the multi-head scan: bad arguments are refused before
+anything is launched (no compute call is made here; the addresses are never dereferenced)."""
+import os
+
+import pytest
+import torch
+
+from selective_state_space_36_amd import ops
+from tests.test_abi_block import call
+
+G = 1 << 34
+BAD, UNS = ops.SS_ERR_INVALID_ARG, ops.SS_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ops.LIB_PATH):
+        from selective_state_space_36_amd import build
+        build.build()
+    return ops.lib()
+
+
+BWD = dict(x=G, dt=2 * G, A=3 * G, B=4 * G, C=5 * G, D=None, z=None, db=None, sp=1, h0=None,
+           dout=6 * G, dhl=None, dx=7 * G, ddt=8 * G, dz=None, dA=9 * G, dB=10 * G, dC=11 * G,
+           dD=None, ddb=None, dh0=None, batch=2, L=100, H=6, P=32, Gr=2, N=16,
+           dtype=ops.SS_BF16, ws=12 * G, wsb=1 << 30, stream=None)
+STEP = dict(state=G, x=2 * G, dt=3 * G, A=4 * G, B=5 * G, C=6 * G, D=None, z=None, db=None, sp=1,
+            out=7 * G, batch=2, H=6, P=32, Gr=2, N=16, dtype=ops.SS_BF16, stream=None)
+CSTEP = dict(state=G, cs=2 * G, xbc=3 * G, xs=1000, w=4 * G, b=None, k=4, dt=5 * G, ds=6,
+             A=6 * G, D=None, z=None, zs=0, db=None, sp=1, out=7 * G, batch=2, H=6, P=32, Gr=2,
+             N=16, dtype=ops.SS_BF16, ws=8 * G, wsb=1 << 30, stream=None)
+NFWD = dict(x=G, res=None, w=None, sc=None, br=0, p=0.0, rng=None, eps=1e-5, out=2 * G, sum=None,
+            rstd=None, brstd=None, rows=4, dim=32, dtype=ops.SS_BF16, stream=None)
+NBWD = dict(dout=G, s=2 * G, sdt=ops.SS_F32, w=None, rstd=3 * G, x=4 * G, sc=None, br=0,
+            brstd=None, p=0.0, rng=None, dsum=None, dx=5 * G, dres=None, dw=6 * G, dsc=None,
+            rows=4, dim=32, dtype=ops.SS_BF16, ws=7 * G, wsb=1 << 30, stream=None)
+GFWD = dict(x=G, z=2 * G, zs=40, w=None, first=1, eps=1e-5, out=3 * G, rstd=None, rows=4, dim=32,
+            groups=2, dtype=ops.SS_BF16, stream=None)
+GBWD = dict(dout=G, x=2 * G, z=3 * G, zs=40, w=None, rstd=4 * G, first=1, dx=5 * G, dz=6 * G,
+            dw=7 * G, rows=4, dim=32, groups=2, dtype=ops.SS_BF16, ws=8 * G, wsb=1 << 30,
+            stream=None)
+DROP = dict(x=G, out=2 * G, p=0.1, rng=3 * G, rows=4, dim=32, dtype=ops.SS_BF16, stream=None)
+
+REFUSED = [
+    ("ss_scan2_bwd", BWD, dict(dtype=7), UNS, b"dtype"),
+    ("ss_scan2_bwd", BWD, dict(batch=-1), BAD, b"negative"),
+    ("ss_scan2_bwd", BWD, dict(N=0), UNS, b"d_state=0"),
+    ("ss_scan2_bwd", BWD, dict(N=257), UNS, b"d_state=257"),
+    ("ss_scan2_bwd", BWD, dict(Gr=4), BAD, b"multiple of ngroups"),
+    ("ss_scan2_bwd", BWD, dict(Gr=0), BAD, b"multiple of ngroups"),
+    ("ss_scan2_bwd", BWD, dict(L=1 << 31), UNS, b"seqlen"),
+    ("ss_scan2_bwd", BWD, dict(P=(1 << 24) + 1), UNS, b"headdim"),
+    ("ss_scan2_bwd", BWD, dict(batch=1 << 40, L=1 << 30), BAD, b"overflow"),
+    ("ss_scan2_bwd", BWD, dict(batch=1 << 30, Gr=1 << 23, H=1 << 23), BAD, b"overflow"),
+    ("ss_scan2_bwd", BWD, dict(batch=1 << 22, H=6), BAD, b"one launch"),
+    ("ss_scan2_bwd", BWD, dict(x=None), BAD, b"x is NULL"),
+    ("ss_scan2_bwd", BWD, dict(dt=None), BAD, b"dt is NULL"),
+    ("ss_scan2_bwd", BWD, dict(A=None), BAD, b"A is NULL"),
+    ("ss_scan2_bwd", BWD, dict(B=None), BAD, b"B is NULL"),
+    ("ss_scan2_bwd", BWD, dict(dout=None), BAD, b"dout is NULL"),
+    ("ss_scan2_bwd", BWD, dict(dx=None), BAD, b"dx is NULL"),
+    ("ss_scan2_bwd", BWD, dict(ddt=None), BAD, b"ddt is NULL"),
+    ("ss_scan2_bwd", BWD, dict(dA=None), BAD, b"dA is NULL"),
+    ("ss_scan2_bwd", BWD, dict(dC=None), BAD, b"dC is NULL"),
+    ("ss_scan2_bwd", BWD, dict(z=13 * G), BAD, b"dz is NULL"),
+    ("ss_scan2_bwd", BWD, dict(x=G + 1), UNS, b"aligned"),
+    ("ss_scan2_bwd", BWD, dict(dA=9 * G + 2), UNS, b"aligned"),
+    ("ss_scan2_bwd", BWD, dict(dx=G), BAD, b"dx overlaps x"),
+    ("ss_scan2_bwd", BWD, dict(dB=11 * G), BAD, b"dB overlaps dC"),
+    ("ss_scan2_bwd", BWD, dict(dhl=14 * G, dh0=14 * G), BAD, b"dh0 overlaps dh_last"),
+    ("ss_scan2_bwd", BWD, dict(ws=None, wsb=0), BAD, b"workspace"),
+    ("ss_scan2_bwd", BWD, dict(wsb=8), BAD, b"workspace"),
+    ("ss_scan2_bwd", BWD, dict(ws=12 * G + 8), UNS, b"16-byte"),
+    ("ss_scan2_bwd", BWD, dict(ws=7 * G), BAD, b"overlaps"),
+    ("ss_scan2_state_update", STEP, dict(dtype=3), UNS, b"dtype"),
+    ("ss_scan2_state_update", STEP, dict(state=None), BAD, b"state is NULL"),
+    ("ss_scan2_state_update", STEP, dict(C=None), BAD, b"C is NULL"),
+    ("ss_scan2_state_update", STEP, dict(out=G), BAD, b"state overlaps out"),
+    ("ss_scan2_state_update", STEP, dict(out=2 * G), BAD, b"out overlaps x"),
+    ("ss_scan2_state_update", STEP, dict(state=G + 2), UNS, b"aligned"),
+    ("ss_scan2_state_update", STEP, dict(Gr=5), BAD, b"multiple of ngroups"),
+    ("ss_scan2_state_update", STEP, dict(batch=1 << 24), BAD, b"one launch"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(k=0), UNS, b"conv_k=0"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(k=5), UNS, b"conv_k=5"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(xs=255), BAD, b"xbc_stride=255"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(ds=5), BAD, b"dt_stride=5"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(z=9 * G, zs=191), BAD, b"z_stride=191"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(xs=1 << 60), BAD, b"overflow"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(cs=None), BAD, b"conv_state is NULL"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(w=None), BAD, b"conv_weight is NULL"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(out=3 * G + 2400), BAD, b"out overlaps xbc"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(cs=G), BAD, b"state overlaps conv_state"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(ws=None, wsb=0), BAD, b"workspace"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(wsb=2047), BAD, b"workspace"),
+    ("ss_scan2_state_update_conv", CSTEP, dict(ws=3 * G), BAD, b"workspace overlaps xbc"),
+    ("ss_rms_norm_fwd", NFWD, dict(rows=-1), BAD, b"negative"),
+    ("ss_rms_norm_fwd", NFWD, dict(eps=-1.0), BAD, b"eps"),
+    ("ss_rms_norm_fwd", NFWD, dict(eps=float("nan")), BAD, b"eps"),
+    ("ss_rms_norm_fwd", NFWD, dict(p=-0.1), BAD, b"probability"),
+    ("ss_rms_norm_fwd", NFWD, dict(p=1.5), BAD, b"probability"),
+    ("ss_rms_norm_fwd", NFWD, dict(p=float("nan")), BAD, b"probability"),
+    ("ss_rms_norm_fwd", NFWD, dict(p=0.1), BAD, b"rng is NULL"),
+    ("ss_rms_norm_fwd", NFWD, dict(p=0.1, rng=G + 4), UNS, b"aligned"),
+    ("ss_rms_norm_fwd", NFWD, dict(x=None), BAD, b"x is NULL"),
+    ("ss_rms_norm_fwd", NFWD, dict(out=G), BAD, b"out overlaps x"),
+    ("ss_rms_norm_fwd", NFWD, dict(res=3 * G, sum=3 * G), BAD, b"sum overlaps residual"),
+    ("ss_rms_norm_fwd", NFWD, dict(dim=(1 << 24) + 1), UNS, b"dim"),
+    ("ss_rms_norm_fwd", NFWD, dict(rows=1 << 31, dim=1), BAD, b"too many rows"),
+    ("ss_rms_norm_bwd", NBWD, dict(dx=None), BAD, b"both NULL"),
+    ("ss_rms_norm_bwd", NBWD, dict(sdt=ops.SS_BF16, dtype=ops.SS_F32), UNS, b"s is either"),
+    ("ss_rms_norm_bwd", NBWD, dict(x=None, dsc=8 * G), BAD, b"x is NULL"),
+    ("ss_rms_norm_bwd", NBWD, dict(x=None, br=1, brstd=8 * G), BAD, b"x is NULL"),
+    ("ss_rms_norm_bwd", NBWD, dict(br=1), BAD, b"branch_rstd is NULL"),
+    ("ss_rms_norm_bwd", NBWD, dict(p=0.1), BAD, b"rng is NULL"),
+    ("ss_rms_norm_bwd", NBWD, dict(dw=G), BAD, b"dweight overlaps dout"),
+    ("ss_rms_norm_bwd", NBWD, dict(dres=5 * G), BAD, b"dx overlaps dresidual"),
+    ("ss_rms_norm_bwd", NBWD, dict(wsb=16), BAD, b"workspace"),
+    ("ss_gated_norm_fwd", GFWD, dict(groups=0), BAD, b"multiple of groups"),
+    ("ss_gated_norm_fwd", GFWD, dict(groups=3), BAD, b"multiple of groups"),
+    ("ss_gated_norm_fwd", GFWD, dict(zs=31), BAD, b"z_stride=31"),
+    ("ss_gated_norm_fwd", GFWD, dict(out=2 * G + 200), BAD, b"out overlaps z"),
+    ("ss_gated_norm_fwd", GFWD, dict(dim=1 << 21, groups=1 << 21), BAD, b"too many groups"),
+    ("ss_gated_norm_fwd", GFWD, dict(rows=1 << 30, groups=32), BAD, b"too many groups"),
+    ("ss_gated_norm_bwd", GBWD, dict(dz=None), BAD, b"dz is NULL"),
+    ("ss_gated_norm_bwd", GBWD, dict(rstd=None), BAD, b"rstd is NULL"),
+    ("ss_gated_norm_bwd", GBWD, dict(dx=G), BAD, b"dx overlaps dout"),
+    ("ss_gated_norm_bwd", GBWD, dict(ws=None, wsb=0), BAD, b"workspace"),
+    ("ss_dropout", DROP, dict(p=2.0), BAD, b"probability"),
+    ("ss_dropout", DROP, dict(rng=None), BAD, b"rng is NULL"),
+    ("ss_dropout", DROP, dict(p=0.0, rng=None), BAD, b"rng is NULL"),
+    ("ss_dropout", DROP, dict(out=G + 4), BAD, b"out overlaps x"),
+    ("ss_dropout", DROP, dict(out=3 * G), BAD, b"out overlaps rng"),
+    ("ss_dropout", DROP, dict(x=None), BAD, b"x is NULL"),
+]
+
+
+@pytest.mark.parametrize("name,defaults,kw,status,text", REFUSED,
+                         ids=[f"{n[3:]}-{'-'.join(k)}-{t.decode()}" for n, _, k, _, t in REFUSED])
+def test_refusals(lib, name, defaults, kw, status, text):
+    assert call(lib, name, defaults, **kw) == status
+    assert text in lib.ss_last_error()
+
+
+def test_empty_problems_succeed_without_a_launch(lib):
+    for name, defaults, kw in (("ss_scan2_bwd", BWD, dict(H=0)),
+                               ("ss_scan2_state_update", STEP, dict(batch=0)),
+                               ("ss_scan2_state_update", STEP, dict(P=0)),
+                               ("ss_scan2_state_update_conv", CSTEP, dict(batch=0)),
+                               ("ss_rms_norm_fwd", NFWD, dict(rows=0)),
+                               ("ss_rms_norm_fwd", NFWD, dict(dim=0)),
+                               ("ss_rms_norm_bwd", NBWD, dict(dim=0)),
+                               ("ss_gated_norm_fwd", GFWD, dict(rows=0)),
+                               ("ss_gated_norm_fwd", GFWD, dict(dim=0)),
+                               ("ss_gated_norm_bwd", GBWD, dict(dim=0)),
+                               ("ss_dropout", DROP, dict(rows=0)),
+                               ("ss_dropout", DROP, dict(dim=0))):
+        assert call(lib, name, defaults, **kw) == ops.SS_OK, name
+        assert lib.ss_last_error() == b""
+
+
+def test_sizes_queries(lib):
+    for q in (lambda: lib.ss_scan2_bwd_workspace_bytes(0, 5, 8, 4, 1, 4, 1),
+              lambda: lib.ss_scan2_bwd_workspace_bytes(2, 5, 8, 4, 3, 4, 1),
+              lambda: lib.ss_scan2_bwd_workspace_bytes(2, 5, 8, 4, 1, 300, 1),
+              lambda: lib.ss_scan2_bwd_workspace_bytes(1 << 40, 1 << 30, 8, 4, 1, 4, 1),
+              lambda: lib.ss_scan2_state_update_conv_workspace_bytes(0, 8, 4, 1, 4),
+              lambda: lib.ss_rms_norm_bwd_workspace_bytes(0, 8),
+              lambda: lib.ss_rms_norm_bwd_workspace_bytes(4, 1 << 25),
+              lambda: lib.ss_gated_norm_bwd_workspace_bytes(4, 8, 3),
+              lambda: lib.ss_gated_norm_bwd_workspace_bytes(0, 8, 2)):
+        assert q() == 0
+    assert lib.ss_scan2_state_update_conv_workspace_bytes(2, 8, 4, 1, 5) == 2 * (32 + 10) * 4
+    # states before and adjoints behind every 64 steps
+    assert lib.ss_scan2_bwd_workspace_bytes(2, 65, 8, 4, 1, 5, 1) >= 2 * 2 * 2 * 8 * 20 * 4
+
+
+def test_the_binding_refuses_host_tensors():
+    x, A = torch.zeros(1, 2, 4, 4), torch.zeros(4)
+    v, rng = torch.zeros(2, 4), torch.zeros(2, dtype=torch.int64)
+    for f in (lambda: ops.scan2_bwd(x, x[..., 0], A, x, x, x),
+              lambda: ops.scan2_state_update(x, x[0], v, A, x[0], x[0]),
+              lambda: ops.scan2_state_update_conv(x, x, v, v, A, v, A),
+              lambda: ops.rms_norm_fwd(v), lambda: ops.rms_norm_bwd(v, v, None, A),
+              lambda: ops.gated_norm_fwd(v), lambda: ops.gated_norm_bwd(v, v, None, None, A),
+              lambda: ops.dropout(v, 0.1, rng)):
+        with pytest.raises(ValueError, match="GPU tensor"):
+            f()

@@ -1,0 +1,393 @@
+"""The RMS norm with the scaled and dropped-out residual add, the gated norm and dropout on the GPU,
+forward and gradients, against float64."""
+import numpy as np
+import pytest
+
+from oracle import head_twin as ht
+from tests.block_helpers import DTYPES, Guarded, check, gpu
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from selective_state_space_36_amd import ops
+    ops.lib()
+    yield
+
+
+def ops():
+    from selective_state_space_36_amd import ops as o
+    return o
+
+
+def rng_of(seed, offset):
+    return torch.tensor([seed, offset], dtype=torch.int64, device="cuda")
+
+
+class Norm:
+    def __init__(self, seed, rows, dim, io, residual=True, scale=True, branch=False, p=0.0,
+                 weight=True, offset=0):
+        print(f"  case rows={rows} dim={dim} {io} residual={residual} scale={scale} "
+              f"branch={branch} p={p}", flush=True)
+        r = np.random.default_rng(seed)
+        n = lambda *s: r.standard_normal(s)  # noqa: E731
+        self.io, self.branch, self.p = io, branch, p
+        self.x, self.vx = gpu(n(rows, dim), io, offset)
+        self.w, self.vw = gpu(1 + 0.1 * n(dim) if weight else None, "f32", offset)
+        self.sc, self.vsc = gpu(0.5 + 0.1 * n(dim) if scale else None, "f32", offset)
+        self.res, self.vres = gpu(3 * n(rows, dim) if residual else None, "f32", offset)
+        self.dout, self.vdout = gpu(n(rows, dim), io, offset)
+        self.dsum, self.vdsum = gpu(n(rows, dim) if residual else None)
+        self.seed = (seed * 0x9E3779B97F4A7C15 % (1 << 63), (1 << 40) + seed)
+        self.rng = rng_of(*self.seed) if p else None
+        self.keep = ht.keep_mask(self.seed, rows, dim, p) if p else None
+        self.summed = residual or scale or branch or bool(p)
+
+    def run(self):
+        o = ops()
+        kw = dict(scale=self.sc, norm_branch=self.branch, p=self.p, rng=self.rng)
+        r = o.rms_norm_fwd(self.x, self.w, residual=self.res, return_stats=True, **kw)
+        out, total, rstd, rb = r if self.summed else (r[0], None, *r[1:])
+        g = o.rms_norm_bwd(self.dout, total if self.summed else self.x, self.w, rstd, x=self.x,
+                           branch_rstd=rb, dsum=self.dsum, want_dresidual=True, **kw)
+        return out, total, rstd, rb, g
+
+    def check(self):
+        out, total, rstd, rb, g = self.run()
+        kw = dict(scale=self.vsc, norm_branch=self.branch, keep=self.keep, p=self.p)
+        want, v, r, vb, _ = ht.rms_fwd(self.vx, self.vw, self.vres, **kw)
+        check(out, want, self.io, "out")
+        if self.summed:
+            check(total, v, "f32", "sum")
+        check(rstd, r, "f32", "rstd")
+        if self.branch:
+            check(rb, vb, "f32", "branch_rstd")
+        want = ht.rms_bwd(self.vdout, self.vx, self.vw, self.vres, dsum=self.vdsum, **kw)
+        check(g["dx"], want["dx"], self.io, "dx")
+        check(g["dresidual"], want["dresidual"], "f32", "dresidual")
+        check(g["dweight"], want["dweight"], "f32", "dweight")
+        if self.sc is not None:
+            check(g["dscale"], want["dscale"], "f32", "dscale")
+        else:
+            assert g["dscale"] is None
+
+
+SIZES = [(1, 1), (1, 2560), (3, 2), (5, 63), (4, 64), (7, 100), (2, 768), (33, 130), (9, 1027),
+         (300, 96), (3, 4096), (2, 5121), (5, 8200), (2, 20001), (600, 3601), (3, 16384),
+         (40, 520), (70, 8), (3, 1024), (2, 16385)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("branch", [False, True])
+@pytest.mark.parametrize("rows,dim", SIZES)
+def test_norm(rows, dim, branch, io):
+    Norm(rows * 10 + dim, rows, dim, io, branch=branch).check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("scale", [False, True])
+@pytest.mark.parametrize("branch", [False, True])
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_norm_options(residual, scale, branch, p, io):
+    Norm(1, 6, 200, io, residual, scale, branch, p, weight=not scale).check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,dim", [(1, 1), (5, 63), (9, 1027), (3, 2560), (2, 9000), (2, 17000)])
+def test_norm_with_dropout(rows, dim, io):
+    Norm(rows + dim, rows, dim, io, branch=True, p=0.1).check()
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_norm_misaligned(offset, io):
+    Norm(offset, 5, 256, io, offset=offset).check()
+    Norm(offset, 3, 17000, io, offset=offset).check()
+
+
+@pytest.mark.parametrize("rows,dim", [((1 << 23) + 7, 2), (4100, 8193), (2100, 16390)])
+def test_norm_more_rows_than_workgroups(rows, dim):
+    o = ops()
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    x = torch.randn(rows, dim, device="cuda", generator=g).bfloat16()
+    out, rstd, _ = o.rms_norm_fwd(x, return_stats=True)
+    dx = o.rms_norm_bwd(x, x, None, rstd)["dx"]
+    for a, b in ((0, 9), (rows // 2, rows // 2 + 9), (rows - 9, rows)):
+        alone, r, _ = o.rms_norm_fwd(x[a:b].contiguous(), return_stats=True)
+        assert torch.equal(out[a:b], alone) and torch.equal(rstd[a:b], r)
+        d = o.rms_norm_bwd(x[a:b].contiguous(), x[a:b].contiguous(), None, r)["dx"]
+        assert torch.equal(dx[a:b], d)
+
+
+def test_norm_of_a_fully_dropped_branch():
+    """p = 1 leaves the residual alone, whatever the branch holds; without one every row is 0."""
+    o = ops()
+    x = torch.full((3, 100), float("nan"), device="cuda")
+    res = torch.randn(3, 100, device="cuda")
+    out, s = o.rms_norm_fwd(x, residual=res, p=1.0, rng=rng_of(1, 2))
+    alone, s0 = o.rms_norm_fwd(torch.zeros_like(x), residual=res)
+    assert torch.equal(out, alone) and torch.equal(s, res)
+    out, s = o.rms_norm_fwd(x, p=1.0, rng=rng_of(1, 2))
+    assert torch.all(out == 0) and torch.all(s == 0)
+
+
+def test_norm_rows_keep_to_themselves():
+    """An infinity or a NaN in one row stays there."""
+    o = ops()
+    c = Norm(5, 7, 300, "bf16", p=0.0)
+    out, total, rstd, _, g = c.run()
+    c.x[2, 5], c.x[4, 299] = float("inf"), float("nan")
+    bad = c.run()
+    good = [0, 1, 3, 5, 6]
+    assert torch.equal(out[good], bad[0][good]) and torch.equal(g["dx"][good], bad[4]["dx"][good])
+
+
+@pytest.mark.parametrize("rows,dim", [(0, 8), (3, 0)])
+def test_norm_empty(rows, dim):
+    o = ops()
+    x, w = torch.zeros(rows, dim, device="cuda"), torch.ones(dim, device="cuda")
+    out, s, rstd, _ = o.rms_norm_fwd(x, w, scale=w, return_stats=True)
+    assert out.shape == x.shape and rstd.shape == (rows,) and bool(rstd.isnan().all())
+    g = o.rms_norm_bwd(x, s, w, rstd, x=x, scale=w)
+    assert torch.all(g["dweight"] == 0) and torch.all(g["dscale"] == 0)
+
+
+# ------------------------------------------------------------------------------------- gated norm
+
+
+class Gated:
+    def __init__(self, seed, rows, dim, groups, io, first, gate=True, weight=True, extra=3,
+                 offset=0):
+        print(f"  case rows={rows} dim={dim} groups={groups} {io} first={first} gate={gate}",
+              flush=True)
+        r = np.random.default_rng(seed)
+        n = lambda *s: r.standard_normal(s)  # noqa: E731
+        self.io, self.kw = io, dict(groups=groups, gate_first=first)
+        self.x, self.vx = gpu(n(rows, dim), io, offset)
+        z, vz = gpu(n(rows, dim + extra), io, offset)
+        self.z, self.vz = (z[:, :dim], vz[:, :dim]) if gate else (None, None)
+        self.w, self.vw = gpu(1 + 0.1 * n(dim) if weight else None, "f32", offset)
+        self.dout, self.vdout = gpu(n(rows, dim), io, offset)
+
+    def check(self):
+        o = ops()
+        out, rstd = o.gated_norm_fwd(self.x, self.z, self.w, return_stats=True, **self.kw)
+        want, r = ht.gated_fwd(self.vx, self.vz, self.vw, **self.kw)
+        check(out, want, self.io, "out")
+        check(rstd, r, "f32", "rstd")
+        g = o.gated_norm_bwd(self.dout, self.x, self.z, self.w, rstd, **self.kw)
+        want = ht.gated_bwd(self.vdout, self.vx, self.vz, self.vw, **self.kw)
+        check(g["dx"], want["dx"], self.io, "dx")
+        if self.z is not None:
+            check(g["dz"], want["dz"], self.io, "dz")
+        check(g["dweight"], want["dweight"], "f32", "dweight")
+
+
+GROUPED = [(1, 1, 1), (128, 5120, 1), (3, 5120, 80), (700, 640, 10), (33, 96, 3), (9, 1539, 3),
+           (50, 35, 7), (20, 2048, 2), (4, 3000, 3), (3, 20000, 1), (2, 66000, 4), (5, 12, 12),
+           (300, 512, 2), (17, 1200, 5), (2, 16400, 2), (11, 33000, 2), (800, 24, 3),
+           (600, 16500, 3)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("rows,dim,groups", GROUPED)
+def test_gated_norm(rows, dim, groups, first, io):
+    if rows * dim > 3_000_000 and io == "f32":
+        rows //= 3
+    Gated(rows + dim, rows, dim, groups, io, first).check()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("first", [False, True])
+def test_gated_norm_options(first, io):
+    Gated(1, 6, 200, 2, io, first, gate=False).check()
+    Gated(2, 6, 200, 2, io, first, weight=False).check()
+    Gated(3, 2, 40000, 2, io, first, gate=False, weight=False).check()
+    for offset in (1, 2, 3):
+        Gated(4, 6, 264, 3, io, first, extra=0, offset=offset).check()
+
+
+def test_gated_norm_extreme_gates():
+    """silu is 0 where the gate is far below 0, z far above: no NaN but where the formula has one."""
+    o = ops()
+    x = torch.ones(2, 16, device="cuda")
+    z = torch.full((2, 16), -1e4, device="cuda")
+    z[1] = 1e4
+    out, rstd = o.gated_norm_fwd(x, z, return_stats=True)
+    assert torch.all(out[0] == 0) and torch.allclose(out[1], torch.ones(16, device="cuda"))
+    g = o.gated_norm_bwd(x, x, z, None, rstd)
+    assert all(torch.isfinite(g[k]).all() for k in ("dx", "dz", "dweight"))
+
+
+def test_gated_norm_of_many_rows():
+    o = ops()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rows, dim = 40000, 640
+    x, z = (torch.randn(rows, dim, device="cuda", generator=gen).bfloat16() for _ in range(2))
+    for groups in (1, 5, 10):
+        out, rstd = o.gated_norm_fwd(x, z, groups=groups, return_stats=True)
+        g = o.gated_norm_bwd(x, x, z, None, rstd, groups=groups)
+        for a in (0, 20001, rows - 7):
+            cut = slice(a, a + 7)
+            c = lambda t: t[cut].contiguous()  # noqa: E731
+            o1, r1 = o.gated_norm_fwd(c(x), c(z), groups=groups, return_stats=True)
+            g1 = o.gated_norm_bwd(c(x), c(x), c(z), None, r1, groups=groups)
+            assert torch.equal(out[cut], o1) and torch.equal(g["dx"][cut], g1["dx"])
+            assert torch.equal(g["dz"][cut], g1["dz"])
+        hat = (out.float() * x.float()).double().sum(0)      # dweight of dout = x
+        size = (out.float() * x.float()).double().abs().sum(0)
+        assert torch.all((g["dweight"].double() - hat).abs() <= 2 ** -8 * size)
+
+
+@pytest.mark.parametrize("lead", [(), (4,), (2, 3)])
+def test_leading_axes(lead):
+    o = ops()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, z = (torch.randn(*lead, 48, device="cuda", generator=gen) for _ in range(2))
+    rows = x.numel() // 48
+    out, rstd = o.gated_norm_fwd(x, z, groups=3, return_stats=True)
+    flat = o.gated_norm_fwd(x.view(rows, 48), z.view(rows, 48), groups=3)
+    assert out.shape == x.shape and rstd.shape == (*lead, 3)
+    assert torch.equal(out.view(rows, 48), flat)
+    out, rstd, none = o.rms_norm_fwd(x, return_stats=True)
+    assert rstd.shape == lead and none is None
+    d = o.dropout(x, 0.5, rng_of(1, 2))
+    assert torch.equal(d.view(rows, 48), o.dropout(x.view(rows, 48), 0.5, rng_of(1, 2)))
+
+
+# ---------------------------------------------------------------------------------------- dropout
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("p", [0.0, 2.0 ** -16, 0.1, 0.5, 0.999, 1.0])
+@pytest.mark.parametrize("rows,dim", [(1, 1), (3, 7), (5, 8), (70, 9), (20, 255), (2, 5000)])
+def test_dropout(rows, dim, p, io):
+    o = ops()
+    x, vx = gpu(np.random.default_rng(rows).standard_normal((rows, dim)), io)
+    seed = (0x7FFFFFFFFFFFFFF1, -5)     # the offset's bits are taken as they are
+    out = o.dropout(x, p, rng_of(*seed))
+    keep = ht.keep_mask(seed, rows, dim, p)
+    want = ht.drop(ht.Bounded(vx), keep, p)
+    check(out, want, io, "out")
+    assert np.array_equal(out.cpu().float().numpy() != 0, keep & (vx != 0))
+
+
+def test_dropout_drops_infinities_and_nans():
+    o = ops()
+    x = torch.full((50, 64), float("nan"), device="cuda")
+    x[:25] = float("inf")
+    out = o.dropout(x, 0.5, rng_of(3, 4))
+    keep = torch.from_numpy(ht.keep_mask((3, 4), 50, 64, 0.5)).cuda()
+    assert torch.all(out[~keep] == 0)
+    assert torch.all(out[:25][keep[:25]] == float("inf")) and out[25:][keep[25:]].isnan().all()
+
+
+def test_dropout_of_a_large_array():
+    """Every workgroup walks the array: a row equals its row of a smaller call of the same rows."""
+    o = ops()
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(5000, 4099, device="cuda", generator=gen).bfloat16()
+    out = o.dropout(x, 0.3, rng_of(9, 1))
+    assert torch.equal(out[:100], o.dropout(x[:100].contiguous(), 0.3, rng_of(9, 1)))
+    mask = torch.from_numpy(ht.keep_mask((9, 1), 2, 4099, 0.3)).cuda()
+    assert torch.equal(out[:2] != 0, mask & (x[:2] != 0))
+    share = float((out != 0).float().mean())
+    assert abs(share - 0.7) < 5 * (0.21 / x.numel()) ** 0.5 + 2 ** -16
+    # the kept elements are scaled by the probability that is used, a multiple of 2^-16
+    kept = out != 0
+    up = 65536 / (65536 - round(0.3 * 65536))
+    torch.testing.assert_close(out[kept].float(), x[kept].float() * up, rtol=2 ** -8, atol=0)
+
+
+def test_the_norm_drops_what_dropout_drops():
+    o = ops()
+    x = torch.randn(37, 1001, device="cuda")
+    rng = rng_of(12345, 678)
+    _, s = o.rms_norm_fwd(x, p=0.25, rng=rng)
+    assert torch.equal(s, o.dropout(x, 0.25, rng))
+
+
+def test_rows_past_32_bit_offsets():
+    o = ops()
+    rows, dim = (1 << 20) + 3, 2100
+    x = torch.ones(rows, dim, dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 1 << 31
+    out = o.dropout(x, 0.5, rng_of(1, 1))
+    row = rows - 1
+    bits = [(ht.philox((c, row, 1, 0), (1, 0))[j // 2] >> (16 * (j % 2))) & 0xFFFF
+            for c in range(3) for j in range(8)]
+    want = torch.tensor([2.0 if b >= 32768 else 0.0 for b in bits])
+    assert torch.equal(out[row, :24].float().cpu(), want)
+    del out
+    n, rstd = o.gated_norm_fwd(x, None, return_stats=True)
+    assert torch.all(n[-3:] == 1) and torch.all(rstd[-3:] > 0.99)
+    g = o.gated_norm_bwd(x, x, None, None, rstd, want_dweight=False)
+    assert torch.all(g["dx"][-3:].abs() < 1e-4)
+
+
+def test_writes_stay_inside():
+    o = ops()
+    for rows, dim, groups in ((3, 37, 1), (33, 1024, 8), (2, 17001, 3), (5, 2561, 1)):
+        for dt in (torch.float32, torch.bfloat16):
+            x = torch.randn(rows, dim, device="cuda").to(dt)
+            a, b, c = (Guarded((rows, dim), d) for d in (dt, torch.float32, dt))
+            o.rms_norm_fwd(x, residual=x.float(), out=a.t, sum_out=b.t, p=0.5, rng=rng_of(1, 1))
+            o.dropout(x, 0.5, rng_of(1, 1), out=c.t)
+            assert a.intact() and b.intact() and c.intact()
+            o.gated_norm_fwd(x, x, groups=groups, out=a.t)
+            assert a.intact()
+            l, code = o.lib(), o._IO[dt]
+            rstd = torch.ones(rows, groups, device="cuda")
+            dw, ds = (Guarded((dim,), torch.float32) for _ in range(2))
+            n = l.ss_gated_norm_bwd_workspace_bytes(rows, dim, groups)
+            ws = Guarded((n,), torch.uint8)
+            s = torch.cuda.current_stream().cuda_stream
+            p = lambda t: t.data_ptr()  # noqa: E731
+            assert l.ss_gated_norm_bwd(p(x), p(x), p(x), dim, None, p(rstd), 1, p(a.t), p(c.t),
+                                       p(dw.t), rows, dim, groups, code, p(ws.t), n, s) == 0
+            torch.cuda.synchronize()
+            assert a.intact() and c.intact() and dw.intact() and ws.intact()
+            n = l.ss_rms_norm_bwd_workspace_bytes(rows, dim)
+            ws = Guarded((n,), torch.uint8)
+            one = torch.ones(dim, device="cuda")
+            assert l.ss_rms_norm_bwd(p(x), p(b.t), 0, None, p(rstd), p(x), p(one), 1, p(rstd), 0.0,
+                                     None, None, p(a.t), None, p(dw.t),
+                                     p(ds.t), rows, dim, code, p(ws.t), n, s) == 0
+            torch.cuda.synchronize()
+            assert a.intact() and dw.intact() and ds.intact() and ws.intact()
+
+
+def test_the_binding_refuses():
+    o = ops()
+    x = torch.randn(4, 16, device="cuda")
+    rng = rng_of(1, 2)
+    w = torch.ones(16, device="cuda")
+    for f, err in (
+            (lambda: o.dropout(x, 0.1, None), "rng"),
+            (lambda: o.dropout(x, -0.1, rng), "probability"),
+            (lambda: o.dropout(x, 0.1, rng.int()), "must be"),
+            (lambda: o.dropout(x, 0.1, rng.cpu()), "is on"),
+            (lambda: o.dropout(x.t(), 0.1, rng), "contiguous"),
+            (lambda: o.dropout(x.half(), 0.1, rng), "float32 or bfloat16"),
+            (lambda: o.rms_norm_fwd(x, p=0.1), "rng"),
+            (lambda: o.rms_norm_fwd(x, w[:15]), "shape"),
+            (lambda: o.rms_norm_fwd(x, residual=x.bfloat16()), "must be"),
+            (lambda: o.rms_norm_bwd(x, x, w, w[:4], scale=w), "x is needed"),
+            (lambda: o.rms_norm_bwd(x, x, w, w[:4], x=x, norm_branch=True), "branch_rstd"),
+            (lambda: o.gated_norm_fwd(x, x[:, :8]), "shape"),
+            (lambda: o.gated_norm_fwd(x, x.t().contiguous().t()), "contiguous"),
+            (lambda: o.gated_norm_fwd(x, x[:1].expand(4, 16)), "overlap"),
+            (lambda: o.gated_norm_bwd(x, x, x, w, w[:4].view(4, 1), groups=2), "shape")):
+        with pytest.raises((ValueError, TypeError), match=err):
+            f()
+    with pytest.raises(o.SSError, match="groups"):
+        o.gated_norm_fwd(x, groups=3)
+    with pytest.raises(o.SSError, match="overlaps"):
+        o.dropout(x, 0.1, rng, out=x)
