@@ -15,7 +15,8 @@ SOURCES = ["ss_api.hip", "ss_scan_fwd.hip", "ss_scan_zoh.hip", "ss_scan_conv.hip
            "ss_scan_conv_zoh.hip", "ss_state_update.hip", "ss_scan_bwd.hip", "ss_scan2.hip",
            "ss_scan2_mfma.hip", "ss_block_api.hip", "ss_block_util.hip", "ss_gated_fwd.hip",
            "ss_gated_bwd.hip", "ss_gated_step.hip", "ss_norm.hip", "ss_conv.hip", "ss_head_api.hip",
-           "ss_rms_norm.hip", "ss_dropout.hip", "ss_scan2_step.hip", "ss_scan2_bwd.hip"]
+           "ss_rms_norm.hip", "ss_dropout.hip", "ss_scan2_step.hip", "ss_scan2_bwd.hip",
+           "ss_scan2_bwd_mfma.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are disabled (-packed-fp32-ops); the host pass warns that it

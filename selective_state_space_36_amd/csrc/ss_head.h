@@ -136,6 +136,11 @@ int64_t scan2_bwd_ws_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64
                             int64_t ngroups, int64_t d_state, Scan2BwdArgs* a, float* ws);
 hipError_t launch_scan2_bwd(const Scan2BwdArgs& a, bool bf16, hipStream_t stream);
 
+// Its first two launches with bf16 matrix products (ss_scan2_bwd_mfma.hip): bf16 io, headdim 64,
+// d_state 64 or 128, 16-byte aligned arrays.
+bool scan2_bwd_mfma_supported(const Scan2BwdArgs& a, bool bf16);
+hipError_t launch_scan2_bwd_mfma(const Scan2BwdArgs& a, hipStream_t stream);
+
 hipError_t launch_dropout(const void* x, void* out, const DropArgs& d, int64_t rows, int64_t dim,
                           bool bf16, hipStream_t stream);
 

@@ -581,7 +581,8 @@ template <class IO>
 hipError_t launch_io(const Scan2BwdArgs& a, hipStream_t stream) {
   using E = typename IO::elem;
   hipError_t e;
-  switch ((a.d_state + kQ - 1) / kQ) {
+  if (scan2_bwd_mfma_supported(a, sizeof(E) == 2)) e = launch_scan2_bwd_mfma(a, stream);
+  else switch ((a.d_state + kQ - 1) / kQ) {
     case 1: e = launch_nb<IO, 1>(a, stream); break;
     case 2: e = launch_nb<IO, 2>(a, stream); break;
     case 3: e = launch_nb<IO, 3>(a, stream); break;
@@ -610,10 +611,10 @@ int64_t round16(int64_t floats) { return (floats + 3) / 4 * 4; }
 
 }  // namespace
 
-// Runs of heads: enough workgroups to fill the chip (one fits a CU), at most a head each.
+// Runs of heads: a workgroup for each of the 256 CUs (one fits a CU), at most a head each.
 int64_t scan2_bwd_splits(int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngroups) {
   const int64_t units = batch * ((seqlen + kQ - 1) / kQ) * ngroups, hg = nheads / ngroups;
-  const int64_t want = (512 + units - 1) / units;
+  const int64_t want = (256 + units - 1) / units;
   return want < hg ? want : hg;
 }
 

@@ -1,0 +1,700 @@
+// ss_scan2_bwd_mfma.hip -- gradients of the multi-head scan for bf16, headdim 64 and 64 or 128
+// states: the formulas and launches of ss_scan2_bwd.hip, with the products on the bf16 matrix
+// instruction.
+//
+// x, B and C are bf16 and enter the products exactly.  The float32 operands (gy, M, the states and
+// their adjoints, w X, e^c gy) are split into bf16 high and low parts, v = hi + lo to about 2^-17,
+// and take a product each; hi lo + lo hi + hi hi where both operands are split.  Products that have
+// K down the rows of a tile read it with the LDS transpose read, so every tile is staged once.
+//
+// The states cross from the first launch to the second as such pairs, one 32-bit word per value,
+// laid out as the first one holds them: [d_state / 16][channel][16 states].
+#include "ss_head.h"
+#include "ss_mfma.h"
+
+namespace ss {
+namespace {
+
+constexpr int kQ = kScan2BwdChunk;
+constexpr int kP = 64;
+constexpr int kPS = kP + 8;   // bf16 per row of the (step, channel) and (step, step) tiles: 36
+                              // dwords, so that the four rows of a transpose read and the sixteen
+                              // of a 16-byte read start in different banks
+
+// Inclusive sum of the log2 decays in float64, as float32 high and low parts: differences of them
+// are exponents, whose error is a relative one of the result.
+struct Step {
+  float raw, dt;
+  float c_hi, c_lo;
+  float before, after, end;  // 2^{c}, 2^{c_end - c}, 2^{c_end}
+};
+__device__ __forceinline__ double scan64(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const double o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ Step step_of(uint16_t dt, bool in, float bias, float A, bool softplus,
+                                        int lane) {
+  Step s;
+  s.raw = BF16::widen(dt) + bias;
+  s.dt = in ? (softplus ? softplus_f(s.raw) : s.raw) : 0.0f;
+  const double c = scan64(static_cast<double>(s.dt) * A * 1.4426950408889634, lane);
+  const double end = __shfl(c, 63);
+  s.c_hi = static_cast<float>(c);
+  s.c_lo = static_cast<float>(c - s.c_hi);
+  s.before = exp2_hw(s.c_hi) * (1.0f + s.c_lo * kLn2);
+  s.after = exp2_hw(static_cast<float>(end - c));
+  s.end = exp2_hw(static_cast<float>(end));
+  return s;
+}
+
+// A pair of bf16 in a word, high part above, and back.
+__device__ __forceinline__ void pair4(f32x4 v, uint4& w) {
+  uint32_t h0, h1, l0, l1;
+  split2(v[0], v[1], h0, l0);
+  split2(v[2], v[3], h1, l1);
+  w.x = __builtin_amdgcn_perm(h0, l0, 0x05040100);
+  w.y = __builtin_amdgcn_perm(h0, l0, 0x07060302);
+  w.z = __builtin_amdgcn_perm(h1, l1, 0x05040100);
+  w.w = __builtin_amdgcn_perm(h1, l1, 0x07060302);
+}
+__device__ __forceinline__ uint2 highs(uint4 w) {
+  return make_uint2(__builtin_amdgcn_perm(w.y, w.x, 0x07060302),
+                    __builtin_amdgcn_perm(w.w, w.z, 0x07060302));
+}
+__device__ __forceinline__ uint2 lows(uint4 w) {
+  return make_uint2(__builtin_amdgcn_perm(w.y, w.x, 0x05040100),
+                    __builtin_amdgcn_perm(w.w, w.z, 0x05040100));
+}
+__device__ __forceinline__ float of_pair(uint32_t w) { return hi_f(w) + lo_f(w); }
+
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
+}
+
+// ------------------------------------------------------------------ the states
+
+template <int N>
+struct alignas(16) StateSmem {
+  uint16_t in[kQ][N + 16];        // B or C, (step, state)
+  uint16_t hi[kQ][kPS], lo[kQ][kPS];  // weighted x or gy, (step, channel)
+  float weight[2][kQ];
+};
+
+// One workgroup per (batch row, head) and direction; wave w owns channels 16 w .. 16 w + 15.
+template <int N>
+__global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) {
+  constexpr int NT = N / 16;
+  constexpr int UNITS = 2 * N, UPT = (UNITS + 255) / 256;  // (4-step, 8-state) pieces
+  __shared__ StateSmem<N> sm;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t pairs = p.batch * p.nheads;
+  const bool back = blockIdx.x >= pairs;
+  const int64_t bh = xcd_remap(back ? blockIdx.x - pairs : blockIdx.x, pairs);
+  const int64_t b = bh / p.nheads, h = bh - b * p.nheads, grp = h / (p.nheads / p.ngroups);
+  const int64_t L = p.seqlen, nc = p.n_chunks, H = p.nheads, gn = p.ngroups * N, hp = H * kP;
+  const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
+  const uint16_t* in = static_cast<const uint16_t*>(back ? p.C : p.B) + b * L * gn + grp * N;
+  const uint16_t* row = static_cast<const uint16_t*>(back ? p.dout : p.x) + b * L * hp + h * kP;
+  const uint16_t* zrow =
+      back && p.z ? static_cast<const uint16_t*>(p.z) + b * L * hp + h * kP : nullptr;
+  const uint16_t* dtg = static_cast<const uint16_t*>(p.dt) + b * L * H + h;
+  uint4* ws = reinterpret_cast<uint4*>(back ? p.lam : p.states) + bh * nc * (N * kP / 4);
+  const float* init = back ? p.dh_last : p.h0;
+  const int rq = tid >> 4, rp = tid & 15;  // this thread's 4 steps x 4 channels of the rows
+
+  uint2 xr[4], zr[4];
+  uint4 ir[UPT][4];
+  uint16_t dtr = 0;
+  auto fetch = [&](int64_t ch) {
+    const int64_t t0 = ch * kQ, left = L - t0;
+    const int nv = static_cast<int>(left < kQ ? left : kQ);
+    dtr = lane < nv ? dtg[(t0 + lane) * H] : 0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = 4 * rq + r;
+      const int64_t o = (t0 + t) * hp + 4 * rp;
+      xr[r] = t < nv ? *reinterpret_cast<const uint2*>(row + o) : make_uint2(0, 0);
+      if (zrow) zr[r] = t < nv ? *reinterpret_cast<const uint2*>(zrow + o) : make_uint2(0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < UPT; ++k) {
+      const int u = tid + 256 * k, tq = u / (N / 8), nb = u % (N / 8);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 4 * tq + r;
+        ir[k][r] = u < UNITS && t < nv
+                       ? *reinterpret_cast<const uint4*>(in + (t0 + t) * gn + 8 * nb)
+                       : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  // w_s = dt e^{c_end - c_s} forward, e^{c_t} backward; the same bits from every wave
+  float decay = 1.0f;
+  auto weigh = [&](int64_t ch, int buf) {
+    const Step s = step_of(dtr, ch * kQ + lane < L, bias, A, p.softplus, lane);
+    decay = s.end;
+    sm.weight[buf][lane] = back ? s.before : s.after * s.dt;
+  };
+
+  f32x4 S[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      S[nt][r] = init ? init[(bh * N + 16 * nt + 4 * g4 + r) * kP + 16 * wv + l16] : 0.0f;
+
+  fetch(back ? nc - 1 : 0);
+  weigh(back ? nc - 1 : 0, 0);
+  for (int64_t k = 0; k < nc; ++k) {
+    const int64_t ch = back ? nc - 1 - k : k;
+    __syncthreads();  // the previous chunk's tiles have been read, this one's weights are there
+#pragma unroll
+    for (int u8 = 0; u8 < UPT; ++u8) {
+      const int u = tid + 256 * u8, tq = u / (N / 8), nb = u % (N / 8);
+      if (UNITS % 256 == 0 || u < UNITS) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<uint4*>(&sm.in[4 * tq + r][8 * nb]) = ir[u8][r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float w = sm.weight[k & 1][4 * rq + r];
+      float v[4] = {lo_f(xr[r].x), hi_f(xr[r].x), lo_f(xr[r].y), hi_f(xr[r].y)};
+      if (zrow) {
+        const float z[4] = {lo_f(zr[r].x), hi_f(zr[r].x), lo_f(zr[r].y), hi_f(zr[r].y)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] *= z[j] * sigmoid_f(z[j]);
+      }
+      uint2 h2, l2;
+      split2(v[0] * w, v[1] * w, h2.x, l2.x);
+      split2(v[2] * w, v[3] * w, h2.y, l2.y);
+      *reinterpret_cast<uint2*>(&sm.hi[4 * rq + r][4 * rp]) = h2;
+      *reinterpret_cast<uint2*>(&sm.lo[4 * rq + r][4 * rp]) = l2;
+    }
+    // the state before the chunk leaves before the next loads are issued, which would be waited
+    // for together with it
+    uint4* out = ws + ch * (N * kP / 4) + (16 * wv + l16) * 4 + g4;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint4 w;
+      pair4(S[nt], w);
+      out[nt * kP * 4] = w;
+    }
+    const float d = decay;
+    const bool more = k + 1 < nc;
+    const int64_t next = back ? ch - 1 : ch + 1;
+    if (more) fetch(next);
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) S[nt] *= d;
+#pragma unroll
+    for (int kb = 0; kb < kQ; kb += 32) {
+      const Op whi = op_down(&sm.hi[0][0], kPS, kb, 16 * wv, l16, g4);
+      const Op wlo = op_down(&sm.lo[0][0], kPS, kb, 16 * wv, l16, g4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const Op a = op_down(&sm.in[0][0], N + 16, kb, 16 * nt, l16, g4);
+        S[nt] = mfma(a, whi, S[nt]);
+        S[nt] = mfma(a, wlo, S[nt]);
+      }
+    }
+    if (more) weigh(next, (k + 1) & 1);
+    lds_reads_done();
+  }
+  if (back && p.dh0) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        p.dh0[(bh * N + 16 * nt + 4 * g4 + r) * kP + 16 * wv + l16] = S[nt][r];
+  }
+}
+
+// ------------------------------------------------------------------ the chunks
+
+constexpr int kThreads = 512;  // eight waves, one workgroup on a CU
+
+template <int N>
+struct alignas(16) ChunkSmem {
+  uint16_t b[kQ][N + 16], c[kQ][N + 16];         // B and C, (step, state)
+  uint16_t shi[kP][N + 8], slo[kP][N + 8];       // S_in, (channel, state)
+  uint16_t lhi[kP][N + 8], llo[kP][N + 8];       // lam_out
+  uint16_t x[kQ][kPS];                           // (step, channel)
+  uint16_t ghi[kQ][kPS], glo[kQ][kPS];           // gy
+  uint16_t mhi[kQ][kPS], mlo[kQ][kPS];           // M dt_s, (t, s); at the end K
+  float dt[kQ], c_hi[kQ], c_lo[kQ], before[kQ], after[kQ];
+  // sums for dl and ddt, by the tile they come from: E / dt over t and over s (strictly below the
+  // diagonal), the diagonal of W M, q, p / dt
+  float ecol[4][kQ], erow[4][kQ], ediag[kQ], near[4][kQ], far[4][kQ];
+  float over[kThreads / 64], diag[4];
+};
+
+// Sum over the four 16-lane rows of a wave.
+__device__ __forceinline__ float sum_rows(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ float sum16(float v) {
+  v += row_ror<8>(v);
+  v += row_ror<4>(v);
+  v += row_ror<2>(v);
+  return v + row_ror<1>(v);
+}
+__device__ __forceinline__ float sum64(float v) { return sum_rows(sum16(v)); }
+
+template <int N, bool GATE>
+__global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArgs p) {
+  constexpr int SK = N * kP / 4 / kThreads;  // 16-byte pieces of a state per thread
+  constexpr int TPW = N / 32;                // tiles of dB and dC per wave
+  __shared__ ChunkSmem<N> sm;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t nc = p.n_chunks, L = p.seqlen, H = p.nheads, hp = H * kP, gn = p.ngroups * N;
+  int64_t w = blockIdx.x;
+  const int64_t split = w % p.splits;
+  w /= p.splits;
+  const int64_t grp = w % p.ngroups;
+  w /= p.ngroups;
+  const int64_t ch = w % nc, b = w / nc, t0 = ch * kQ;
+  const int rows = L - t0 < kQ ? static_cast<int>(L - t0) : kQ;
+  const int64_t hg = H / p.ngroups;
+  const int64_t h_beg = grp * hg + split * hg / p.splits,
+                h_end = grp * hg + (split + 1) * hg / p.splits;
+
+  // B and C of the chunk, and the zeros that are never written again
+  {
+    const uint16_t* Bg = static_cast<const uint16_t*>(p.B) + (b * L + t0) * gn + grp * N;
+    const uint16_t* Cg = static_cast<const uint16_t*>(p.C) + (b * L + t0) * gn + grp * N;
+    for (int u = tid; u < kQ * N / 8; u += kThreads) {
+      const int t = u / (N / 8), n = 8 * (u % (N / 8));
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(&sm.b[t][n]) =
+          t < rows ? *reinterpret_cast<const uint4*>(Bg + t * gn + n) : none;
+      *reinterpret_cast<uint4*>(&sm.c[t][n]) =
+          t < rows ? *reinterpret_cast<const uint4*>(Cg + t * gn + n) : none;
+    }
+    uint4* m = reinterpret_cast<uint4*>(&sm.mhi[0][0]);
+    for (int i = tid; i < 2 * kQ * kPS * 2 / 16; i += kThreads) m[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < 4 * kQ; i += kThreads) (&sm.ecol[0][0])[i] = (&sm.erow[0][0])[i] = 0.0f;
+  }
+  __syncthreads();
+
+  // The causal 16x16 tiles (s-tile ti <= t-tile tj), dealt to the waves in the order (0,0) (0,1)
+  // (1,1) (0,2) ...: lane (l16, g4) holds steps s = 16 ti + 4 g4 + r and t = 16 tj + l16.
+  int ti[2], tj[2];
+  f32x4 G[2] = {}, K[2] = {};  // B C^T of them, and the sum of K over the heads
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = wv + 8 * i;
+    tj[i] = (k >= 1) + (k >= 3) + (k >= 6);
+    ti[i] = k - tj[i] * (tj[i] + 1) / 2;
+    if (k < 10) {
+#pragma unroll
+      for (int kb = 0; kb < N; kb += 32)
+        G[i] = mfma(op_along(&sm.b[0][0], N + 16, 16 * ti[i], kb, l16, g4),
+                    op_along(&sm.c[0][0], N + 16, 16 * tj[i], kb, l16, g4), G[i]);
+    }
+  }
+  const int mine = wv < 2 ? 2 : 1;
+  // Y and V are formed transposed (rows: channels, columns: steps): wave w has channels
+  // 16 (w / 2).. and the steps of two tiles that balance each other's causal products.
+  const int pt = wv >> 1, jt[2] = {wv & 1, 3 - (wv & 1)};
+  // dB and dC transposed as well (rows: states): a tile of states and TPW tiles of steps.
+  const int nt = N == 128 ? wv : wv >> 1, j0 = N == 128 ? 0 : 2 * (wv & 1);
+  f32x4 dC[TPW] = {}, dB[TPW] = {};
+
+  // A head's inputs on their way: 16-byte pieces of the states, 8 channels of one step of the rows
+  uint4 sr[SK], lr[SK], xr, gr, zr;
+  uint16_t dtr = 0;
+  const int r8 = tid >> 3, c8 = (tid & 7) * 8;
+  // (buffer resources: a row past the last step reads as 0, and an access costs one offset)
+  const uint32_t row_bytes = static_cast<uint32_t>(hp * 2);
+  const uint32_t tile_bytes = static_cast<uint32_t>(rows - 1) * row_bytes + kP * 2;
+  const uint32_t row_off = r8 * row_bytes + c8 * 2;
+  uint32_t out_off[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    out_off[i] = (16 * jt[i] + l16) * row_bytes + (16 * pt + 4 * g4) * 2;
+  auto fetch = [&](int64_t h) {
+    const int64_t o = (b * L + t0) * hp + h * kP;
+    dtr = lane < rows ? static_cast<const uint16_t*>(p.dt)[(b * L + t0 + lane) * H + h] : 0;
+    xr = buf_load<uint4>(make_buf(static_cast<const uint16_t*>(p.x) + o, tile_bytes), row_off);
+    gr = buf_load<uint4>(make_buf(static_cast<const uint16_t*>(p.dout) + o, tile_bytes), row_off);
+    if (GATE)
+      zr = buf_load<uint4>(make_buf(static_cast<const uint16_t*>(p.z) + o, tile_bytes), row_off);
+    const int64_t at = ((b * H + h) * nc + ch) * (N * kP);
+    const rsrc_t sp = make_buf(p.states + at, N * kP * 4), lp = make_buf(p.lam + at, N * kP * 4);
+#pragma unroll
+    for (int k = 0; k < SK; ++k) {
+      sr[k] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(sp, tid * 16, k * kThreads * 16, 0));
+      lr[k] = __builtin_bit_cast(
+          uint4, __builtin_amdgcn_raw_buffer_load_b128(lp, tid * 16, k * kThreads * 16, 0));
+    }
+  };
+
+  // dl, ddt and the head's sums from what the products left (one wave)
+  auto finish = [&](int64_t h, const Step& st) {
+    const float q = (sm.near[0][lane] + sm.near[1][lane]) + (sm.near[2][lane] + sm.near[3][lane]);
+    const float f = (sm.far[0][lane] + sm.far[1][lane]) + (sm.far[2][lane] + sm.far[3][lane]);
+    const float col = (sm.ecol[0][lane] + sm.ecol[1][lane]) + (sm.ecol[2][lane] + sm.ecol[3][lane]);
+    const float row = (sm.erow[0][lane] + sm.erow[1][lane]) + (sm.erow[2][lane] + sm.erow[3][lane]);
+    const float xv = f + (col + sm.ediag[lane]);
+    float ov = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kThreads / 64; ++k) ov += sm.over[k];
+    // inclusive sums; what lies strictly before a step is the sum less its own
+    const double in = static_cast<double>(st.dt) * col - row, ps = static_cast<double>(st.dt) * f;
+    const double before = scan64(in + ps, lane) - (in + ps);
+    const double since = __shfl(scan64(__shfl(static_cast<double>(q), 63 - lane), lane), 63 - lane);
+    const float dl = static_cast<float>(before + since + static_cast<double>(st.end) * ov);
+    float ddt = fmaf(p.A[h], dl, xv);
+    if (p.softplus) ddt *= sigmoid_f(st.raw);
+    if (lane < rows)
+      static_cast<uint16_t*>(p.ddt)[(b * L + t0 + lane) * H + h] = BF16::from_float(ddt);
+    else
+      ddt = 0.0f;
+    const float sa = sum64(st.dt * dl), sb = sum64(ddt);
+    if (lane == 0) {
+      float* line = p.head_part + (b * nc + ch) * 3 * H + h;
+      line[0] = sa;
+      line[H] = (sm.diag[0] + sm.diag[1]) + (sm.diag[2] + sm.diag[3]);
+      line[2 * H] = sb;
+    }
+  };
+
+  if (h_beg < h_end) fetch(h_beg);
+  Step st{};
+  const int lane16 = l16, lane4 = g4;
+  for (int64_t h = h_beg; h < h_end; ++h) {
+    // (hides that the lane's places in the tiles stay the same from head to head: the compiler
+    // would keep some sixty addresses in registers, and spill; a spilled value's reload waits for
+    // the loads of the next head, which were issued before it)
+    int l16 = lane16, g4 = lane4;
+    asm volatile("" : "+v"(l16), "+v"(g4));
+    const float Dh = p.D ? p.D[h] : 0.0f;
+    __syncthreads();  // the previous head's tiles have been read, its sums are there
+    if (wv == 7 && h > h_beg) finish(h - 1, st);
+    if (wv == 0 || wv == 7)
+      st = step_of(dtr, lane < rows, p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h], p.softplus, lane);
+    if (wv == 0) {
+      sm.dt[lane] = st.dt;
+      sm.c_hi[lane] = st.c_hi;
+      sm.c_lo[lane] = st.c_lo;
+      sm.before[lane] = st.before;
+      sm.after[lane] = st.after;
+    }
+    float over = 0.0f;
+#pragma unroll
+    for (int k = 0; k < SK; ++k) {
+      const int u = tid + kThreads * k, ch16 = (u >> 2) & (kP - 1), n = 16 * (u >> 8) + 4 * (u & 3);
+      *reinterpret_cast<uint2*>(&sm.shi[ch16][n]) = highs(sr[k]);
+      *reinterpret_cast<uint2*>(&sm.slo[ch16][n]) = lows(sr[k]);
+      *reinterpret_cast<uint2*>(&sm.lhi[ch16][n]) = highs(lr[k]);
+      *reinterpret_cast<uint2*>(&sm.llo[ch16][n]) = lows(lr[k]);
+      const uint32_t a[4] = {sr[k].x, sr[k].y, sr[k].z, sr[k].w};
+      const uint32_t c[4] = {lr[k].x, lr[k].y, lr[k].z, lr[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) over = fmaf(of_pair(a[j]), of_pair(c[j]), over);
+    }
+    *reinterpret_cast<uint4*>(&sm.x[r8][c8]) = xr;
+    {
+      const uint32_t gw[4] = {gr.x, gr.y, gr.z, gr.w}, zw[4] = {zr.x, zr.y, zr.z, zr.w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a = lo_f(gw[j]), c = hi_f(gw[j]);
+        if (GATE) {
+          const float za = lo_f(zw[j]), zc = hi_f(zw[j]);
+          a *= za * sigmoid_f(za);
+          c *= zc * sigmoid_f(zc);
+        }
+        split2(a, c, hi[j], lo[j]);
+      }
+      *reinterpret_cast<uint4*>(&sm.ghi[r8][c8]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(&sm.glo[r8][c8]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    __syncthreads();  // the tiles are there
+    // z and dout again for the epilogue, in its layout (they lie in the caches); then the next head
+    uint2 ze[2], ge[2];
+    if (GATE) {
+      const int64_t o = (b * L + t0) * hp + h * kP;
+      const rsrc_t rz = make_buf(static_cast<const uint16_t*>(p.z) + o, tile_bytes);
+      const rsrc_t rg = make_buf(static_cast<const uint16_t*>(p.dout) + o, tile_bytes);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ze[i] = buf_load<uint2>(rz, out_off[i]);
+        ge[i] = buf_load<uint2>(rg, out_off[i]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);  // in this order: loads are waited for in theirs
+    if (h + 1 < h_end) fetch(h + 1);
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- W = X gy^T over the causal tiles; M dt to LDS, K into its sum, the sums of E
+    over = sum64(over);
+    if (lane == 0) sm.over[wv] = over;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i >= mine) continue;
+      f32x4 W = {};
+#pragma unroll
+      for (int kb = 0; kb < kP; kb += 32) {
+        const Op a = op_along(&sm.x[0][0], kPS, 16 * ti[i], kb, l16, g4);
+        W = mfma(a, op_along(&sm.ghi[0][0], kPS, 16 * tj[i], kb, l16, g4), W);
+        W = mfma(a, op_along(&sm.glo[0][0], kPS, 16 * tj[i], kb, l16, g4), W);
+      }
+      const int t = 16 * tj[i] + l16, s0 = 16 * ti[i] + 4 * g4;
+      const float cth = sm.c_hi[t], ctl = sm.c_lo[t];
+      float m[4], row = 0.0f, col[4], dg = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int s = s0 + r;
+        const float dts = sm.dt[s];
+        const float seg = s <= t ? exp2_hw((cth - sm.c_hi[s]) + (ctl - sm.c_lo[s])) : 0.0f;
+        const float g = s <= t ? G[i][r] * seg : 0.0f;
+        const float e = s <= t ? W[r] * g : 0.0f;
+        K[i][r] += s <= t ? W[r] * seg * dts : 0.0f;
+        m[r] = g * dts;
+        row += s < t ? e * dts : 0.0f;
+        col[r] = s < t ? e : 0.0f;
+        if (s == t) {
+          sm.ediag[t] = e;
+          dg += W[r];
+        }
+      }
+      uint2 h2, l2;
+      split2(m[0], m[1], h2.x, l2.x);
+      split2(m[2], m[3], h2.y, l2.y);
+      *reinterpret_cast<uint2*>(&sm.mhi[t][s0]) = h2;
+      *reinterpret_cast<uint2*>(&sm.mlo[t][s0]) = l2;
+      row = sum_rows(row);
+      if (g4 == 0) sm.erow[ti[i]][t] = row;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        col[r] = sum16(col[r]);
+        if (l16 == r) sm.ecol[tj[i]][s0 + r] = col[r];
+      }
+      if (ti[i] == tj[i]) {
+        dg = sum64(dg);
+        if (lane == 0) sm.diag[ti[i]] = dg;
+      }
+    }
+
+    // ---- S_in^T C^T and lam_out^T B^T
+    f32x4 Y[2] = {}, V[2] = {};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+    for (int kb = 0; kb < N; kb += 32) {
+      const Op sh = op_along(&sm.shi[0][0], N + 8, 16 * pt, kb, l16, g4);
+      const Op sl = op_along(&sm.slo[0][0], N + 8, 16 * pt, kb, l16, g4);
+      const Op lh = op_along(&sm.lhi[0][0], N + 8, 16 * pt, kb, l16, g4);
+      const Op ll = op_along(&sm.llo[0][0], N + 8, 16 * pt, kb, l16, g4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const Op c = op_along(&sm.c[0][0], N + 16, 16 * jt[i], kb, l16, g4);
+        Y[i] = mfma(sh, c, Y[i]);
+        Y[i] = mfma(sl, c, Y[i]);
+        const Op bo = op_along(&sm.b[0][0], N + 16, 16 * jt[i], kb, l16, g4);
+        V[i] = mfma(lh, bo, V[i]);
+        V[i] = mfma(ll, bo, V[i]);
+      }
+    }
+    // ---- S_in gy^T and lam_out X^T, scaled by their steps into dC and dB
+    {
+      f32x4 T[TPW] = {};
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+      for (int kb = 0; kb < kP; kb += 32) {
+        const Op sh = op_down(&sm.shi[0][0], N + 8, kb, 16 * nt, l16, g4);
+        const Op sl = op_down(&sm.slo[0][0], N + 8, kb, 16 * nt, l16, g4);
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+          const Op gh = op_along(&sm.ghi[0][0], kPS, 16 * (j0 + j), kb, l16, g4);
+          const Op gl = op_along(&sm.glo[0][0], kPS, 16 * (j0 + j), kb, l16, g4);
+          T[j] = mfma(sh, gh, T[j]);
+          T[j] = mfma(sl, gh, T[j]);
+          T[j] = mfma(sh, gl, T[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < TPW; ++j) {
+        const float e = sm.before[16 * (j0 + j) + l16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dC[j][r] = fmaf(e, T[j][r], dC[j][r]);
+      }
+    }
+    {
+      f32x4 U[TPW] = {};
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll 1
+      for (int kb = 0; kb < kP; kb += 32) {
+        const Op lh = op_down(&sm.lhi[0][0], N + 8, kb, 16 * nt, l16, g4);
+        const Op ll = op_down(&sm.llo[0][0], N + 8, kb, 16 * nt, l16, g4);
+#pragma unroll
+        for (int j = 0; j < TPW; ++j) {
+          const Op xo = op_along(&sm.x[0][0], kPS, 16 * (j0 + j), kb, l16, g4);
+          U[j] = mfma(lh, xo, U[j]);
+          U[j] = mfma(ll, xo, U[j]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < TPW; ++j) {
+        const int t = 16 * (j0 + j) + l16;
+        const float wt = sm.after[t] * sm.dt[t];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) dB[j][r] = fmaf(wt, U[j][r], dB[j][r]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();  // M is there
+
+    // ---- the carried parts scaled and summed, then the chunk's own: X^T (M dt)^T over s <= t,
+    // gy^T (M dt) over t >= s
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int j = jt[i], t = 16 * j + l16;
+      const float ev = sm.before[t], av = sm.after[t], dts = sm.dt[t];
+      const int c0 = 16 * pt + 4 * g4;
+      const uint2 xw = *reinterpret_cast<const uint2*>(&sm.x[t][c0]);
+      const uint2 gh = *reinterpret_cast<const uint2*>(&sm.ghi[t][c0]);
+      const uint2 gl = *reinterpret_cast<const uint2*>(&sm.glo[t][c0]);
+      const float x[4] = {lo_f(xw.x), hi_f(xw.x), lo_f(xw.y), hi_f(xw.y)};
+      const float gy[4] = {lo_f(gh.x) + lo_f(gl.x), hi_f(gh.x) + hi_f(gl.x),
+                           lo_f(gh.y) + lo_f(gl.y), hi_f(gh.y) + hi_f(gl.y)};
+      float near = 0.0f, far = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        Y[i][r] *= ev;
+        V[i][r] *= av;
+        near = fmaf(gy[r], Y[i][r], near);
+        far = fmaf(x[r], V[i][r], far);
+        V[i][r] *= dts;
+      }
+      near = sum_rows(near);
+      far = sum_rows(far);
+      if (g4 == 0) {
+        sm.near[pt][t] = near;
+        sm.far[pt][t] = far;
+      }
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        if (kb <= (j >> 1)) {
+          const Op xo = op_down(&sm.x[0][0], kPS, 32 * kb, 16 * pt, l16, g4);
+          Y[i] = mfma(xo, op_along(&sm.mhi[0][0], kPS, 16 * j, 32 * kb, l16, g4), Y[i]);
+          Y[i] = mfma(xo, op_along(&sm.mlo[0][0], kPS, 16 * j, 32 * kb, l16, g4), Y[i]);
+        }
+        if (kb >= (j >> 1)) {
+          const Op ga = op_down(&sm.ghi[0][0], kPS, 32 * kb, 16 * pt, l16, g4);
+          const Op gb = op_down(&sm.glo[0][0], kPS, 32 * kb, 16 * pt, l16, g4);
+          const Op ma = op_down(&sm.mhi[0][0], kPS, 32 * kb, 16 * j, l16, g4);
+          const Op mb = op_down(&sm.mlo[0][0], kPS, 32 * kb, 16 * j, l16, g4);
+          V[i] = mfma(ga, ma, V[i]);
+          V[i] = mfma(gb, ma, V[i]);
+          V[i] = mfma(ga, mb, V[i]);
+        }
+      }
+      float dx[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dx[r] = fmaf(Dh, gy[r], V[i][r]);
+      const int64_t o = (b * L + t0) * hp + h * kP;
+      store8(make_uint2(pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])),
+             make_buf(static_cast<uint16_t*>(p.dx) + o, tile_bytes), out_off[i]);
+      if (GATE) {
+        const float z[4] = {lo_f(ze[i].x), hi_f(ze[i].x), lo_f(ze[i].y), hi_f(ze[i].y)};
+        const float go[4] = {lo_f(ge[i].x), hi_f(ge[i].x), lo_f(ge[i].y), hi_f(ge[i].y)};
+        float dz[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float sg = sigmoid_f(z[r]);
+          dz[r] = go[r] * fmaf(Dh, x[r], Y[i][r]) * (sg * fmaf(z[r], 1.0f - sg, 1.0f));
+        }
+        store8(make_uint2(pack_bf16(dz[0], dz[1]), pack_bf16(dz[2], dz[3])),
+               make_buf(static_cast<uint16_t*>(p.dz) + o, tile_bytes), out_off[i]);
+      }
+    }
+    lds_reads_done();
+  }
+  __syncthreads();
+  if (wv == 7 && h_beg < h_end) finish(h_end - 1, st);
+
+  // ---- dC^T += B^T K^T, dB^T += C^T K, K (t, s) in M's place
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i >= mine) continue;
+    const int t = 16 * tj[i] + l16, s0 = 16 * ti[i] + 4 * g4;
+    uint2 h2, l2;
+    split2(K[i][0], K[i][1], h2.x, l2.x);
+    split2(K[i][2], K[i][3], h2.y, l2.y);
+    *reinterpret_cast<uint2*>(&sm.mhi[t][s0]) = h2;
+    *reinterpret_cast<uint2*>(&sm.mlo[t][s0]) = l2;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int kb = 0; kb < kQ; kb += 32) {
+    const Op bo = op_down(&sm.b[0][0], N + 16, kb, 16 * nt, l16, g4);
+    const Op co = op_down(&sm.c[0][0], N + 16, kb, 16 * nt, l16, g4);
+#pragma unroll
+    for (int j = 0; j < TPW; ++j) {
+      dC[j] = mfma(bo, op_along(&sm.mhi[0][0], kPS, 16 * (j0 + j), kb, l16, g4), dC[j]);
+      dC[j] = mfma(bo, op_along(&sm.mlo[0][0], kPS, 16 * (j0 + j), kb, l16, g4), dC[j]);
+      dB[j] = mfma(co, op_down(&sm.mhi[0][0], kPS, kb, 16 * (j0 + j), l16, g4), dB[j]);
+      dB[j] = mfma(co, op_down(&sm.mlo[0][0], kPS, kb, 16 * (j0 + j), l16, g4), dB[j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < TPW; ++j) {
+    const int t = 16 * (j0 + j) + l16;
+    if (t >= rows) continue;
+    const int64_t o = ((b * L + t0 + t) * p.ngroups + grp) * N + 16 * nt + 4 * g4;
+    if (p.splits == 1) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dB) + o) =
+          make_uint2(pack_bf16(dB[j][0], dB[j][1]), pack_bf16(dB[j][2], dB[j][3]));
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dC) + o) =
+          make_uint2(pack_bf16(dC[j][0], dC[j][1]), pack_bf16(dC[j][2], dC[j][3]));
+    } else {
+      const int64_t all = p.batch * L * gn;
+      float* q = p.bc_part + split * 2 * all + o;
+      *reinterpret_cast<f32x4*>(q) = dB[j];
+      *reinterpret_cast<f32x4*>(q + all) = dC[j];
+    }
+  }
+}
+
+template <int N>
+hipError_t launch_n(const Scan2BwdArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(scan2_states_mfma_kernel<N>,
+                     dim3(static_cast<unsigned>(2 * a.batch * a.nheads)), dim3(256), 0, stream, a);
+  const dim3 grid(static_cast<unsigned>(a.batch * a.n_chunks * a.ngroups * a.splits));
+  if (a.z)
+    hipLaunchKernelGGL((scan2_chunks_mfma_kernel<N, true>), grid, dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((scan2_chunks_mfma_kernel<N, false>), grid, dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// (a chunk's rows are addressed with 32-bit byte offsets)
+bool scan2_bwd_mfma_supported(const Scan2BwdArgs& a, bool bf16) {
+  const uintptr_t al =
+      reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.z) |
+      reinterpret_cast<uintptr_t>(a.B) | reinterpret_cast<uintptr_t>(a.C) |
+      reinterpret_cast<uintptr_t>(a.dout) | reinterpret_cast<uintptr_t>(a.dx) |
+      reinterpret_cast<uintptr_t>(a.dz) | reinterpret_cast<uintptr_t>(a.dB) |
+      reinterpret_cast<uintptr_t>(a.dC);
+  return bf16 && a.headdim == kP && (a.d_state == 64 || a.d_state == 128) && (al & 15) == 0 &&
+         kQ * a.nheads * kP * 2 < (int64_t(1) << 31);
+}
+
+hipError_t launch_scan2_bwd_mfma(const Scan2BwdArgs& a, hipStream_t stream) {
+  return a.d_state == 64 ? launch_n<64>(a, stream) : launch_n<128>(a, stream);
+}
+
+}  // namespace ss
