@@ -28,21 +28,37 @@ struct Step {
   float c_hi, c_lo;
   float before, after, end;  // 2^{c}, 2^{c_end - c}, 2^{c_end}
 };
-__device__ __forceinline__ double scan64(double v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const double o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
+// x plus the value that the DPP control brings (0 where it brings none), in the rows of the mask.
+template <int CTRL, int ROWS, bool CLEAR>
+__device__ __forceinline__ double dpp_add(double x) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(w), CTRL, ROWS, 0xf, CLEAR);
+  const uint32_t hi =
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(w >> 32), CTRL, ROWS, 0xf, CLEAR);
+  return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
-__device__ __forceinline__ Step step_of(uint16_t dt, bool in, float bias, float A, bool softplus,
-                                        int lane) {
+// Inclusive sum over the 64 lanes, as wave_prefix_sum.
+__device__ __forceinline__ double scan64(double x) {
+  x = dpp_add<0x111, 0xf, true>(x);
+  x = dpp_add<0x112, 0xf, true>(x);
+  x = dpp_add<0x114, 0xf, true>(x);
+  x = dpp_add<0x118, 0xf, true>(x);
+  x = dpp_add<0x142, 0xa, false>(x);
+  return dpp_add<0x143, 0xc, false>(x);
+}
+__device__ __forceinline__ double last_lane(double x) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(w), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(w >> 32), 63);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ Step step_of(uint16_t dt, bool in, float bias, float A,
+                                        bool softplus) {
   Step s;
   s.raw = BF16::widen(dt) + bias;
   s.dt = in ? (softplus ? softplus_f(s.raw) : s.raw) : 0.0f;
-  const double c = scan64(static_cast<double>(s.dt) * A * 1.4426950408889634, lane);
-  const double end = __shfl(c, 63);
+  const double c = scan64(static_cast<double>(s.dt) * A * 1.4426950408889634);
+  const double end = last_lane(c);
   s.c_hi = static_cast<float>(c);
   s.c_lo = static_cast<float>(c - s.c_hi);
   s.before = exp2_hw(s.c_hi) * (1.0f + s.c_lo * kLn2);
@@ -69,7 +85,14 @@ __device__ __forceinline__ uint2 lows(uint4 w) {
   return make_uint2(__builtin_amdgcn_perm(w.y, w.x, 0x05040100),
                     __builtin_amdgcn_perm(w.w, w.z, 0x05040100));
 }
-__device__ __forceinline__ float of_pair(uint32_t w) { return hi_f(w) + lo_f(w); }
+// c + a b of two such pairs: the products of like parts, then of unlike ones.
+__device__ __forceinline__ float dot_pairs(uint32_t a, uint32_t b, float c) {
+  using b2 = __bf16 __attribute__((ext_vector_type(2)));
+  const b2 v = __builtin_bit_cast(b2, a);
+  c = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(b2, b), c, false);
+  return __builtin_amdgcn_fdot2_f32_bf16(
+      v, __builtin_bit_cast(b2, __builtin_amdgcn_alignbit(b, b, 16)), c, false);
+}
 
 __device__ __forceinline__ float sigmoid_f(float z) {
   return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
@@ -136,7 +159,7 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
   // w_s = dt e^{c_end - c_s} forward, e^{c_t} backward; the same bits from every wave
   float decay = 1.0f;
   auto weigh = [&](int64_t ch, int buf) {
-    const Step s = step_of(dtr, ch * kQ + lane < L, bias, A, p.softplus, lane);
+    const Step s = step_of(dtr, ch * kQ + lane < L, bias, A, p.softplus);
     decay = s.end;
     sm.weight[buf][lane] = back ? s.before : s.after * s.dt;
   };
@@ -222,23 +245,32 @@ constexpr int kThreads = 512;  // eight waves, one workgroup on a CU
 
 template <int N>
 struct alignas(16) ChunkSmem {
-  uint16_t b[kQ][N + 16], c[kQ][N + 16];         // B and C, (step, state)
-  uint16_t shi[kP][N + 8], slo[kP][N + 8];       // S_in, (channel, state)
-  uint16_t lhi[kP][N + 8], llo[kP][N + 8];       // lam_out
+  uint16_t b[kQ][N + 8], c[kQ][N + 8];           // B and C, (step, state)
+  // S_in and lam_out, (channel, state)
+  uint16_t shi[kP][N + 8], slo[kP][N + 8];
+  uint16_t lhi[kP][N + 8], llo[kP][N + 8];
   uint16_t x[kQ][kPS];                           // (step, channel)
   uint16_t ghi[kQ][kPS], glo[kQ][kPS];           // gy
   uint16_t mhi[kQ][kPS], mlo[kQ][kPS];           // M dt_s, (t, s); at the end K
   float dt[kQ], c_hi[kQ], c_lo[kQ], before[kQ], after[kQ];
   // sums for dl and ddt, by the tile they come from: E / dt over t and over s (strictly below the
   // diagonal), the diagonal of W M, q, p / dt
-  float ecol[4][kQ], erow[4][kQ], ediag[kQ], near[4][kQ], far[4][kQ];
+  float ecol[4][kQ], erow[4][kQ], ediag[kQ], near[2][kQ], far[2][kQ];
   float over[kThreads / 64], diag[4];
 };
 
-// Sum over the four 16-lane rows of a wave.
+// Sum over the four 16-lane rows of a wave, in each of them: an exchange of odd and even rows, then
+// of halves (both operands the same value: one result holds the first of each pair twice, the other
+// the second).
+__device__ __forceinline__ float sum_halves(float v) {
+  const uint32_t w = __float_as_uint(v);
+  const auto pair = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return __uint_as_float(pair[0]) + __uint_as_float(pair[1]);
+}
 __device__ __forceinline__ float sum_rows(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const uint32_t w = __float_as_uint(v);
+  const auto pair = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  return sum_halves(__uint_as_float(pair[0]) + __uint_as_float(pair[1]));
 }
 __device__ __forceinline__ float sum16(float v) {
   v += row_ror<8>(v);
@@ -248,10 +280,32 @@ __device__ __forceinline__ float sum16(float v) {
 }
 __device__ __forceinline__ float sum64(float v) { return sum_rows(sum16(v)); }
 
+// 32 x 32 tiles: the operand's rows (or columns) are 32 of the tile, lane % 32 each, K = k0 + 8
+// (lane / 32) + 0..7; the result has column lane % 32, and in element 4 q + r row 8 q +
+// 4 (lane / 32) + r.  Half the operand bytes of four 16 x 16 tiles per product.
+using f32x16 = float __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x16 mfma32(const Op& a, const Op& b, f32x16 c) {
+  using u4 = uint32_t __attribute__((ext_vector_type(4)));
+  const u4 av = {a.w[0], a.w[1], a.w[2], a.w[3]};
+  const u4 bv = {b.w[0], b.w[1], b.w[2], b.w[3]};
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, av),
+                                                 __builtin_bit_cast(bf16x8, bv), c, 0, 0, 0);
+}
+__device__ __forceinline__ Op along32(const uint16_t* tile, int stride, int r0, int k0, int lane) {
+  const uint4 v = *reinterpret_cast<const uint4*>(tile + (r0 + (lane & 31)) * stride + k0 +
+                                                  8 * (lane >> 5));
+  return Op{{v.x, v.y, v.z, v.w}};
+}
+__device__ __forceinline__ Op down32(const uint16_t* tile, int stride, int k0, int c0, int lane) {
+  const int k = k0 + 8 * (lane >> 5), c = c0 + (lane & 16), l16 = lane & 15;
+  const uint2 k03 = tr_read4(tile, stride, k, c, l16), k47 = tr_read4(tile, stride, k + 4, c, l16);
+  return Op{{k03.x, k03.y, k47.x, k47.y}};
+}
+
 template <int N, bool GATE>
 __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArgs p) {
   constexpr int SK = N * kP / 4 / kThreads;  // 16-byte pieces of a state per thread
-  constexpr int TPW = N / 32;                // tiles of dB and dC per wave
+  constexpr int TPW = N / 64;                // 32 x 32 tiles of dB or dC per wave
   __shared__ ChunkSmem<N> sm;
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -267,22 +321,27 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
   const int64_t h_beg = grp * hg + split * hg / p.splits,
                 h_end = grp * hg + (split + 1) * hg / p.splits;
 
-  // B and C of the chunk, and the zeros that are never written again
+  // B and C of the chunk
   {
     const uint16_t* Bg = static_cast<const uint16_t*>(p.B) + (b * L + t0) * gn + grp * N;
     const uint16_t* Cg = static_cast<const uint16_t*>(p.C) + (b * L + t0) * gn + grp * N;
     for (int u = tid; u < kQ * N / 8; u += kThreads) {
       const int t = u / (N / 8), n = 8 * (u % (N / 8));
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(&sm.b[t][n]) =
-          t < rows ? *reinterpret_cast<const uint4*>(Bg + t * gn + n) : none;
-      *reinterpret_cast<uint4*>(&sm.c[t][n]) =
-          t < rows ? *reinterpret_cast<const uint4*>(Cg + t * gn + n) : none;
+      uint4 bw = make_uint4(0, 0, 0, 0), cw = bw;
+      if (t < rows) {
+        bw = *reinterpret_cast<const uint4*>(Bg + t * gn + n);
+        cw = *reinterpret_cast<const uint4*>(Cg + t * gn + n);
+      }
+      *reinterpret_cast<uint4*>(&sm.b[t][n]) = bw;
+      *reinterpret_cast<uint4*>(&sm.c[t][n]) = cw;
     }
+  }
+  // the zeros above the diagonal are never written again
+  {
     uint4* m = reinterpret_cast<uint4*>(&sm.mhi[0][0]);
     for (int i = tid; i < 2 * kQ * kPS * 2 / 16; i += kThreads) m[i] = make_uint4(0, 0, 0, 0);
-    for (int i = tid; i < 4 * kQ; i += kThreads) (&sm.ecol[0][0])[i] = (&sm.erow[0][0])[i] = 0.0f;
   }
+  for (int i = tid; i < 4 * kQ; i += kThreads) (&sm.ecol[0][0])[i] = (&sm.erow[0][0])[i] = 0.0f;
   __syncthreads();
 
   // The causal 16x16 tiles (s-tile ti <= t-tile tj), dealt to the waves in the order (0,0) (0,1)
@@ -297,17 +356,20 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     if (k < 10) {
 #pragma unroll
       for (int kb = 0; kb < N; kb += 32)
-        G[i] = mfma(op_along(&sm.b[0][0], N + 16, 16 * ti[i], kb, l16, g4),
-                    op_along(&sm.c[0][0], N + 16, 16 * tj[i], kb, l16, g4), G[i]);
+        G[i] = mfma(op_along(&sm.b[0][0], N + 8, 16 * ti[i], kb, l16, g4),
+                    op_along(&sm.c[0][0], N + 8, 16 * tj[i], kb, l16, g4), G[i]);
     }
   }
   const int mine = wv < 2 ? 2 : 1;
-  // Y and V are formed transposed (rows: channels, columns: steps): wave w has channels
-  // 16 (w / 2).. and the steps of two tiles that balance each other's causal products.
-  const int pt = wv >> 1, jt[2] = {wv & 1, 3 - (wv & 1)};
-  // dB and dC transposed as well (rows: states): a tile of states and TPW tiles of steps.
-  const int nt = N == 128 ? wv : wv >> 1, j0 = N == 128 ? 0 : 2 * (wv & 1);
-  f32x4 dC[TPW] = {}, dB[TPW] = {};
+  // Waves 0 to 3 form Y and dC, waves 4 to 7 V and dB, transposed (rows: channels or states,
+  // columns: steps): a tile of 32 channels and 32 steps each, and TPW tiles of 32 states.
+  const int role = wv >> 2, ph = (wv >> 1) & 1, sh = wv & 1;
+  const int nt = N == 128 ? wv & 3 : ph, j0 = N == 128 ? 0 : sh;
+  const uint16_t* hi_t = role ? &sm.lhi[0][0] : &sm.shi[0][0];  // (channel, state)
+  const uint16_t* lo_t = role ? &sm.llo[0][0] : &sm.slo[0][0];
+  const uint16_t* bc_t = role ? &sm.b[0][0] : &sm.c[0][0];      // (step, state)
+  const uint16_t* by_t = role ? &sm.x[0][0] : &sm.ghi[0][0];    // (step, channel)
+  f32x16 dBC[TPW] = {};
 
   // A head's inputs on their way: 16-byte pieces of the states, 8 channels of one step of the rows
   uint4 sr[SK], lr[SK], xr, gr, zr;
@@ -317,13 +379,21 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
   const uint32_t row_bytes = static_cast<uint32_t>(hp * 2);
   const uint32_t tile_bytes = static_cast<uint32_t>(rows - 1) * row_bytes + kP * 2;
   const uint32_t row_off = r8 * row_bytes + c8 * 2;
-  uint32_t out_off[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    out_off[i] = (16 * jt[i] + l16) * row_bytes + (16 * pt + 4 * g4) * 2;
+  const uint32_t out_off = (32 * sh + (lane & 31)) * row_bytes + (32 * ph + 4 * (lane >> 5)) * 2;
+  // (the head's parameters too: a load that is waited for at once would stand in every head's way)
+  float An = 0.0f, Dn = 0.0f, bn = 0.0f;
+  const uint32_t dt_off = lane * static_cast<uint32_t>(H * 2);
+  const uint32_t dt_bytes = static_cast<uint32_t>((rows - 1) * H * 2) + 2;
+  const rsrc_t ra = make_buf(p.A, static_cast<uint32_t>(H * 4));
+  const rsrc_t rd = make_buf(p.D, p.D ? static_cast<uint32_t>(H * 4) : 0);
+  const rsrc_t rb = make_buf(p.dt_bias, p.dt_bias ? static_cast<uint32_t>(H * 4) : 0);
   auto fetch = [&](int64_t h) {
     const int64_t o = (b * L + t0) * hp + h * kP;
-    dtr = lane < rows ? static_cast<const uint16_t*>(p.dt)[(b * L + t0 + lane) * H + h] : 0;
+    dtr = buf_load<uint16_t>(
+        make_buf(static_cast<const uint16_t*>(p.dt) + (b * L + t0) * H + h, dt_bytes), dt_off);
+    An = buf_load<float>(ra, static_cast<uint32_t>(h * 4));
+    Dn = buf_load<float>(rd, static_cast<uint32_t>(h * 4));
+    bn = buf_load<float>(rb, static_cast<uint32_t>(h * 4));
     xr = buf_load<uint4>(make_buf(static_cast<const uint16_t*>(p.x) + o, tile_bytes), row_off);
     gr = buf_load<uint4>(make_buf(static_cast<const uint16_t*>(p.dout) + o, tile_bytes), row_off);
     if (GATE)
@@ -340,21 +410,21 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
   };
 
   // dl, ddt and the head's sums from what the products left (one wave)
-  auto finish = [&](int64_t h, const Step& st) {
-    const float q = (sm.near[0][lane] + sm.near[1][lane]) + (sm.near[2][lane] + sm.near[3][lane]);
-    const float f = (sm.far[0][lane] + sm.far[1][lane]) + (sm.far[2][lane] + sm.far[3][lane]);
+  auto finish = [&](int64_t h, float A, const Step& st) {
+    const float q = sm.near[0][lane] + sm.near[1][lane];
+    const float f = sm.far[0][lane] + sm.far[1][lane];
     const float col = (sm.ecol[0][lane] + sm.ecol[1][lane]) + (sm.ecol[2][lane] + sm.ecol[3][lane]);
     const float row = (sm.erow[0][lane] + sm.erow[1][lane]) + (sm.erow[2][lane] + sm.erow[3][lane]);
     const float xv = f + (col + sm.ediag[lane]);
     float ov = 0.0f;
 #pragma unroll
     for (int k = 0; k < kThreads / 64; ++k) ov += sm.over[k];
-    // inclusive sums; what lies strictly before a step is the sum less its own
+    // inclusive sums in float64; what lies before a step is the sum less its own
     const double in = static_cast<double>(st.dt) * col - row, ps = static_cast<double>(st.dt) * f;
-    const double before = scan64(in + ps, lane) - (in + ps);
-    const double since = __shfl(scan64(__shfl(static_cast<double>(q), 63 - lane), lane), 63 - lane);
+    const double before = scan64(in + ps) - (in + ps);
+    const double upto = scan64(q), since = last_lane(upto) - (upto - q);
     const float dl = static_cast<float>(before + since + static_cast<double>(st.end) * ov);
-    float ddt = fmaf(p.A[h], dl, xv);
+    float ddt = fmaf(A, dl, xv);
     if (p.softplus) ddt *= sigmoid_f(st.raw);
     if (lane < rows)
       static_cast<uint16_t*>(p.ddt)[(b * L + t0 + lane) * H + h] = BF16::from_float(ddt);
@@ -369,20 +439,23 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     }
   };
 
-  if (h_beg < h_end) fetch(h_beg);
+  fetch(h_beg);
+  float A = 0.0f;
   Step st{};
-  const int lane16 = l16, lane4 = g4;
+  const int lane0 = lane;
   for (int64_t h = h_beg; h < h_end; ++h) {
     // (hides that the lane's places in the tiles stay the same from head to head: the compiler
     // would keep some sixty addresses in registers, and spill; a spilled value's reload waits for
     // the loads of the next head, which were issued before it)
-    int l16 = lane16, g4 = lane4;
-    asm volatile("" : "+v"(l16), "+v"(g4));
-    const float Dh = p.D ? p.D[h] : 0.0f;
+    int lane = lane0;
+    asm volatile("" : "+v"(lane));
+    const int l16 = lane & 15, g4 = lane >> 4, l32 = lane & 31, hi32 = lane >> 5;
     __syncthreads();  // the previous head's tiles have been read, its sums are there
-    if (wv == 7 && h > h_beg) finish(h - 1, st);
+    if (wv == 7 && h > h_beg) finish(h - 1, A, st);
+    const float Dh = Dn;
+    A = An;
     if (wv == 0 || wv == 7)
-      st = step_of(dtr, lane < rows, p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h], p.softplus, lane);
+      st = step_of(dtr, lane < rows, bn, A, p.softplus);
     if (wv == 0) {
       sm.dt[lane] = st.dt;
       sm.c_hi[lane] = st.c_hi;
@@ -401,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       const uint32_t a[4] = {sr[k].x, sr[k].y, sr[k].z, sr[k].w};
       const uint32_t c[4] = {lr[k].x, lr[k].y, lr[k].z, lr[k].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) over = fmaf(of_pair(a[j]), of_pair(c[j]), over);
+      for (int j = 0; j < 4; ++j) over = dot_pairs(a[j], c[j], over);
     }
     *reinterpret_cast<uint4*>(&sm.x[r8][c8]) = xr;
     {
@@ -422,19 +495,21 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     }
     __syncthreads();  // the tiles are there
     // z and dout again for the epilogue, in its layout (they lie in the caches); then the next head
-    uint2 ze[2], ge[2];
-    if (GATE) {
-      const int64_t o = (b * L + t0) * hp + h * kP;
-      const rsrc_t rz = make_buf(static_cast<const uint16_t*>(p.z) + o, tile_bytes);
-      const rsrc_t rg = make_buf(static_cast<const uint16_t*>(p.dout) + o, tile_bytes);
+    uint2 ze[4], ge[4];
+    const int64_t tile0 = (b * L + t0) * hp + h * kP;
+    if (GATE && !role) {
+      const rsrc_t rz = make_buf(static_cast<const uint16_t*>(p.z) + tile0, tile_bytes);
+      const rsrc_t rg = make_buf(static_cast<const uint16_t*>(p.dout) + tile0, tile_bytes);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ze[i] = buf_load<uint2>(rz, out_off[i]);
-        ge[i] = buf_load<uint2>(rg, out_off[i]);
+      for (int q = 0; q < 4; ++q) {
+        ze[q] = buf_load<uint2>(rz, out_off + 16 * q);
+        ge[q] = buf_load<uint2>(rg, out_off + 16 * q);
       }
     }
     __builtin_amdgcn_sched_barrier(0);  // in this order: loads are waited for in theirs
-    if (h + 1 < h_end) fetch(h + 1);
+    // (the last head fetches itself again: the compiler counts loads, and takes what may not have
+    // been issued for what it waits for)
+    fetch(h + 1 < h_end ? h + 1 : h);
     __builtin_amdgcn_sched_barrier(0);
 
     // ---- W = X gy^T over the causal tiles; M dt to LDS, K into its sum, the sums of E
@@ -452,177 +527,162 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       }
       const int t = 16 * tj[i] + l16, s0 = 16 * ti[i] + 4 * g4;
       const float cth = sm.c_hi[t], ctl = sm.c_lo[t];
-      float m[4], row = 0.0f, col[4], dg = 0.0f;
+      const float4 csh = *reinterpret_cast<const float4*>(&sm.c_hi[s0]);
+      const float4 csl = *reinterpret_cast<const float4*>(&sm.c_lo[s0]);
+      const float4 dt4 = *reinterpret_cast<const float4*>(&sm.dt[s0]);
+      const float ch[4] = {csh.x, csh.y, csh.z, csh.w}, cl[4] = {csl.x, csl.y, csl.z, csl.w};
+      const float dts[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
+      float m[4], e[4], row = 0.0f;
+      const bool diag = ti[i] == tj[i];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int s = s0 + r;
-        const float dts = sm.dt[s];
-        const float seg = s <= t ? exp2_hw((cth - sm.c_hi[s]) + (ctl - sm.c_lo[s])) : 0.0f;
-        const float g = s <= t ? G[i][r] * seg : 0.0f;
-        const float e = s <= t ? W[r] * g : 0.0f;
-        K[i][r] += s <= t ? W[r] * seg * dts : 0.0f;
-        m[r] = g * dts;
-        row += s < t ? e * dts : 0.0f;
-        col[r] = s < t ? e : 0.0f;
-        if (s == t) {
-          sm.ediag[t] = e;
-          dg += W[r];
-        }
+        const float seg = exp2_hw((cth - ch[r]) + (ctl - cl[r]));
+        const bool in = !diag || s0 + r <= t;
+        m[r] = in ? G[i][r] * seg : 0.0f;
+        e[r] = in ? W[r] * m[r] : 0.0f;
+        K[i][r] += in ? W[r] * seg * dts[r] : 0.0f;
+        m[r] *= dts[r];
       }
       uint2 h2, l2;
       split2(m[0], m[1], h2.x, l2.x);
       split2(m[2], m[3], h2.y, l2.y);
       *reinterpret_cast<uint2*>(&sm.mhi[t][s0]) = h2;
       *reinterpret_cast<uint2*>(&sm.mlo[t][s0]) = l2;
-      row = sum_rows(row);
-      if (g4 == 0) sm.erow[ti[i]][t] = row;
+      if (diag) {  // the diagonal itself apart
+        float ed = 0.0f, wd = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool on = s0 + r == t;
+          ed += on ? e[r] : 0.0f;
+          wd += on ? W[r] : 0.0f;
+          e[r] = on ? 0.0f : e[r];
+        }
+        ed = sum_rows(ed);
+        wd = sum64(wd);
+        if (g4 == 0) sm.ediag[t] = ed;
+        if (lane == 0) sm.diag[ti[i]] = wd;
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        col[r] = sum16(col[r]);
-        if (l16 == r) sm.ecol[tj[i]][s0 + r] = col[r];
+        row = fmaf(e[r], dts[r], row);
+        e[r] = sum16(e[r]);
       }
-      if (ti[i] == tj[i]) {
-        dg = sum64(dg);
-        if (lane == 0) sm.diag[ti[i]] = dg;
-      }
+      row = sum_rows(row);
+      if (g4 == 0) sm.erow[ti[i]][t] = row;
+      if (l16 == 0)
+        *reinterpret_cast<float4*>(&sm.ecol[tj[i]][s0]) = make_float4(e[0], e[1], e[2], e[3]);
     }
 
-    // ---- S_in^T C^T and lam_out^T B^T
-    f32x4 Y[2] = {}, V[2] = {};
+    // ---- S_in^T C^T or lam_out^T B^T
+    f32x16 Y = {};
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll 1
-    for (int kb = 0; kb < N; kb += 32) {
-      const Op sh = op_along(&sm.shi[0][0], N + 8, 16 * pt, kb, l16, g4);
-      const Op sl = op_along(&sm.slo[0][0], N + 8, 16 * pt, kb, l16, g4);
-      const Op lh = op_along(&sm.lhi[0][0], N + 8, 16 * pt, kb, l16, g4);
-      const Op ll = op_along(&sm.llo[0][0], N + 8, 16 * pt, kb, l16, g4);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const Op c = op_along(&sm.c[0][0], N + 16, 16 * jt[i], kb, l16, g4);
-        Y[i] = mfma(sh, c, Y[i]);
-        Y[i] = mfma(sl, c, Y[i]);
-        const Op bo = op_along(&sm.b[0][0], N + 16, 16 * jt[i], kb, l16, g4);
-        V[i] = mfma(lh, bo, V[i]);
-        V[i] = mfma(ll, bo, V[i]);
-      }
+#pragma unroll 2
+    for (int kb = 0; kb < N; kb += 16) {
+      const Op to = along32(bc_t, N + 8, 32 * sh, kb, lane);
+      Y = mfma32(along32(hi_t, N + 8, 32 * ph, kb, lane), to, Y);
+      Y = mfma32(along32(lo_t, N + 8, 32 * ph, kb, lane), to, Y);
     }
-    // ---- S_in gy^T and lam_out X^T, scaled by their steps into dC and dB
+    // ---- S_in gy^T or lam_out X^T, scaled by their steps into dC or dB
     {
-      f32x4 T[TPW] = {};
+      f32x16 T[TPW] = {};
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll 1
-      for (int kb = 0; kb < kP; kb += 32) {
-        const Op sh = op_down(&sm.shi[0][0], N + 8, kb, 16 * nt, l16, g4);
-        const Op sl = op_down(&sm.slo[0][0], N + 8, kb, 16 * nt, l16, g4);
+#pragma unroll 2
+      for (int kb = 0; kb < kP; kb += 16) {
+        const Op ah = down32(hi_t, N + 8, kb, 32 * nt, lane);
+        const Op al = down32(lo_t, N + 8, kb, 32 * nt, lane);
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
-          const Op gh = op_along(&sm.ghi[0][0], kPS, 16 * (j0 + j), kb, l16, g4);
-          const Op gl = op_along(&sm.glo[0][0], kPS, 16 * (j0 + j), kb, l16, g4);
-          T[j] = mfma(sh, gh, T[j]);
-          T[j] = mfma(sl, gh, T[j]);
-          T[j] = mfma(sh, gl, T[j]);
+          const Op to = along32(by_t, kPS, 32 * (j0 + j), kb, lane);
+          T[j] = mfma32(ah, to, T[j]);
+          T[j] = mfma32(al, to, T[j]);
+          if (!role) T[j] = mfma32(ah, along32(&sm.glo[0][0], kPS, 32 * (j0 + j), kb, lane), T[j]);
         }
       }
 #pragma unroll
       for (int j = 0; j < TPW; ++j) {
-        const float e = sm.before[16 * (j0 + j) + l16];
+        const int t = 32 * (j0 + j) + l32;
+        const float by = role ? sm.after[t] * sm.dt[t] : sm.before[t];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) dC[j][r] = fmaf(e, T[j][r], dC[j][r]);
-      }
-    }
-    {
-      f32x4 U[TPW] = {};
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll 1
-      for (int kb = 0; kb < kP; kb += 32) {
-        const Op lh = op_down(&sm.lhi[0][0], N + 8, kb, 16 * nt, l16, g4);
-        const Op ll = op_down(&sm.llo[0][0], N + 8, kb, 16 * nt, l16, g4);
-#pragma unroll
-        for (int j = 0; j < TPW; ++j) {
-          const Op xo = op_along(&sm.x[0][0], kPS, 16 * (j0 + j), kb, l16, g4);
-          U[j] = mfma(lh, xo, U[j]);
-          U[j] = mfma(ll, xo, U[j]);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < TPW; ++j) {
-        const int t = 16 * (j0 + j) + l16;
-        const float wt = sm.after[t] * sm.dt[t];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) dB[j][r] = fmaf(wt, U[j][r], dB[j][r]);
+        for (int r = 0; r < 16; ++r) dBC[j][r] = fmaf(by, T[j][r], dBC[j][r]);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
     __syncthreads();  // M is there
 
-    // ---- the carried parts scaled and summed, then the chunk's own: X^T (M dt)^T over s <= t,
+    // ---- the carried parts scaled and summed, then the chunk's own: X^T (M dt)^T over s <= t, or
     // gy^T (M dt) over t >= s
+    const int t = 32 * sh + l32, c0 = 32 * ph + 4 * hi32;
+    const float dts = sm.dt[t], by = role ? sm.after[t] : sm.before[t];
+    float part = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int j = jt[i], t = 16 * j + l16;
-      const float ev = sm.before[t], av = sm.after[t], dts = sm.dt[t];
-      const int c0 = 16 * pt + 4 * g4;
-      const uint2 xw = *reinterpret_cast<const uint2*>(&sm.x[t][c0]);
-      const uint2 gh = *reinterpret_cast<const uint2*>(&sm.ghi[t][c0]);
-      const uint2 gl = *reinterpret_cast<const uint2*>(&sm.glo[t][c0]);
-      const float x[4] = {lo_f(xw.x), hi_f(xw.x), lo_f(xw.y), hi_f(xw.y)};
-      const float gy[4] = {lo_f(gh.x) + lo_f(gl.x), hi_f(gh.x) + hi_f(gl.x),
-                           lo_f(gh.y) + lo_f(gl.y), hi_f(gh.y) + hi_f(gl.y)};
-      float near = 0.0f, far = 0.0f;
+    for (int q = 0; q < 4; ++q) {
+      float v[4];
+      if (role) {
+        const uint2 xw = *reinterpret_cast<const uint2*>(&sm.x[t][c0 + 8 * q]);
+        v[0] = lo_f(xw.x), v[1] = hi_f(xw.x), v[2] = lo_f(xw.y), v[3] = hi_f(xw.y);
+      } else {
+        const uint2 gh = *reinterpret_cast<const uint2*>(&sm.ghi[t][c0 + 8 * q]);
+        const uint2 gl = *reinterpret_cast<const uint2*>(&sm.glo[t][c0 + 8 * q]);
+        v[0] = lo_f(gh.x) + lo_f(gl.x), v[1] = hi_f(gh.x) + hi_f(gl.x);
+        v[2] = lo_f(gh.y) + lo_f(gl.y), v[3] = hi_f(gh.y) + hi_f(gl.y);
+      }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        Y[i][r] *= ev;
-        V[i][r] *= av;
-        near = fmaf(gy[r], Y[i][r], near);
-        far = fmaf(x[r], V[i][r], far);
-        V[i][r] *= dts;
+        Y[4 * q + r] *= by;
+        part = fmaf(v[r], Y[4 * q + r], part);
+        if (role) Y[4 * q + r] *= dts;
       }
-      near = sum_rows(near);
-      far = sum_rows(far);
-      if (g4 == 0) {
-        sm.near[pt][t] = near;
-        sm.far[pt][t] = far;
+    }
+    part = sum_halves(part);
+    if (hi32 == 0) (role ? sm.far : sm.near)[ph][t] = part;
+    if (role) {
+      for (int kb = 32 * sh; kb < kQ; kb += 16) {
+        const Op ga = down32(&sm.ghi[0][0], kPS, kb, 32 * ph, lane);
+        const Op gb = down32(&sm.glo[0][0], kPS, kb, 32 * ph, lane);
+        const Op ma = down32(&sm.mhi[0][0], kPS, kb, 32 * sh, lane);
+        const Op mb = down32(&sm.mlo[0][0], kPS, kb, 32 * sh, lane);
+        Y = mfma32(ga, ma, Y);
+        Y = mfma32(gb, ma, Y);
+        Y = mfma32(ga, mb, Y);
       }
+      const rsrc_t rx = make_buf(static_cast<uint16_t*>(p.dx) + tile0, tile_bytes);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (kb <= (j >> 1)) {
-          const Op xo = op_down(&sm.x[0][0], kPS, 32 * kb, 16 * pt, l16, g4);
-          Y[i] = mfma(xo, op_along(&sm.mhi[0][0], kPS, 16 * j, 32 * kb, l16, g4), Y[i]);
-          Y[i] = mfma(xo, op_along(&sm.mlo[0][0], kPS, 16 * j, 32 * kb, l16, g4), Y[i]);
-        }
-        if (kb >= (j >> 1)) {
-          const Op ga = op_down(&sm.ghi[0][0], kPS, 32 * kb, 16 * pt, l16, g4);
-          const Op gb = op_down(&sm.glo[0][0], kPS, 32 * kb, 16 * pt, l16, g4);
-          const Op ma = op_down(&sm.mhi[0][0], kPS, 32 * kb, 16 * j, l16, g4);
-          const Op mb = op_down(&sm.mlo[0][0], kPS, 32 * kb, 16 * j, l16, g4);
-          V[i] = mfma(ga, ma, V[i]);
-          V[i] = mfma(gb, ma, V[i]);
-          V[i] = mfma(ga, mb, V[i]);
-        }
-      }
-      float dx[4];
+      for (int q = 0; q < 4; ++q) {
+        const uint2 gh = *reinterpret_cast<const uint2*>(&sm.ghi[t][c0 + 8 * q]);
+        const uint2 gl = *reinterpret_cast<const uint2*>(&sm.glo[t][c0 + 8 * q]);
+        const float gy[4] = {lo_f(gh.x) + lo_f(gl.x), hi_f(gh.x) + hi_f(gl.x),
+                             lo_f(gh.y) + lo_f(gl.y), hi_f(gh.y) + hi_f(gl.y)};
+        float dx[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dx[r] = fmaf(Dh, gy[r], V[i][r]);
-      const int64_t o = (b * L + t0) * hp + h * kP;
-      store8(make_uint2(pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])),
-             make_buf(static_cast<uint16_t*>(p.dx) + o, tile_bytes), out_off[i]);
-      if (GATE) {
-        const float z[4] = {lo_f(ze[i].x), hi_f(ze[i].x), lo_f(ze[i].y), hi_f(ze[i].y)};
-        const float go[4] = {lo_f(ge[i].x), hi_f(ge[i].x), lo_f(ge[i].y), hi_f(ge[i].y)};
+        for (int r = 0; r < 4; ++r) dx[r] = fmaf(Dh, gy[r], Y[4 * q + r]);
+        store8(make_uint2(pack_bf16(dx[0], dx[1]), pack_bf16(dx[2], dx[3])), rx, out_off + 16 * q);
+      }
+    } else if (GATE) {
+      for (int kb = 0; kb < 32 * (sh + 1); kb += 16) {
+        const Op xo = down32(&sm.x[0][0], kPS, kb, 32 * ph, lane);
+        Y = mfma32(xo, along32(&sm.mhi[0][0], kPS, 32 * sh, kb, lane), Y);
+        Y = mfma32(xo, along32(&sm.mlo[0][0], kPS, 32 * sh, kb, lane), Y);
+      }
+      const rsrc_t rz = make_buf(static_cast<uint16_t*>(p.dz) + tile0, tile_bytes);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint2 xw = *reinterpret_cast<const uint2*>(&sm.x[t][c0 + 8 * q]);
+        const float x[4] = {lo_f(xw.x), hi_f(xw.x), lo_f(xw.y), hi_f(xw.y)};
+        const float z[4] = {lo_f(ze[q].x), hi_f(ze[q].x), lo_f(ze[q].y), hi_f(ze[q].y)};
+        const float go[4] = {lo_f(ge[q].x), hi_f(ge[q].x), lo_f(ge[q].y), hi_f(ge[q].y)};
         float dz[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float sg = sigmoid_f(z[r]);
-          dz[r] = go[r] * fmaf(Dh, x[r], Y[i][r]) * (sg * fmaf(z[r], 1.0f - sg, 1.0f));
+          dz[r] = go[r] * fmaf(Dh, x[r], Y[4 * q + r]) * (sg * fmaf(z[r], 1.0f - sg, 1.0f));
         }
-        store8(make_uint2(pack_bf16(dz[0], dz[1]), pack_bf16(dz[2], dz[3])),
-               make_buf(static_cast<uint16_t*>(p.dz) + o, tile_bytes), out_off[i]);
+        store8(make_uint2(pack_bf16(dz[0], dz[1]), pack_bf16(dz[2], dz[3])), rz, out_off + 16 * q);
       }
     }
     lds_reads_done();
   }
   __syncthreads();
-  if (wv == 7 && h_beg < h_end) finish(h_end - 1, st);
+  if (wv == 7) finish(h_end - 1, A, st);
 
   // ---- dC^T += B^T K^T, dB^T += C^T K, K (t, s) in M's place
 #pragma unroll
@@ -636,33 +696,36 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     *reinterpret_cast<uint2*>(&sm.mlo[t][s0]) = l2;
   }
   __syncthreads();
+  const uint16_t* kt = role ? &sm.c[0][0] : &sm.b[0][0];
 #pragma unroll
-  for (int kb = 0; kb < kQ; kb += 32) {
-    const Op bo = op_down(&sm.b[0][0], N + 16, kb, 16 * nt, l16, g4);
-    const Op co = op_down(&sm.c[0][0], N + 16, kb, 16 * nt, l16, g4);
+  for (int kb = 0; kb < kQ; kb += 16) {
+    const Op a = down32(kt, N + 8, kb, 32 * nt, lane);
 #pragma unroll
     for (int j = 0; j < TPW; ++j) {
-      dC[j] = mfma(bo, op_along(&sm.mhi[0][0], kPS, 16 * (j0 + j), kb, l16, g4), dC[j]);
-      dC[j] = mfma(bo, op_along(&sm.mlo[0][0], kPS, 16 * (j0 + j), kb, l16, g4), dC[j]);
-      dB[j] = mfma(co, op_down(&sm.mhi[0][0], kPS, kb, 16 * (j0 + j), l16, g4), dB[j]);
-      dB[j] = mfma(co, op_down(&sm.mlo[0][0], kPS, kb, 16 * (j0 + j), l16, g4), dB[j]);
+      const int c = 32 * (j0 + j);
+      dBC[j] = mfma32(a, role ? down32(&sm.mhi[0][0], kPS, kb, c, lane)
+                              : along32(&sm.mhi[0][0], kPS, c, kb, lane), dBC[j]);
+      dBC[j] = mfma32(a, role ? down32(&sm.mlo[0][0], kPS, kb, c, lane)
+                              : along32(&sm.mlo[0][0], kPS, c, kb, lane), dBC[j]);
     }
   }
 #pragma unroll
   for (int j = 0; j < TPW; ++j) {
-    const int t = 16 * (j0 + j) + l16;
+    const int t = 32 * (j0 + j) + (lane & 31);
     if (t >= rows) continue;
-    const int64_t o = ((b * L + t0 + t) * p.ngroups + grp) * N + 16 * nt + 4 * g4;
-    if (p.splits == 1) {
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dB) + o) =
-          make_uint2(pack_bf16(dB[j][0], dB[j][1]), pack_bf16(dB[j][2], dB[j][3]));
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dC) + o) =
-          make_uint2(pack_bf16(dC[j][0], dC[j][1]), pack_bf16(dC[j][2], dC[j][3]));
-    } else {
-      const int64_t all = p.batch * L * gn;
-      float* q = p.bc_part + split * 2 * all + o;
-      *reinterpret_cast<f32x4*>(q) = dB[j];
-      *reinterpret_cast<f32x4*>(q + all) = dC[j];
+    const int64_t o =
+        ((b * L + t0 + t) * p.ngroups + grp) * N + 32 * nt + 4 * (lane >> 5);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float v[4] = {dBC[j][4 * q], dBC[j][4 * q + 1], dBC[j][4 * q + 2], dBC[j][4 * q + 3]};
+      if (p.splits == 1) {
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(role ? p.dB : p.dC) + o + 8 * q) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      } else {
+        const int64_t all = p.batch * L * gn;
+        *reinterpret_cast<float4*>(p.bc_part + split * 2 * all + (role ? 0 : all) + o + 8 * q) =
+            make_float4(v[0], v[1], v[2], v[3]);
+      }
     }
   }
 }
@@ -690,7 +753,7 @@ bool scan2_bwd_mfma_supported(const Scan2BwdArgs& a, bool bf16) {
       reinterpret_cast<uintptr_t>(a.dz) | reinterpret_cast<uintptr_t>(a.dB) |
       reinterpret_cast<uintptr_t>(a.dC);
   return bf16 && a.headdim == kP && (a.d_state == 64 || a.d_state == 128) && (al & 15) == 0 &&
-         kQ * a.nheads * kP * 2 < (int64_t(1) << 31);
+         kQ * a.nheads * kP * 2 < (int64_t(1) << 31);  // covers the rows of dt and the heads' A
 }
 
 hipError_t launch_scan2_bwd_mfma(const Scan2BwdArgs& a, hipStream_t stream) {
