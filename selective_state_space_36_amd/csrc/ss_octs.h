@@ -19,34 +19,53 @@ struct OctBytes<float> {
   typedef uint32_t raw __attribute__((ext_vector_type(4), aligned(4)));
 };
 
+// Eight elements on their way, as loaded.
+template <class IO>
+struct Oct {
+  static constexpr int kWords = sizeof(typename IO::elem) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (kWords == 8) return __uint_as_float(w[j]);
+    else return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+  }
+};
+
 // Eight elements at `p`, of which n are there (n >= 8: all of them, in 16-byte accesses of whatever
 // alignment the row has; fewer: one by one, the rest 0; n <= 0: none).  PAST: non-temporal.
 template <class IO, bool PAST = false>
-__device__ __forceinline__ void load8(const typename IO::elem* p, int n, float (&v)[8]) {
+__device__ __forceinline__ Oct<IO> load_oct(const typename IO::elem* p, int n) {
   using E = typename IO::elem;
   using raw = typename OctBytes<E>::raw;
+  Oct<IO> o;
   if (n >= 8) {
     const raw* q = reinterpret_cast<const raw*>(p);
-    if constexpr (sizeof(E) == 2) {
-      const raw a = PAST ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(a[j] << 16);
-        v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
-      }
-    } else {
-      const raw a = PAST ? __builtin_nontemporal_load(q) : q[0];
-      const raw b = PAST ? __builtin_nontemporal_load(q + 1) : q[1];
+    for (int h = 0; h < Oct<IO>::kWords / 4; ++h) {
+      const raw a = PAST ? __builtin_nontemporal_load(q + h) : q[h];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = __uint_as_float(a[j]);
-        v[4 + j] = __uint_as_float(b[j]);
-      }
+      for (int j = 0; j < 4; ++j) o.w[4 * h + j] = a[j];
     }
   } else {
+    uint32_t e[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? IO::widen(p[j]) : 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      e[j] = 0;
+      if (j < n) {
+        if constexpr (sizeof(E) == 4) e[j] = __float_as_uint(p[j]);
+        else e[j] = p[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < Oct<IO>::kWords; ++j)
+      o.w[j] = sizeof(E) == 4 ? e[j] : e[(2 * j) & 7] | e[(2 * j + 1) & 7] << 16;
   }
+  return o;
+}
+template <class IO, bool PAST = false>
+__device__ __forceinline__ void load8(const typename IO::elem* p, int n, float (&v)[8]) {
+  const Oct<IO> o = load_oct<IO, PAST>(p, n);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = o[j];
 }
 
 template <class IO, bool PAST = false>

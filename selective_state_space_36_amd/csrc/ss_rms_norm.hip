@@ -14,8 +14,6 @@
 namespace ss {
 namespace {
 
-constexpr int kMaxUnit = 16384;  // columns of a unit held in registers (1024 lanes, two octs each)
-
 // sigmoid as 1 / (1 + 2^(-z log2 e)): 0 at -infinity, 1 at +infinity.
 __device__ __forceinline__ float sigmoid_f(float z) {
   return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
@@ -130,130 +128,119 @@ __global__ __launch_bounds__(1024) void rms_fwd_kernel(RmsArgs p, UnitLayout l) 
 // Where a place's parameter sums go: its line of `part` (cols columns a line), group g's columns.
 // One line per place that shares the group with no other of its workgroup; with a single group the
 // places of a workgroup are first added in order through LDS, and it writes one line.
-template <int K, int N>
-__device__ __forceinline__ void write_lines(float (&acc)[N][K][8], const UnitLayout& l,
+template <int N>
+__device__ __forceinline__ void write_lines(float (&acc)[N][8], const UnitLayout& l,
                                             const Place& at, int g, int64_t cols, float* part,
                                             float* fold) {
   int64_t line;
   if (l.groups == 1) {
     line = blockIdx.x;
     if (l.segs > 1) {
-      const int per = l.lanes * K * 8;  // floats a place holds of one sum
+      const int per = l.lanes * 8;  // floats a place holds of one sum
 #pragma unroll
       for (int q = 0; q < N; ++q)
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            fold[(at.seg * N + q) * per + (k * 8 + j) * l.lanes + at.lane] = acc[q][k][j];
+        for (int j = 0; j < 8; ++j)
+          fold[(at.seg * N + q) * per + j * l.lanes + at.lane] = acc[q][j];
       __syncthreads();
       if (at.seg) return;
       for (int s = 1; s < l.segs; ++s)
 #pragma unroll
         for (int q = 0; q < N; ++q)
 #pragma unroll
-          for (int k = 0; k < K; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[q][k][j] += fold[(s * N + q) * per + (k * 8 + j) * l.lanes + at.lane];
+          for (int j = 0; j < 8; ++j)
+            acc[q][j] += fold[(s * N + q) * per + j * l.lanes + at.lane];
     }
   } else {
     line = (static_cast<int64_t>(blockIdx.x) * l.segs + at.seg) / l.groups;
   }
+  const int c = at.lane * 8;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int c = (k * l.lanes + at.lane) * 8;
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-      store8<F32>(part + (line * N + q) * cols + static_cast<int64_t>(g) * l.width + c,
-                  l.width - c, acc[q][k]);
-  }
+  for (int q = 0; q < N; ++q)
+    store8<F32>(part + (line * N + q) * cols + static_cast<int64_t>(g) * l.width + c, l.width - c,
+                acc[q]);
 }
 
-template <class IO, class S, int K, bool DROP>
-__global__ __launch_bounds__(1024) void rms_bwd_kernel(RmsArgs p, UnitLayout l, float* part) {
+// One oct per lane: a place's sums, its row and the next one take about 140 registers.  (The next row
+// asked for ahead: 210 -> 140 us at 16384 x 2560 bf16, where its rows are not spilled: MOST 512, for
+// up to 4096 columns; with 1024 lanes the compiler has 128 registers and spills 8 to 24.)  Rows of
+// over 8192 columns go to the wide kernels.
+template <class IO, class S, bool DROP, bool PAST, int MOST>
+__global__ __launch_bounds__(MOST) void rms_bwd_kernel(RmsArgs p, UnitLayout l, float* part) {
   using E = typename IO::elem;
   __shared__ float lds[2 * 16];
-  __shared__ float fold[256 * 2 * 8 * K];
+  __shared__ float fold[256 * 2 * 8];
   const Place at = place(l);
   const float inv = 1.0f / static_cast<float>(l.width);
+  const int c = at.lane * 8, left = l.width - c;
   PhiloxKey key{};
   if constexpr (DROP) key = philox_key(p.drop.rng);
-  float acc[2][K][8] = {};  // dweight, dscale
+  float acc[2][8] = {};  // dweight, dscale
+  float wt[8], sc[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) wt[j] = sc[j] = 1.0f;
+  if (p.weight) load8<F32>(p.weight + c, left, wt);
+  if (p.scale) load8<F32>(p.scale + c, left, sc);
+  // The next row is asked for before this one's sums.
+  Oct<IO> go, xo;
+  Oct<S> so;
+  Oct<F32> uo;
+  float rstd = 0.0f, rb = 1.0f;
+  auto fetch = [&](int64_t row, int n) {
+    const int64_t base = row * l.width;
+    go = load_oct<IO, PAST>(static_cast<const E*>(p.dout) + base + c, n);
+    so = load_oct<S, PAST>(static_cast<const typename S::elem*>(p.s) + base + c, n);
+    if (p.x) xo = load_oct<IO, PAST>(static_cast<const E*>(p.x) + base + c, n);
+    if (p.dsum) uo = load_oct<F32, PAST>(p.dsum + base + c, n);
+    rstd = p.rstd_in[row];
+    if (p.branch) rb = p.branch_rstd_in[row];
+  };
   int phase = 0;
-  for (Walk w(l, at.seg); w.u < l.units; w.next(l)) {
-    const int64_t base = w.row * l.width;
-    const float rstd = p.rstd_in[w.row];
-    const float rb = p.branch ? p.branch_rstd_in[w.row] : 1.0f;
-    float sh[K][8], g[K][8], x[K][8], u[K][8], c1[1] = {0.0f};
+  Walk w(l, at.seg);
+  if (w.u < l.units) fetch(w.row, left);
+  while (w.u < l.units) {
+    const int64_t row = w.row, base = row * l.width;
+    float sh[8], g[8], x[8], u[8], c1[1] = {0.0f};
+    const float rs = rstd, rbs = rb;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * l.lanes + at.lane) * 8, left = l.width - c;
-      load8<IO>(static_cast<const E*>(p.dout) + base + c, left, g[k]);
-      load8<S>(static_cast<const typename S::elem*>(p.s) + base + c, left, sh[k]);
-      if (p.x) load8<IO>(static_cast<const E*>(p.x) + base + c, left, x[k]);
-      if (p.dsum) load8<F32>(p.dsum + base + c, left, u[k]);
+    for (int j = 0; j < 8; ++j) {
+      g[j] = go[j];
+      sh[j] = so[j] * rs;
+      x[j] = p.x ? xo[j] * rbs : 0.0f;
+      u[j] = p.dsum ? uo[j] : 0.0f;
     }
+    w.next(l);
+    if (w.u < l.units) fetch(w.row, left);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * l.lanes + at.lane) * 8, left = l.width - c;
-      float wt[8];
-      if (p.weight) load8<F32>(p.weight + c, left, wt);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        sh[k][j] *= rstd;
-        acc[0][k][j] = fmaf(g[k][j], sh[k][j], acc[0][k][j]);
-        if (p.weight) g[k][j] *= wt[j];
-        c1[0] = fmaf(g[k][j], sh[k][j], c1[0]);
-      }
+    for (int j = 0; j < 8; ++j) {
+      acc[0][j] = fmaf(g[j], sh[j], acc[0][j]);
+      g[j] *= wt[j];
+      c1[0] = fmaf(g[j], sh[j], c1[0]);
     }
     unit_sums<1>(c1, l.lanes, lds, phase++);
     const float m1 = c1[0] * inv;
-    float c2[1] = {0.0f};
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * l.lanes + at.lane) * 8, left = l.width - c;
+    for (int j = 0; j < 8; ++j) g[j] = fmaf(rs, fmaf(-sh[j], m1, g[j]), u[j]);
+    if (p.dresidual) store8<F32>(p.dresidual + base + c, left, g);
+    if constexpr (DROP)
+      drop8(g, key, at.lane, static_cast<uint32_t>(row), p.drop.cut, p.drop.up);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        g[k][j] = fmaf(rstd, fmaf(-sh[k][j], m1, g[k][j]), p.dsum ? u[k][j] : 0.0f);
-      if (p.dresidual) store8<F32>(p.dresidual + base + c, left, g[k]);
-      if constexpr (DROP) drop8(g[k], key, c >> 3, static_cast<uint32_t>(w.row), p.drop.cut,
-                                p.drop.up);
-      if (p.x) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[k][j] *= rb;
-          acc[1][k][j] = fmaf(g[k][j], x[k][j], acc[1][k][j]);
-        }
-      }
-      if (p.scale) {
-        float s[8];
-        load8<F32>(p.scale + c, left, s);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[k][j] *= s[j];
-      }
-      if (p.branch) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) c2[0] = fmaf(g[k][j], x[k][j], c2[0]);
-      }
+    for (int j = 0; j < 8; ++j) {
+      acc[1][j] = fmaf(g[j], x[j], acc[1][j]);
+      g[j] *= sc[j];
     }
     if (p.branch) {
+      float c2[1] = {0.0f};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) c2[0] = fmaf(g[j], x[j], c2[0]);
       unit_sums<1>(c2, l.lanes, lds, phase++);
       const float m2 = c2[0] * inv;
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[k][j] = rb * fmaf(-x[k][j], m2, g[k][j]);
+      for (int j = 0; j < 8; ++j) g[j] = rbs * fmaf(-x[j], m2, g[j]);
     }
-    if (p.dx) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = (k * l.lanes + at.lane) * 8;
-        store8<IO>(static_cast<E*>(p.dx) + base + c, l.width - c, g[k]);
-      }
-    }
+    if (p.dx) store8<IO>(static_cast<E*>(p.dx) + base + c, left, g);
   }
-  if (part) write_lines<K, 2>(acc, l, at, 0, l.width, part, fold);
+  if (part) write_lines<2>(acc, l, at, 0, l.width, part, fold);
 }
 
 // ------------------------------------------------------------------ the gated norm
@@ -302,70 +289,67 @@ __global__ __launch_bounds__(1024) void gated_norm_fwd_kernel(GatedNormArgs p, U
   }
 }
 
-template <class IO, int K, bool FIRST>
+template <class IO, bool FIRST, bool PAST>
 __global__ __launch_bounds__(1024) void gated_norm_bwd_kernel(GatedNormArgs p, UnitLayout l,
                                                               float* part) {
   using E = typename IO::elem;
   __shared__ float lds[2 * 16];
-  __shared__ float fold[256 * 8 * K];
+  __shared__ float fold[256 * 8];
   const Place at = place(l);
   const float inv = 1.0f / static_cast<float>(l.width);
-  float acc[1][K][8] = {};
+  const int c = at.lane * 8, left = l.width - c;
+  float acc[1][8] = {};
   int phase = 0;
   Walk w(l, at.seg);
   const int g0 = w.g;  // a place keeps its group (launch: stride is a multiple of the groups)
-  const int64_t col = static_cast<int64_t>(g0) * l.width;
-  for (; w.u < l.units; w.next(l)) {
-    const int64_t base = w.row * p.dim + col, zbase = w.row * p.z_stride + col;
-    const float rstd = p.rstd_in[w.u];
-    float x[K][8], z[K][8], d[K][8], c1[1] = {0.0f};
+  const int64_t col = static_cast<int64_t>(g0) * l.width + c;
+  float wt[8];
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * l.lanes + at.lane) * 8, left = l.width - c;
-      load8<IO>(static_cast<const E*>(p.dout) + base + c, left, d[k]);
-      load8<IO>(static_cast<const E*>(p.x) + base + c, left, x[k]);
-      if (p.z) load8<IO>(static_cast<const E*>(p.z) + zbase + c, left, z[k]);
-    }
+  for (int j = 0; j < 8; ++j) wt[j] = 1.0f;
+  if (p.weight) load8<F32>(p.weight + col, left, wt);
+  Oct<IO> xo, zo, go;
+  float rstd = 0.0f;
+  auto fetch = [&]() {
+    const int64_t base = w.row * p.dim + col;
+    go = load_oct<IO, PAST>(static_cast<const E*>(p.dout) + base, left);
+    xo = load_oct<IO, PAST>(static_cast<const E*>(p.x) + base, left);
+    if (p.z) zo = load_oct<IO, PAST>(static_cast<const E*>(p.z) + w.row * p.z_stride + col, left);
+    rstd = p.rstd_in[w.u];
+  };
+  if (w.u < l.units) fetch();
+  while (w.u < l.units) {
+    const int64_t base = w.row * p.dim + col;
     // FIRST: u = x silu(z), hat = u rstd, out = hat w.   Else: hat = x rstd, out = hat w silu(z).
+    // hat and g = w d (silu(z)) stay; of dx = du gate and dz the factors x (or d hat w), gate, slope
+    float hat[8], g[8], gate[8], side[8], c1[1] = {0.0f};
+    const float rs = rstd;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * l.lanes + at.lane) * 8, left = l.width - c;
-      float wt[8];
-      if (p.weight) load8<F32>(p.weight + col + c, left, wt);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gate = p.z ? z[k][j] * sigmoid_f(z[k][j]) : 1.0f;
-        const float hat = x[k][j] * rstd * (FIRST ? gate : 1.0f);
-        const float after = FIRST ? d[k][j] : d[k][j] * gate;
-        acc[0][k][j] = fmaf(after, hat, acc[0][k][j]);
-        c1[0] = fmaf(p.weight ? after * wt[j] : after, hat, c1[0]);
-      }
+    for (int j = 0; j < 8; ++j) {
+      const float d = go[j], x = xo[j], zz = p.z ? zo[j] : 0.0f;
+      const float sg = p.z ? sigmoid_f(zz) : 1.0f;
+      const float slope = sg * fmaf(zz, 1.0f - sg, 1.0f);
+      gate[j] = p.z ? zz * sg : 1.0f;
+      hat[j] = x * rs * (FIRST ? gate[j] : 1.0f);
+      const float after = FIRST ? d : d * gate[j];
+      side[j] = (FIRST ? x : d * hat[j] * wt[j]) * slope;
+      acc[0][j] = fmaf(after, hat[j], acc[0][j]);
+      g[j] = after * wt[j];
+      c1[0] = fmaf(g[j], hat[j], c1[0]);
     }
+    w.next(l);
+    if (w.u < l.units) fetch();
     unit_sums<1>(c1, l.lanes, lds, phase++);
     const float m1 = c1[0] * inv;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * l.lanes + at.lane) * 8, left = l.width - c;
-      float wt[8], dx[8], dz[8];
-      if (p.weight) load8<F32>(p.weight + col + c, left, wt);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float zz = p.z ? z[k][j] : 0.0f;
-        const float sg = p.z ? sigmoid_f(zz) : 1.0f;
-        const float gate = p.z ? zz * sg : 1.0f;
-        const float slope = sg * fmaf(zz, 1.0f - sg, 1.0f);
-        const float wj = p.weight ? wt[j] : 1.0f;
-        const float hat = x[k][j] * rstd * (FIRST ? gate : 1.0f);
-        const float after = FIRST ? d[k][j] : d[k][j] * gate;
-        const float du = rstd * fmaf(-hat, m1, after * wj);
-        dx[j] = FIRST ? du * gate : du;
-        dz[j] = (FIRST ? du * x[k][j] : d[k][j] * hat * wj) * slope;
-      }
-      store8<IO>(static_cast<E*>(p.dx) + base + c, left, dx);
-      if (p.z) store8<IO>(static_cast<E*>(p.dz) + base + c, left, dz);
+    for (int j = 0; j < 8; ++j) {
+      const float du = rs * fmaf(-hat[j], m1, g[j]);
+      g[j] = FIRST ? du * gate[j] : du;
+      if (FIRST) side[j] *= du;
     }
+    store8<IO>(static_cast<E*>(p.dx) + base, left, g);
+    if (p.z) store8<IO>(static_cast<E*>(p.dz) + base, left, side);
   }
-  if (part) write_lines<K, 1>(acc, l, at, g0, p.dim, part, fold);
+  if (part) write_lines<1>(acc, l, at, g0, p.dim, part, fold);
 }
 
 // ------------------------------------------------------------------ units too wide for registers
@@ -656,34 +640,43 @@ struct Shape {
   int k, threads, blocks;
 };
 
+constexpr int64_t kFwdBlocks = 1 << 20;
+// Workgroups, and so lines of sums, of the backward.  Few rows: one each as long as the lines are
+// few (1001 x 1027 f32, 1001 workgroups 12.3 + 5.2 us for the sums, 256 of four rows 18.1 + 3.9).
+// Many: about as many workgroups as run at once (16384 x 2560 bf16, 512 workgroups 140 + 4.7 us,
+// 1024 144 + 5.2, 3276 196 + 14).
+constexpr int64_t kFewRowsBlocks = 1024, kManyRowsBlocks = 512;
+
 int64_t gcd(int64_t a, int64_t b) { return b ? gcd(b, a % b) : a; }
 
-// Lanes, octs per lane and workgroups for `rows` rows of `groups` groups of `width` columns.
-// `most`: workgroups at most (of 256 threads or more); keep_group: a place keeps its group.
-Shape shape_of(int64_t rows, int64_t groups, int64_t width, int64_t most, bool keep_group) {
+// Lanes, octs per lane and workgroups for `rows` rows of `groups` groups of `width` columns: an oct
+// a lane, in the forward two where 1024 lanes are not enough.  Backward: a place keeps its group,
+// and the workgroups are few enough for their lines of sums.
+Shape shape_of(int64_t rows, int64_t groups, int64_t width, bool backward) {
   Shape s{};
   const int64_t octs = (width + 7) / 8;
   s.l.groups = static_cast<int32_t>(groups);
   s.l.width = static_cast<int32_t>(width);
   s.l.units = rows * groups;
-  if (width > kMaxUnit) {
-    s.k = 0;
+  s.k = octs <= 1024 ? 1 : octs <= 2048 && !backward ? 2 : 0;
+  if (s.k == 0) {
     s.l.lanes = s.threads = kWide;
-  } else if (octs <= 128) {
-    s.k = octs > 64 ? 2 : 1;
+  } else if (octs <= 64) {
     s.l.lanes = 8;
-    while (s.l.lanes * s.k < octs) s.l.lanes *= 2;
+    while (s.l.lanes < octs) s.l.lanes *= 2;
     s.threads = 256;
   } else {
-    s.k = octs > 1024 ? 2 : 1;
     s.l.lanes = s.threads = static_cast<int>(((octs + s.k - 1) / s.k + 63) / 64 * 64);
   }
   s.l.segs = s.l.lanes > 64 ? 1 : s.threads / s.l.lanes;
   int64_t blocks = (s.l.units + s.l.segs - 1) / s.l.segs;
-  if (blocks > most) blocks = most;
-  if (keep_group) {
+  if (backward) {
+    const int64_t cap = blocks > 4096 ? kManyRowsBlocks : kFewRowsBlocks;
+    if (blocks > cap) blocks = cap;
     const int64_t step = groups / gcd(groups, s.l.segs);
     blocks = (blocks + step - 1) / step * step;
+  } else if (blocks > kFwdBlocks) {
+    blocks = kFwdBlocks;
   }
   s.blocks = static_cast<int>(blocks);
   s.l.stride = blocks * s.l.segs;
@@ -692,15 +685,9 @@ Shape shape_of(int64_t rows, int64_t groups, int64_t width, int64_t most, bool k
   return s;
 }
 
-constexpr int64_t kFwdBlocks = 1 << 20;
-// Lines of parameter sums: enough workgroups to fill the chip, few enough to sum.
-constexpr int64_t kBwdBlocks = 1024;
-
-Shape rms_bwd_shape(int64_t rows, int64_t dim) {
-  return shape_of(rows, 1, dim, kBwdBlocks, true);
-}
+Shape rms_bwd_shape(int64_t rows, int64_t dim) { return shape_of(rows, 1, dim, true); }
 Shape gated_bwd_shape(int64_t rows, int64_t dim, int64_t groups) {
-  return shape_of(rows, groups, dim / groups, kBwdBlocks, true);
+  return shape_of(rows, groups, dim / groups, true);
 }
 int64_t gated_lines(const Shape& s) { return s.l.groups == 1 ? s.blocks : s.l.drow; }
 
@@ -717,7 +704,7 @@ size_t rms_bwd_ws_bytes(int64_t rows, int64_t dim) {
 }
 
 hipError_t launch_rms_fwd(const RmsArgs& a, bool bf16, hipStream_t stream) {
-  const Shape s = shape_of(a.rows, 1, a.dim, kFwdBlocks, false);
+  const Shape s = shape_of(a.rows, 1, a.dim, false);
   with_io(bf16, [&](auto io) {
     using IO = decltype(io);
     auto go = [&](auto kernel) {
@@ -739,21 +726,22 @@ hipError_t launch_rms_fwd(const RmsArgs& a, bool bf16, hipStream_t stream) {
 hipError_t launch_rms_bwd(const RmsArgs& a, bool bf16, hipStream_t stream) {
   const Shape s = rms_bwd_shape(a.rows, a.dim);
   float* part = a.dweight || a.dscale ? a.workspace : nullptr;
+  const int64_t es = bf16 ? 2 : 4, n = a.rows * a.dim;
+  const bool past =
+      passes_cache(n * (es + (a.s_f32 ? 4 : es) + (a.x ? es : 0) + (a.dsum ? 4 : 0) +
+                        (a.dx ? es : 0) + (a.dresidual ? 4 : 0)));
   auto run = [&](auto io, auto sv) {
     using IO = decltype(io);
     using S = decltype(sv);
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(s.blocks), dim3(s.threads), 0, stream, a, s.l, part);
     };
-    if (a.drop.rng) {
-      if (s.k == 0) go(rms_bwd_wide_kernel<IO, S, true>);
-      else if (s.k == 1) go(rms_bwd_kernel<IO, S, 1, true>);
-      else go(rms_bwd_kernel<IO, S, 2, true>);
-    } else {
-      if (s.k == 0) go(rms_bwd_wide_kernel<IO, S, false>);
-      else if (s.k == 1) go(rms_bwd_kernel<IO, S, 1, false>);
-      else go(rms_bwd_kernel<IO, S, 2, false>);
-    }
+    with_bools([&](auto drop, auto nt) {
+      constexpr bool D = decltype(drop)::value, T = decltype(nt)::value;
+      if (s.k == 0) go(rms_bwd_wide_kernel<IO, S, D>);
+      else if (s.threads <= 512) go(rms_bwd_kernel<IO, S, D, T, 512>);
+      else go(rms_bwd_kernel<IO, S, D, T, 1024>);
+    }, a.drop.rng != nullptr, past);
   };
   if (!bf16) run(F32{}, F32{});
   else if (a.s_f32) run(BF16{}, F32{});
@@ -775,7 +763,7 @@ size_t gated_norm_bwd_ws_bytes(int64_t rows, int64_t dim, int64_t groups) {
 }
 
 hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, bool bf16, hipStream_t stream) {
-  const Shape s = shape_of(a.rows, a.groups, a.dim / a.groups, kFwdBlocks, false);
+  const Shape s = shape_of(a.rows, a.groups, a.dim / a.groups, false);
   with_io(bf16, [&](auto io) {
     using IO = decltype(io);
     auto go = [&](auto kernel) {
@@ -797,20 +785,17 @@ hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, bool bf16, hipStream_t 
 hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, bool bf16, hipStream_t stream) {
   const Shape s = gated_bwd_shape(a.rows, a.dim, a.groups);
   float* part = a.dweight ? a.workspace : nullptr;
+  const bool past = passes_cache(a.rows * a.dim * (bf16 ? 2 : 4) * (a.z ? 5 : 3));
   with_io(bf16, [&](auto io) {
     using IO = decltype(io);
     auto go = [&](auto kernel) {
       hipLaunchKernelGGL(kernel, dim3(s.blocks), dim3(s.threads), 0, stream, a, s.l, part);
     };
-    if (a.gate_first) {
-      if (s.k == 0) go(gated_norm_bwd_wide_kernel<IO, true>);
-      else if (s.k == 1) go(gated_norm_bwd_kernel<IO, 1, true>);
-      else go(gated_norm_bwd_kernel<IO, 2, true>);
-    } else {
-      if (s.k == 0) go(gated_norm_bwd_wide_kernel<IO, false>);
-      else if (s.k == 1) go(gated_norm_bwd_kernel<IO, 1, false>);
-      else go(gated_norm_bwd_kernel<IO, 2, false>);
-    }
+    with_bools([&](auto first, auto nt) {
+      constexpr bool G = decltype(first)::value, T = decltype(nt)::value;
+      if (s.k == 0) go(gated_norm_bwd_wide_kernel<IO, G>);
+      else go(gated_norm_bwd_kernel<IO, G, T>);
+    }, a.gate_first, past);
   });
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !part) return e;
