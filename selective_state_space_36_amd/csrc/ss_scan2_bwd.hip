@@ -28,6 +28,7 @@
 #include "ss_head.h"
 #include "ss_octs.h"
 #include "ss_rows.h"
+#include "ss_scan2_bwd.h"
 
 namespace ss {
 namespace {
@@ -76,45 +77,15 @@ __device__ __forceinline__ f32x4 mac(const Frag& a, const Frag& b, f32x4 c) {
   return c;
 }
 
-// Inclusive sums over the 64 lanes.
-template <class T>
-__device__ __forceinline__ T scan64(T v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const T o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-__device__ __forceinline__ float sum16(float v) {  // over the 16 lanes of a row
-  v += row_ror<8>(v);
-  v += row_ror<4>(v);
-  v += row_ror<2>(v);
-  return v + row_ror<1>(v);
-}
-__device__ __forceinline__ float sum64(float v) {
-  v = sum16(v);
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
-
-// Step sizes and decays of a chunk, one lane per step: raw = dt + bias, dt, c (log2).
-struct Step {
-  float raw, dt, c, end;
-};
+// The chunk's steps, one per lane.
 template <class IO>
 __device__ __forceinline__ Step steps(const Scan2BwdArgs& p, int64_t b, int64_t h, int64_t t0,
                                       int lane) {
-  Step s{0.0f, 0.0f, 0.0f, 0.0f};
-  if (t0 + lane < p.seqlen) {
-    s.raw = IO::widen(static_cast<const typename IO::elem*>(
-                p.dt)[(b * p.seqlen + t0 + lane) * p.nheads + h]) +
-            (p.dt_bias ? p.dt_bias[h] : 0.0f);
-    s.dt = p.softplus ? softplus_f(s.raw) : s.raw;
-  }
-  s.c = scan64(s.dt * (p.A[h] * kLog2e), lane);
-  s.end = __shfl(s.c, 63);
-  return s;
+  const bool in = t0 + lane < p.seqlen;
+  const float dt = in ? IO::widen(static_cast<const typename IO::elem*>(
+                            p.dt)[(b * p.seqlen + t0 + lane) * p.nheads + h])
+                      : 0.0f;
+  return step_of(dt, in, p.dt_bias ? p.dt_bias[h] : 0.0f, p.A[h], p.softplus);
 }
 
 // A thread's eight values of a 64 x 64 tile: row tid / 8, columns 8 (tid % 8).. of the `rows` x
@@ -136,15 +107,19 @@ template <int NB>
 struct alignas(16) StateSmem {
   float in[NB][kQ * kPitch];  // B or C, (step, state)
   float row[kQ * kPitch];     // weighted x or gy, (step, channel)
-  float weight[kQ], dt[kQ];
+  float weight[kQ];
 };
 
-// NB: 64-state blocks.  Workgroups 0 .. n - 1 walk forward (S_in), the others backward (lam_out).
+// NB: 64-state blocks.  Workgroups 0 .. n - 1 walk forward (S_in), the others backward (lam_out);
+// wave w holds channels 16 (w % 4).. and every other state tile from w / 4 on.  The next chunk is
+// asked for before this one's products.
 template <class IO, int NB>
-__global__ __launch_bounds__(256) void scan2_states_kernel(Scan2BwdArgs p) {
+__global__ __launch_bounds__(512) void scan2_states_kernel(Scan2BwdArgs p) {
   using E = typename IO::elem;
+  constexpr int NT = 2 * NB;
   __shared__ StateSmem<NB> sm;
-  const int tid = threadIdx.x, wv = tid >> 6, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), pw = wv & 3, nw = wv >> 2;
   const int64_t half = gridDim.x / 2;
   const bool back = blockIdx.x >= half;
   int64_t w = back ? blockIdx.x - half : blockIdx.x;
@@ -160,70 +135,80 @@ __global__ __launch_bounds__(256) void scan2_states_kernel(Scan2BwdArgs p) {
   const E* zrow = back && p.z ? static_cast<const E*>(p.z) + b * p.seqlen * hp + h * P + p0
                               : nullptr;
   const float* init = back ? p.dh_last : p.h0;
-  const int col = 16 * wv + l16;  // this lane's channel of the block
+  const int col = 16 * pw + l16;  // this lane's channel of the block
   const bool live = col < pcols;
-  f32x4 S[4 * NB];
+  const int r8 = tid >> 3, c8 = (tid & 7) * 8;
+  Oct<IO> io[NB], ro, zo;
+  Step st;
+  auto fetch = [&](int64_t ch) {
+    const int64_t t0 = ch * kQ;
+    const bool there = r8 < p.seqlen - t0;
 #pragma unroll
-  for (int nt = 0; nt < 4 * NB; ++nt)
+    for (int nb = 0; nb < NB; ++nb)
+      io[nb] = load_oct<IO>(in + (t0 + r8) * gn + nb * kQ + c8, there ? N - nb * kQ - c8 : 0);
+    ro = load_oct<IO>(row + (t0 + r8) * hp + c8, there ? pcols - c8 : 0);
+    if (zrow) zo = load_oct<IO>(zrow + (t0 + r8) * hp + c8, there ? pcols - c8 : 0);
+    st = steps<IO>(p, b, h, t0, lane);
+  };
+  f32x4 S[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int n = 16 * nt + 4 * g4 + r;
-      S[nt][r] = init && live && n < N
-                     ? init[((b * p.nheads + h) * N + n) * P + p0 + col]
-                     : 0.0f;
+      const int n = 16 * (2 * i + nw) + 4 * g4 + r;
+      S[i][r] = init && live && n < N
+                    ? init[((b * p.nheads + h) * N + n) * P + p0 + col]
+                    : 0.0f;
     }
+  fetch(back ? nc - 1 : 0);
   for (int64_t k = 0; k < nc; ++k) {
-    const int64_t ch = back ? nc - 1 - k : k, t0 = ch * kQ;
-    const int rows = p.seqlen - t0 < kQ ? static_cast<int>(p.seqlen - t0) : kQ;
+    const int64_t ch = back ? nc - 1 - k : k;
     float* out = ws + ch * N * P;
 #pragma unroll
-    for (int nt = 0; nt < 4 * NB; ++nt)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int n = 16 * nt + 4 * g4 + r;
-        if (live && n < N) out[static_cast<int64_t>(n) * P + col] = S[nt][r];
+        const int n = 16 * (2 * i + nw) + 4 * g4 + r;
+        if (live && n < N) out[static_cast<int64_t>(n) * P + col] = S[i][r];
       }
-    const Step st = steps<IO>(p, b, h, t0, lane);
-    // w_s = dt e^{c_end - c_s} forward, e^{c_t} backward
-    const float wt = back ? exp2_hw(st.c) : exp2_hw(st.end - st.c) * st.dt;
-    const float decay = exp2_hw(st.end);
+    const float decay = st.end;
     __syncthreads();  // the previous chunk's tiles have been read
-    if (wv == 0) sm.weight[lane] = wt;
+    // w_s = dt e^{c_end - c_s} forward, e^{c_t} backward
+    if (wv == 0) sm.weight[lane] = back ? st.before : st.after * st.dt;
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (tid >> 3) + 32 * i, c = (tid & 7) * 8;
-      float v[8], z[8];
+    for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        tile8<IO, 256>(in + t0 * gn + nb * kQ, gn, rows, N - nb * kQ, r, c, v);
-        put8(sm.in[nb], r, c, v);
-      }
-      tile8<IO, 256>(row + t0 * hp, hp, rows, pcols, r, c, v);
-      if (zrow) {
-        tile8<IO, 256>(zrow + t0 * hp, hp, rows, pcols, r, c, z);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= silu_f(z[j]);
-      }
-      put8(sm.row, r, c, v);
+      for (int j = 0; j < 8; ++j) v[j] = io[nb][j];
+      put8(sm.in[nb], r8, c8, v);
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[j] = ro[j];
+      if (zrow) v[j] *= zo[j] * sigmoid_f(zo[j]);
+    }
+    put8(sm.row, r8, c8, v);
+    if (k + 1 < nc) fetch(back ? ch - 1 : ch + 1);
     __syncthreads();
 #pragma unroll
-    for (int nt = 0; nt < 4 * NB; ++nt) S[nt] *= decay;
+    for (int i = 0; i < NT; ++i) S[i] *= decay;
 #pragma unroll 1
     for (int kb = 0; kb < kQ; kb += 16) {
-      const Frag x = scaled(down(sm.row, kb, 16 * wv, l16, g4), sm.weight, kb, g4);
+      const Frag x = scaled(down(sm.row, kb, 16 * pw, l16, g4), sm.weight, kb, g4);
 #pragma unroll
-      for (int nt = 0; nt < 4 * NB; ++nt)
-        S[nt] = mac(down(sm.in[nt / 4], kb, 16 * (nt & 3), l16, g4), x, S[nt]);
+      for (int i = 0; i < NT; ++i) {
+        const int nt = 2 * i + nw;
+        S[i] = mac(down(sm.in[nt / 4], kb, 16 * (nt & 3), l16, g4), x, S[i]);
+      }
     }
   }
   if (back && p.dh0) {
 #pragma unroll
-    for (int nt = 0; nt < 4 * NB; ++nt)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int n = 16 * nt + 4 * g4 + r;
-        if (live && n < N) p.dh0[((b * p.nheads + h) * N + n) * P + p0 + col] = S[nt][r];
+        const int n = 16 * (2 * i + nw) + 4 * g4 + r;
+        if (live && n < N) p.dh0[((b * p.nheads + h) * N + n) * P + p0 + col] = S[i][r];
       }
   }
 }
@@ -240,7 +225,7 @@ struct alignas(16) ChunkSmem {
   float s[kQ * kPitch];     // S_in, (n, p)
   float lam[kQ * kPitch];   // lam_out, (n, p)
   float m[kQ * kPitch];     // M, (t, s); at the end K
-  float dt[kQ], c2[kQ];     // step sizes, sums of log2 decays
+  float dt[kQ], c_hi[kQ], c_lo[kQ];  // step sizes, sums of log2 decays
   float before[kQ], w[kQ];  // e^{c_t}, dt_s e^{c_end - c_s}
   float after[kQ];          // e^{c_end - c_s}
   float erow[2][kQ], ecol[4][kQ];                 // sums of E, by the waves' tiles
@@ -301,10 +286,11 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
     __syncthreads();  // the previous head's values have been read
     if (wv == 0) {
       sm.dt[lane] = st.dt;
-      sm.c2[lane] = st.c;
-      sm.before[lane] = exp2_hw(st.c);
-      sm.after[lane] = exp2_hw(st.end - st.c);
-      sm.w[lane] = exp2_hw(st.end - st.c) * st.dt;
+      sm.c_hi[lane] = st.c_hi;
+      sm.c_lo[lane] = st.c_lo;
+      sm.before[lane] = st.before;
+      sm.after[lane] = st.after;
+      sm.w[lane] = st.after * st.dt;
     }
     // x and gy of a block of channels
     auto stage_rows = [&](int p0) {
@@ -337,11 +323,12 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = 16 * (tc + i) + l16;
-      const float cs = sm.c2[s], dts = sm.dt[s];
+      const float ch = sm.c_hi[s], cl = sm.c_lo[s], dts = sm.dt[s];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = row0 + r;
-        const float seg = s <= t ? exp2_hw(sm.c2[t] - cs) : 0.0f;
+        const float seg =
+            s <= t ? exp2_hw((sm.c_hi[t] - ch) + (sm.c_lo[t] - cl)) : 0.0f;
         const float m = s <= t ? G[i][r] * seg : 0.0f;
         const float k = s <= t ? W[i][r] * seg * dts : 0.0f;
         const float e = s < t ? W[i][r] * dts * m : 0.0f;
@@ -445,8 +432,8 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
             if (p.z) {
               const float z = IO::widen(static_cast<const E*>(p.z)[o]);
               const float go = IO::widen(static_cast<const E*>(p.dout)[o]);
-              const float sg = rcp_hw(1.0f + exp2_hw(-z * kLog2e));
-              static_cast<E*>(p.dz)[o] = IO::from_float(
+              const float sg = sigmoid_f(z);
+                  static_cast<E*>(p.dz)[o] = IO::from_float(
                   go * fmaf(Dh, x, Y[i][r]) * (sg * fmaf(z, 1.0f - sg, 1.0f)));
             }
           }
@@ -468,19 +455,18 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
     __syncthreads();
     if (wv == 0) {
       const float q = sm.near[0][lane] + sm.near[1][lane];
-      const float ps = st.dt * (sm.far[0][lane] + sm.far[1][lane]);
+      const double ps = static_cast<double>(st.dt) * (sm.far[0][lane] + sm.far[1][lane]);
       const double in = (static_cast<double>(sm.ecol[0][lane]) + sm.ecol[1][lane]) +
                         (static_cast<double>(sm.ecol[2][lane]) + sm.ecol[3][lane]);
       const double out = static_cast<double>(sm.erow[0][lane]) + sm.erow[1][lane];
-      // inclusive sums; what lies strictly before a step is the sum less its own
-      const double e = scan64(in - out, lane) - (in - out);
-      const float before = scan64(ps, lane) - ps;
-      const float since = __shfl(scan64(__shfl(q, 63 - lane), lane), 63 - lane);
+      // inclusive sums in float64; what lies before a step is the sum less its own
+      const double flow = in - out + ps, before = scan64(flow) - flow;
+      const double upto = scan64(q), since = last_lane(upto) - (upto - q);
       float ov = 0.0f;
       for (int k = 0; k < kThreads / 64; ++k) ov += sm.over[k];
-      const float dl = static_cast<float>(e) + (since + before) + exp2_hw(st.end) * ov;
+      const float dl = static_cast<float>(before + since + static_cast<double>(st.end) * ov);
       float ddt = fmaf(p.A[h], dl, sm.xv[0][lane] + sm.xv[1][lane]);
-      if (p.softplus) ddt *= rcp_hw(1.0f + exp2_hw(-st.raw * kLog2e));
+      ddt *= st.slope;
       if (lane >= rows) ddt = 0.0f;
       else
         static_cast<E*>(p.ddt)[(b * p.seqlen + t0 + lane) * H + h] = IO::from_float(ddt);
@@ -571,7 +557,7 @@ __global__ __launch_bounds__(256) void scan2_runs_kernel(const float* part, int6
 template <class IO, int NB>
 hipError_t launch_nb(const Scan2BwdArgs& a, hipStream_t stream) {
   const dim3 walks(static_cast<unsigned>(2 * a.batch * a.nheads * a.n_pblk));
-  hipLaunchKernelGGL((scan2_states_kernel<IO, NB>), walks, dim3(256), 0, stream, a);
+  hipLaunchKernelGGL((scan2_states_kernel<IO, NB>), walks, dim3(512), 0, stream, a);
   const dim3 chunks(static_cast<unsigned>(a.batch * a.n_chunks * a.ngroups * a.splits));
   hipLaunchKernelGGL((scan2_chunks_kernel<IO, NB>), chunks, dim3(kThreads), 0, stream, a);
   return hipGetLastError();

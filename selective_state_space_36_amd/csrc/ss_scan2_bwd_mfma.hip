@@ -11,6 +11,7 @@
 // laid out as the first one holds them: [d_state / 16][channel][16 states].
 #include "ss_head.h"
 #include "ss_mfma.h"
+#include "ss_scan2_bwd.h"
 
 namespace ss {
 namespace {
@@ -20,52 +21,6 @@ constexpr int kP = 64;
 constexpr int kPS = kP + 8;   // bf16 per row of the (step, channel) and (step, step) tiles: 36
                               // dwords, so that the four rows of a transpose read and the sixteen
                               // of a 16-byte read start in different banks
-
-// Inclusive sum of the log2 decays in float64, as float32 high and low parts: differences of them
-// are exponents, whose error is a relative one of the result.
-struct Step {
-  float raw, dt;
-  float c_hi, c_lo;
-  float before, after, end;  // 2^{c}, 2^{c_end - c}, 2^{c_end}
-};
-// x plus the value that the DPP control brings (0 where it brings none), in the rows of the mask.
-template <int CTRL, int ROWS, bool CLEAR>
-__device__ __forceinline__ double dpp_add(double x) {
-  const uint64_t w = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(w), CTRL, ROWS, 0xf, CLEAR);
-  const uint32_t hi =
-      __builtin_amdgcn_update_dpp(0, static_cast<int>(w >> 32), CTRL, ROWS, 0xf, CLEAR);
-  return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-// Inclusive sum over the 64 lanes, as wave_prefix_sum.
-__device__ __forceinline__ double scan64(double x) {
-  x = dpp_add<0x111, 0xf, true>(x);
-  x = dpp_add<0x112, 0xf, true>(x);
-  x = dpp_add<0x114, 0xf, true>(x);
-  x = dpp_add<0x118, 0xf, true>(x);
-  x = dpp_add<0x142, 0xa, false>(x);
-  return dpp_add<0x143, 0xc, false>(x);
-}
-__device__ __forceinline__ double last_lane(double x) {
-  const uint64_t w = __builtin_bit_cast(uint64_t, x);
-  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(w), 63);
-  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(w >> 32), 63);
-  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
-}
-__device__ __forceinline__ Step step_of(uint16_t dt, bool in, float bias, float A,
-                                        bool softplus) {
-  Step s;
-  s.raw = BF16::widen(dt) + bias;
-  s.dt = in ? (softplus ? softplus_f(s.raw) : s.raw) : 0.0f;
-  const double c = scan64(static_cast<double>(s.dt) * A * 1.4426950408889634);
-  const double end = last_lane(c);
-  s.c_hi = static_cast<float>(c);
-  s.c_lo = static_cast<float>(c - s.c_hi);
-  s.before = exp2_hw(s.c_hi) * (1.0f + s.c_lo * kLn2);
-  s.after = exp2_hw(static_cast<float>(end - c));
-  s.end = exp2_hw(static_cast<float>(end));
-  return s;
-}
 
 // A pair of bf16 in a word, high part above, and back.
 __device__ __forceinline__ void pair4(f32x4 v, uint4& w) {
@@ -92,10 +47,6 @@ __device__ __forceinline__ float dot_pairs(uint32_t a, uint32_t b, float c) {
   c = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(b2, b), c, false);
   return __builtin_amdgcn_fdot2_f32_bf16(
       v, __builtin_bit_cast(b2, __builtin_amdgcn_alignbit(b, b, 16)), c, false);
-}
-
-__device__ __forceinline__ float sigmoid_f(float z) {
-  return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
 }
 
 // ------------------------------------------------------------------ the states
@@ -159,7 +110,7 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
   // w_s = dt e^{c_end - c_s} forward, e^{c_t} backward; the same bits from every wave
   float decay = 1.0f;
   auto weigh = [&](int64_t ch, int buf) {
-    const Step s = step_of(dtr, ch * kQ + lane < L, bias, A, p.softplus);
+    const Step s = step_of(BF16::widen(dtr), ch * kQ + lane < L, bias, A, p.softplus);
     decay = s.end;
     sm.weight[buf][lane] = back ? s.before : s.after * s.dt;
   };
@@ -256,29 +207,8 @@ struct alignas(16) ChunkSmem {
   // sums for dl and ddt, by the tile they come from: E / dt over t and over s (strictly below the
   // diagonal), the diagonal of W M, q, p / dt
   float ecol[4][kQ], erow[4][kQ], ediag[kQ], near[2][kQ], far[2][kQ];
-  float over[kThreads / 64], diag[4];
+  float over[kThreads / 64], gx[kThreads / 64];  // <S_in, lam_out>, gy . x, by wave
 };
-
-// Sum over the four 16-lane rows of a wave, in each of them: an exchange of odd and even rows, then
-// of halves (both operands the same value: one result holds the first of each pair twice, the other
-// the second).
-__device__ __forceinline__ float sum_halves(float v) {
-  const uint32_t w = __float_as_uint(v);
-  const auto pair = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  return __uint_as_float(pair[0]) + __uint_as_float(pair[1]);
-}
-__device__ __forceinline__ float sum_rows(float v) {
-  const uint32_t w = __float_as_uint(v);
-  const auto pair = __builtin_amdgcn_permlane16_swap(w, w, false, false);
-  return sum_halves(__uint_as_float(pair[0]) + __uint_as_float(pair[1]));
-}
-__device__ __forceinline__ float sum16(float v) {
-  v += row_ror<8>(v);
-  v += row_ror<4>(v);
-  v += row_ror<2>(v);
-  return v + row_ror<1>(v);
-}
-__device__ __forceinline__ float sum64(float v) { return sum_rows(sum16(v)); }
 
 // 32 x 32 tiles: the operand's rows (or columns) are 32 of the tile, lane % 32 each, K = k0 + 8
 // (lane / 32) + 0..7; the result has column lane % 32, and in element 4 q + r row 8 q +
@@ -416,16 +346,19 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     const float col = (sm.ecol[0][lane] + sm.ecol[1][lane]) + (sm.ecol[2][lane] + sm.ecol[3][lane]);
     const float row = (sm.erow[0][lane] + sm.erow[1][lane]) + (sm.erow[2][lane] + sm.erow[3][lane]);
     const float xv = f + (col + sm.ediag[lane]);
-    float ov = 0.0f;
+    float ov = 0.0f, gx = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kThreads / 64; ++k) ov += sm.over[k];
+    for (int k = 0; k < kThreads / 64; ++k) {
+      ov += sm.over[k];
+      gx += sm.gx[k];
+    }
     // inclusive sums in float64; what lies before a step is the sum less its own
     const double in = static_cast<double>(st.dt) * col - row, ps = static_cast<double>(st.dt) * f;
     const double before = scan64(in + ps) - (in + ps);
     const double upto = scan64(q), since = last_lane(upto) - (upto - q);
     const float dl = static_cast<float>(before + since + static_cast<double>(st.end) * ov);
     float ddt = fmaf(A, dl, xv);
-    if (p.softplus) ddt *= sigmoid_f(st.raw);
+    ddt *= st.slope;
     if (lane < rows)
       static_cast<uint16_t*>(p.ddt)[(b * L + t0 + lane) * H + h] = BF16::from_float(ddt);
     else
@@ -434,7 +367,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     if (lane == 0) {
       float* line = p.head_part + (b * nc + ch) * 3 * H + h;
       line[0] = sa;
-      line[H] = (sm.diag[0] + sm.diag[1]) + (sm.diag[2] + sm.diag[3]);
+      line[H] = gx;
       line[2 * H] = sb;
     }
   };
@@ -455,7 +388,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     const float Dh = Dn;
     A = An;
     if (wv == 0 || wv == 7)
-      st = step_of(dtr, lane < rows, bn, A, p.softplus);
+      st = step_of(BF16::widen(dtr), lane < rows, bn, A, p.softplus);
     if (wv == 0) {
       sm.dt[lane] = st.dt;
       sm.c_hi[lane] = st.c_hi;
@@ -463,7 +396,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       sm.before[lane] = st.before;
       sm.after[lane] = st.after;
     }
-    float over = 0.0f;
+    float over = 0.0f, gx = 0.0f;
 #pragma unroll
     for (int k = 0; k < SK; ++k) {
       const int u = tid + kThreads * k, ch16 = (u >> 2) & (kP - 1), n = 16 * (u >> 8) + 4 * (u & 3);
@@ -488,6 +421,8 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
           a *= za * sigmoid_f(za);
           c *= zc * sigmoid_f(zc);
         }
+        const uint32_t xw = j == 0 ? xr.x : j == 1 ? xr.y : j == 2 ? xr.z : xr.w;
+        gx = fmaf(a, lo_f(xw), fmaf(c, hi_f(xw), gx));
         split2(a, c, hi[j], lo[j]);
       }
       *reinterpret_cast<uint4*>(&sm.ghi[r8][c8]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -514,7 +449,11 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
 
     // ---- W = X gy^T over the causal tiles; M dt to LDS, K into its sum, the sums of E
     over = sum64(over);
-    if (lane == 0) sm.over[wv] = over;
+    gx = sum64(gx);
+    if (lane == 0) {
+      sm.over[wv] = over;
+      sm.gx[wv] = gx;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i >= mine) continue;
@@ -549,18 +488,15 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       *reinterpret_cast<uint2*>(&sm.mhi[t][s0]) = h2;
       *reinterpret_cast<uint2*>(&sm.mlo[t][s0]) = l2;
       if (diag) {  // the diagonal itself apart
-        float ed = 0.0f, wd = 0.0f;
+        float ed = 0.0f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const bool on = s0 + r == t;
           ed += on ? e[r] : 0.0f;
-          wd += on ? W[r] : 0.0f;
           e[r] = on ? 0.0f : e[r];
         }
         ed = sum_rows(ed);
-        wd = sum64(wd);
         if (g4 == 0) sm.ediag[t] = ed;
-        if (lane == 0) sm.diag[ti[i]] = wd;
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {

@@ -980,10 +980,9 @@ def scan2_state_update_conv(state, conv_state, xbc, conv_weight, conv_bias, dt, 
     zs = _row_stride("z", z, dev, io, (batch, H * P)) if z is not None else 0
     if out is None:
         out = xbc.new_empty((batch, H, P))
-    l = lib()
-    nbytes = l.ss_scan2_state_update_conv_workspace_bytes(batch, H, P, ngroups, N)
-    ws, ws_len, keep = _scratch(workspace, nbytes, dev)
-    _check(l.ss_scan2_state_update_conv(
+    # (4 bytes a column: what ss_scan2_state_update_conv_workspace_bytes says, without the call)
+    ws, ws_len, keep = _scratch(workspace, 4 * batch * width, dev)
+    _check(lib().ss_scan2_state_update_conv(
         state.data_ptr(), _ptr(conv_state), xbc.data_ptr(), xs, conv_weight.data_ptr(),
         _ptr(conv_bias), k, dt.data_ptr(), ds, A.data_ptr(), _ptr(D), _ptr(z), zs, _ptr(dt_bias),
         1 if dt_softplus else 0, out.data_ptr(), batch, H, P, ngroups, N, code, ws, ws_len,
