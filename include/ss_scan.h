@@ -557,6 +557,9 @@ ss_status ss_causal_conv_update(void* conv_state, const void* x, const float* we
  *                       same time need one each.
  * d_state outside 1..256, headdim or nheads above 2^24 or seqlen above 2^31 - 1 ->
  * SS_ERR_UNSUPPORTED.  Outputs must not overlap inputs, each other or the workspace.
+ * The products are formed for 64 steps at a time, pairs in the wrong order times 0: an infinity or
+ * a NaN at a step reaches the gradients of other steps of its 64, also ones that do not depend on
+ * it (as in ss_scan2_fwd's matrix form).
  */
 ss_status ss_scan2_bwd(const void* x, const void* dt, const float* A, const void* B,
                        const void* C, const float* D, const void* z, const float* dt_bias,
@@ -639,7 +642,8 @@ ss_status ss_rms_norm_fwd(const void* x, const float* residual, const float* wei
  *     b mean(db scale b))
  *
  *   s            : (rows, dim) in `s_dtype`: x itself (s_dtype == dtype, where the forward had
- *                  none of residual, scale, norm_branch and dropout) or the sum it wrote.
+ *                  none of residual, scale, norm_branch and dropout) or the float32 sum it wrote
+ *                  (SS_ERR_INVALID_ARG otherwise, where the call shows it).
  *   x            : as the forward's; read for dscale and with norm_branch, else it may be NULL.
  *   rstd, branch_rstd : as the forward wrote them (branch_rstd with norm_branch only).
  *   weight, scale, p, rng : as the forward's.

@@ -752,6 +752,6 @@ const char* ss_status_string(ss_status s) {
 
 const char* ss_last_error(void) { return g_err; }
 
-int ss_version(void) { return 102; }
+int ss_version(void) { return 103; }
 
 }  // extern "C"

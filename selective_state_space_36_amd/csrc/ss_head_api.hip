@@ -313,6 +313,9 @@ ss_status ss_rms_norm_bwd(const void* dout, const void* sum, ss_dtype s_dtype,
   if (dim == 0) return ok();
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const bool some = n > 0, branch = norm_branch != 0;
+  if (s_dtype != SS_F32 && (branch || scale || a.drop.rng))
+    return fail(SS_ERR_INVALID_ARG, "s has to be the float32 sum with scale, norm_branch or "
+                "dropout");
   const size_t need = some && (dweight || dscale) ? ss::rms_bwd_ws_bytes(rows, dim) : 0;
   const bool want_x = branch || dscale;
   const Arr in[] = {{"dout", dout, n, es, some}, {"s", sum, n, ses, some},

@@ -108,6 +108,9 @@ REFUSED = [
     ("ss_rms_norm_fwd", NFWD, dict(rows=1 << 31, dim=1), BAD, b"too many rows"),
     ("ss_rms_norm_bwd", NBWD, dict(dx=None), BAD, b"both NULL"),
     ("ss_rms_norm_bwd", NBWD, dict(sdt=ops.SS_BF16, dtype=ops.SS_F32), UNS, b"s is either"),
+    ("ss_rms_norm_bwd", NBWD, dict(sdt=ops.SS_BF16, sc=8 * G), BAD, b"float32 sum"),
+    ("ss_rms_norm_bwd", NBWD, dict(sdt=ops.SS_BF16, br=1, brstd=8 * G), BAD, b"float32 sum"),
+    ("ss_rms_norm_bwd", NBWD, dict(sdt=ops.SS_BF16, p=0.5, rng=8 * G), BAD, b"float32 sum"),
     ("ss_rms_norm_bwd", NBWD, dict(x=None, dsc=8 * G), BAD, b"x is NULL"),
     ("ss_rms_norm_bwd", NBWD, dict(x=None, br=1, brstd=8 * G), BAD, b"x is NULL"),
     ("ss_rms_norm_bwd", NBWD, dict(br=1), BAD, b"branch_rstd is NULL"),
