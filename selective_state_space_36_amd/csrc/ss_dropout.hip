@@ -1,5 +1,6 @@
 // ss_dropout.hip -- dropout of a (rows, dim) array by the mask of ss_philox.h; its gradient is the
-// same call on the upstream gradient.
+// same call on the upstream gradient.  Memory and the generator bind it alike: 16384 x 2560 bf16, 168
+// MB, in 30.3 us (5.5 TB/s); the generator's multiplies alone would take about 25.
 #include "ss_head.h"
 #include "ss_octs.h"
 #include "ss_philox.h"

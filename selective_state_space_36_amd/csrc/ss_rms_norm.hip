@@ -6,6 +6,13 @@
 // each pass by the wide kernels.  Parameter gradients are added in registers while a workgroup
 // walks its units, written as one line per workgroup (or unit place) and summed by
 // column_sums_kernel in a fixed order.
+//
+// What bounds it: memory.  16384 x 2560 bf16 with residual, scale and dropout: forward 504 MB in
+// 106 us (4.8 TB/s; a copy of 1 GiB reaches 5.2), backward 756 MB in 140 us (5.4, some of it from the
+// 256 MB cache) and 5 us for the sums; the generator's 14 slots an element hide behind the loads.
+// Gated, 16384 x 5120 bf16, z part of longer rows: forward 504 MB in 140 us, backward 840 MB in 140
+// to 170.  One row: 2.8 us, a launch.  Non-temporal loads are kept to the backward: in the forward
+// they gain 11 us and cost the backward, which finds less in the cache, 20.
 #include "ss_head.h"
 #include "ss_octs.h"
 #include "ss_philox.h"

@@ -24,7 +24,10 @@
 // and ddt_bias, in a fixed order.
 //
 // All products run as v_mfma_f32_16x16x4_f32 here: operands of every type and size, exact in
-// float32.  Sizes that are not multiples of the tiles are filled with zeros.
+// float32.  Sizes that are not multiples of the tiles are filled with zeros.  What bounds it: the
+// float32 products (at 4 x 4096 x 80 heads the chunks took 2308 us, the states 1223; the bf16 kernels
+// of ss_scan2_bwd_mfma.hip take such calls) and, for few heads, the walk's latency: 3 x 777, 6 heads
+// of 48 x 40 float32, 36 workgroups and 13 chunks in a row, states 37 us, chunks 27.
 #include "ss_head.h"
 #include "ss_octs.h"
 #include "ss_rows.h"

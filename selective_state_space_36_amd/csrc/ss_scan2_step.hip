@@ -9,6 +9,12 @@
 // The convolution's window of B and C is shared by all heads of a group, and it is shifted in
 // place, so it is a kernel of its own in front of this one: x, B and C cross in float32 (the
 // workspace), unrounded.
+//
+// What bounds it: memory.  128 rows of 80 heads x 128 x 64: 671 MB of states in 115 us (5.8 TB/s,
+// non-temporal; four channels a lane, eight states of a lane in flight), the convolution's kernel 9
+// (two channels a lane the same: it waits for a window that nothing has left in a cache).  One row:
+// 5.9 us and 3.4 (latency; in 16-channel blocks, 320 workgroups), below the 15 us of the call on the
+// host.
 #include "ss_head.h"
 #include "ss_octs.h"
 #include "ss_rows.h"
