@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(const typename IO::elem* x
     const int n = left < 8 ? static_cast<int>(left) : 8;
     float v[8];
     load8<IO>(x + at, n, v);
-    drop8(v, key, static_cast<uint32_t>(oct), static_cast<uint32_t>(row), d.cut, d.up);
+    drop8(v, keep8(key, static_cast<uint32_t>(oct), static_cast<uint32_t>(row), d.cut), d.up);
     store8<IO>(out + at, n, v);
     row += w.drow;
     oct += w.doct;

@@ -45,17 +45,25 @@ __device__ __forceinline__ uint4 philox(const PhiloxKey& k, uint32_t col8, uint3
   return make_uint4(c0, c1, c2, c3);
 }
 
-// Drops among eight columns: v becomes v * up where its bits are at least `cut`, else 0 (chosen, not
-// multiplied: an infinity or a NaN that is dropped is gone).
-__device__ __forceinline__ void drop8(float (&v)[8], const PhiloxKey& k, uint32_t col8,
-                                      uint32_t row, uint32_t cut, float up) {
+// Which of eight columns are kept, bit j for column j: those whose bits are at least `cut`.
+__device__ __forceinline__ uint32_t keep8(const PhiloxKey& k, uint32_t col8, uint32_t row,
+                                          uint32_t cut) {
   const uint4 w = philox(k, col8, row);
   const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+  uint32_t keep = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t bits = j & 1 ? q[j >> 1] >> 16 : q[j >> 1] & 0xffffu;
-    v[j] = bits >= cut ? v[j] * up : 0.0f;
+    keep |= bits >= cut ? 1u << j : 0u;
   }
+  return keep;
+}
+
+// v times `up` where it is kept, else 0 (chosen, not multiplied: an infinity or a NaN that is dropped
+// is gone).
+__device__ __forceinline__ void drop8(float (&v)[8], uint32_t keep, float up) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = keep >> j & 1 ? v[j] * up : 0.0f;
 }
 
 }  // namespace ss

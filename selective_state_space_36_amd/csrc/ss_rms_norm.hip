@@ -102,8 +102,8 @@ __global__ __launch_bounds__(1024) void rms_fwd_kernel(RmsArgs p, UnitLayout l) 
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] *= s[j];
       }
-      if constexpr (DROP) drop8(v[k], key, c >> 3, static_cast<uint32_t>(w.row), p.drop.cut,
-                                p.drop.up);
+      if constexpr (DROP)
+        drop8(v[k], keep8(key, c >> 3, static_cast<uint32_t>(w.row), p.drop.cut), p.drop.up);
       if (p.residual) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] += r[k][j];
@@ -229,11 +229,15 @@ __global__ __launch_bounds__(MOST) void rms_bwd_kernel(RmsArgs p, UnitLayout l, 
 #pragma unroll
     for (int j = 0; j < 8; ++j) g[j] = fmaf(rs, fmaf(-sh[j], m1, g[j]), u[j]);
     if (p.dresidual) store8<F32>(p.dresidual + base + c, left, g);
-    if constexpr (DROP)
-      drop8(g, key, at.lane, static_cast<uint32_t>(row), p.drop.cut, p.drop.up);
+    uint32_t keep = 0xff;
+    if constexpr (DROP) {
+      keep = keep8(key, at.lane, static_cast<uint32_t>(row), p.drop.cut);
+      drop8(g, keep, p.drop.up);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      acc[1][j] = fmaf(g[j], x[j], acc[1][j]);
+      // (a dropped x is no factor, whatever it is)
+      if (!DROP || keep >> j & 1) acc[1][j] = fmaf(g[j], x[j], acc[1][j]);
       g[j] *= sc[j];
     }
     if (p.branch) {
@@ -399,7 +403,8 @@ __global__ __launch_bounds__(kWide) void rms_fwd_wide_kernel(RmsArgs p, UnitLayo
       if (p.scale) load8<F32>(p.scale + c, left, s);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= p.scale ? rb * s[j] : rb;
-      if constexpr (DROP) drop8(v, key, c >> 3, static_cast<uint32_t>(row), p.drop.cut, p.drop.up);
+      if constexpr (DROP)
+        drop8(v, keep8(key, c >> 3, static_cast<uint32_t>(row), p.drop.cut), p.drop.up);
       if (p.residual) {
         load8<F32>(p.residual + base + c, left, s);
 #pragma unroll
@@ -491,7 +496,12 @@ __global__ __launch_bounds__(kWide) void rms_bwd_wide_kernel(RmsArgs p, UnitLayo
         g[j] = fmaf(rstd, fmaf(-sh[j], m1, g[j]), p.dsum ? u[j] : 0.0f);
     };
     auto drop = [&](int c, float (&g)[8]) {
-      if constexpr (DROP) drop8(g, key, c >> 3, static_cast<uint32_t>(row), p.drop.cut, p.drop.up);
+      uint32_t keep = 0xff;
+      if constexpr (DROP) {
+        keep = keep8(key, c >> 3, static_cast<uint32_t>(row), p.drop.cut);
+        drop8(g, keep, p.drop.up);
+      }
+      return keep;
     };
     auto hat = [&](int c, int left, float (&x)[8]) {
       load8<IO>(static_cast<const E*>(p.x) + base + c, left, x);
@@ -517,11 +527,11 @@ __global__ __launch_bounds__(kWide) void rms_bwd_wide_kernel(RmsArgs p, UnitLayo
       float g[8], x[8], ds[8];
       dsum(c, left, g);
       if (p.dresidual) store8<F32>(p.dresidual + base + c, left, g);
-      drop(c, g);
+      const uint32_t keep = drop(c, g);
       if (p.x) {
         hat(c, left, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ds[j] = g[j] * x[j];
+        for (int j = 0; j < 8; ++j) ds[j] = keep >> j & 1 ? g[j] * x[j] : 0.0f;
         if (line) add_line(line + l.width + c, left, ds, first);
       }
       weigh(p.scale, c, left, g);

@@ -137,6 +137,27 @@ def test_norm_of_a_fully_dropped_branch():
     assert torch.all(out == 0) and torch.all(s == 0)
 
 
+@pytest.mark.parametrize("dim", [200, 17000])
+def test_norm_ignores_what_is_dropped(dim):
+    """Infinities and NaN where dropout drops: as if zeros stood there, in every output."""
+    o = ops()
+    seed, p = (11, 5), 0.4
+    keep = torch.from_numpy(ht.keep_mask(seed, 4, dim, p)).cuda()
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    x, res, w, sc, dout = r(4, dim), r(4, dim), r(dim), r(dim), r(4, dim)
+    bad = torch.where(keep, x, torch.tensor(float("nan"), device="cuda"))
+    bad[0] = torch.where(keep[0], x[0], torch.tensor(float("inf"), device="cuda"))
+    kw = dict(scale=sc, p=p, rng=rng_of(*seed))
+    got = []
+    for v in (torch.where(keep, x, torch.zeros_like(x)), bad):
+        out, s, rstd, _ = o.rms_norm_fwd(v, w, residual=res, return_stats=True, **kw)
+        g = o.rms_norm_bwd(dout, s, w, rstd, x=v, want_dresidual=True, **kw)
+        got.append((out, s, *g.values()))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
 def test_norm_rows_keep_to_themselves():
     """An infinity or a NaN in one row stays there."""
     o = ops()
