@@ -98,7 +98,7 @@ ss_status ss_scan2_bwd(const void* x, const void* dt, const float* A, const void
                  sizeof(float)
            : 0;
   if (some) {
-    if ((s = check_grid(2 * n.heads * a.n_pblk, 512)) != SS_OK) return s;
+    if ((s = check_grid(2 * n.heads * a.n_pblk * (a.cut ? n.chunks : 1), 512)) != SS_OK) return s;
     if ((s = check_grid(batch * n.chunks * ngroups * a.splits, 512)) != SS_OK) return s;
   }
   const Arr in[] = {{"x", x, n.elems, es, some}, {"dt", dt, n.dts, es, some},

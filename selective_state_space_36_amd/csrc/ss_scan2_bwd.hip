@@ -17,7 +17,8 @@
 //     ddt = (A dl + x . V) softplus',   dA = sum dt dl,   dD = sum gy x
 //
 // Three launches.  states: one workgroup per (batch row, head, 64 channels) walks the chunks and
-// writes S_in, others walk them backwards and write lam_out (their state in registers).  chunks:
+// writes S_in, others walk them backwards and write lam_out (their state in registers); for few
+// heads there is one per chunk instead, from a state of 0, and a fourth launch joins them.  chunks:
 // one workgroup per (batch row, chunk, run of heads of one group) forms everything else, and adds
 // K, e^c gy S_in^T and w X lam_out^T over its heads in registers, so that C B^T is formed once for
 // them and dB and dC leave once.  sums: dB and dC over the runs, and the per-chunk sums of dA, dD
@@ -26,17 +27,16 @@
 // All products run as v_mfma_f32_16x16x4_f32 here: operands of every type and size, exact in
 // float32.  Sizes that are not multiples of the tiles are filled with zeros.  What bounds it: the
 // float32 products (at 4 x 4096 x 80 heads the chunks took 2308 us, the states 1223; the bf16 kernels
-// of ss_scan2_bwd_mfma.hip take such calls) and, for few heads, the walk's latency: 3 x 777, 6 heads
-// of 48 x 40 float32, 36 workgroups and 13 chunks in a row, states 37 us, chunks 27.
+// of ss_scan2_bwd_mfma.hip take such calls) and, for few heads, latency: 3 x 777, 6 heads of 48 x 40
+// float32, 36 walks of 13 chunks, states 10 us and their join 5 (37 walked whole), chunks 27.
 #include "ss_head.h"
+#include "ss_mfma.h"
 #include "ss_octs.h"
 #include "ss_rows.h"
 #include "ss_scan2_bwd.h"
 
 namespace ss {
 namespace {
-
-using f32x4 = float __attribute__((ext_vector_type(4)));
 
 constexpr int kQ = kScan2BwdChunk;   // steps of a chunk, and the side of every tile
 constexpr int kPitch = kQ + 4;       // floats per tile row: 16 rows start 4 banks apart, so 16-byte
@@ -126,6 +126,9 @@ __global__ __launch_bounds__(512) void scan2_states_kernel(Scan2BwdArgs p) {
   const int64_t half = gridDim.x / 2;
   const bool back = blockIdx.x >= half;
   int64_t w = back ? blockIdx.x - half : blockIdx.x;
+  // a walk that is cut: this workgroup has one chunk, from a state of 0
+  const int64_t only = p.cut ? w % p.n_chunks : 0;
+  if (p.cut) w /= p.n_chunks;
   const int64_t pb = w % p.n_pblk;
   w /= p.n_pblk;
   const int64_t b = w / p.nheads, h = w - b * p.nheads, grp = h / (p.nheads / p.ngroups);
@@ -137,7 +140,7 @@ __global__ __launch_bounds__(512) void scan2_states_kernel(Scan2BwdArgs p) {
   const E* row = static_cast<const E*>(back ? p.dout : p.x) + b * p.seqlen * hp + h * P + p0;
   const E* zrow = back && p.z ? static_cast<const E*>(p.z) + b * p.seqlen * hp + h * P + p0
                               : nullptr;
-  const float* init = back ? p.dh_last : p.h0;
+  const float* init = p.cut ? nullptr : back ? p.dh_last : p.h0;
   const int col = 16 * pw + l16;  // this lane's channel of the block
   const bool live = col < pcols;
   const int r8 = tid >> 3, c8 = (tid & 7) * 8;
@@ -163,10 +166,7 @@ __global__ __launch_bounds__(512) void scan2_states_kernel(Scan2BwdArgs p) {
                     ? init[((b * p.nheads + h) * N + n) * P + p0 + col]
                     : 0.0f;
     }
-  fetch(back ? nc - 1 : 0);
-  for (int64_t k = 0; k < nc; ++k) {
-    const int64_t ch = back ? nc - 1 - k : k;
-    float* out = ws + ch * N * P;
+  auto store = [&](float* out) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -174,6 +174,13 @@ __global__ __launch_bounds__(512) void scan2_states_kernel(Scan2BwdArgs p) {
         const int n = 16 * (2 * i + nw) + 4 * g4 + r;
         if (live && n < N) out[static_cast<int64_t>(n) * P + col] = S[i][r];
       }
+  };
+  const int64_t steps_of_walk = p.cut ? 1 : nc;
+  const int64_t first = p.cut ? only : back ? nc - 1 : 0;
+  fetch(first);
+  for (int64_t k = 0; k < steps_of_walk; ++k) {
+    const int64_t ch = back ? first - k : first + k;
+    if (!p.cut) store(ws + ch * N * P);
     const float decay = st.end;
     __syncthreads();  // the previous chunk's tiles have been read
     // w_s = dt e^{c_end - c_s} forward, e^{c_t} backward
@@ -191,7 +198,7 @@ __global__ __launch_bounds__(512) void scan2_states_kernel(Scan2BwdArgs p) {
       if (zrow) v[j] *= zo[j] * sigmoid_f(zo[j]);
     }
     put8(sm.row, r8, c8, v);
-    if (k + 1 < nc) fetch(back ? ch - 1 : ch + 1);
+    if (k + 1 < steps_of_walk) fetch(back ? ch - 1 : ch + 1);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < NT; ++i) S[i] *= decay;
@@ -205,7 +212,11 @@ __global__ __launch_bounds__(512) void scan2_states_kernel(Scan2BwdArgs p) {
       }
     }
   }
-  if (back && p.dh0) {
+  if (p.cut) {
+    store(ws + only * N * P);
+    if (tid == 0 && pb == 0)
+      p.decay[((back ? p.batch : 0) * p.nheads + b * p.nheads + h) * nc + only] = st.end;
+  } else if (back && p.dh0) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -529,6 +540,54 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
   }
 }
 
+// Where walks are cut, S' = decay S + part along the chunks: one value of a state per lane and
+// direction, whose slots hold the chunks' own parts and take what lies before (behind) each chunk.
+// Latency bounds it, so eight chunks' parts are in flight (5 us for 13 chunks of 18 heads of 48 x 40).
+template <bool PAIRS>
+__global__ __launch_bounds__(256) void scan2_join_kernel(Scan2BwdArgs p) {
+  const int64_t np = static_cast<int64_t>(p.d_state) * p.headdim, heads = p.batch * p.nheads;
+  const int64_t all = heads * np, nc = p.n_chunks;
+  int64_t i = blockIdx.x * 256ll + threadIdx.x;
+  if (i >= 2 * all) return;
+  const bool back = i >= all;
+  if (back) i -= all;
+  const int64_t bh = i / np;
+  const int e = static_cast<int>(i - bh * np);
+  // the value's place in h0, dh_last and dh0: (state, channel)
+  const int64_t at = PAIRS ? bh * np + (e / (16 * p.headdim) * 16 + e % 16) * p.headdim +
+                                 e / 16 % p.headdim
+                           : i;
+  const float* init = back ? p.dh_last : p.h0;
+  float* slot = (back ? p.lam : p.states) + bh * nc * np + e;
+  const float* decay = p.decay + ((back ? heads : 0) + bh) * nc;
+  float S = init ? init[at] : 0.0f;
+  constexpr int kAhead = 8;
+  for (int64_t k = 0; k < nc; k += kAhead) {
+    float part[kAhead], d[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (k + j < nc) {
+        const int64_t ch = back ? nc - 1 - (k + j) : k + j;
+        part[j] = slot[ch * np];
+        d[j] = decay[ch];
+      }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (k + j < nc) {
+        const int64_t ch = back ? nc - 1 - (k + j) : k + j;
+        if constexpr (PAIRS) {
+          uint32_t hi, lo;
+          split2(S, 0.0f, hi, lo);
+          slot[ch * np] = __uint_as_float(hi << 16 | (lo & 0xffffu));
+        } else {
+          slot[ch * np] = S;
+        }
+        S = fmaf(d[j], S, part[j]);
+      }
+  }
+  if (back && p.dh0) p.dh0[at] = S;
+}
+
 // dB and dC: the runs of heads added in order.
 template <class IO>
 __global__ __launch_bounds__(256) void scan2_runs_kernel(const float* part, int64_t n,
@@ -559,8 +618,13 @@ __global__ __launch_bounds__(256) void scan2_runs_kernel(const float* part, int6
 
 template <class IO, int NB>
 hipError_t launch_nb(const Scan2BwdArgs& a, hipStream_t stream) {
-  const dim3 walks(static_cast<unsigned>(2 * a.batch * a.nheads * a.n_pblk));
+  const dim3 walks(
+      static_cast<unsigned>(2 * a.batch * a.nheads * a.n_pblk * (a.cut ? a.n_chunks : 1)));
   hipLaunchKernelGGL((scan2_states_kernel<IO, NB>), walks, dim3(512), 0, stream, a);
+  if (a.cut) {
+    const hipError_t e = launch_scan2_join(a, false, stream);
+    if (e != hipSuccess) return e;
+  }
   const dim3 chunks(static_cast<unsigned>(a.batch * a.n_chunks * a.ngroups * a.splits));
   hipLaunchKernelGGL((scan2_chunks_kernel<IO, NB>), chunks, dim3(kThreads), 0, stream, a);
   return hipGetLastError();
@@ -600,6 +664,25 @@ int64_t round16(int64_t floats) { return (floats + 3) / 4 * 4; }
 
 }  // namespace
 
+hipError_t launch_scan2_join(const Scan2BwdArgs& a, bool pairs, hipStream_t stream) {
+  const int64_t n = 2 * a.batch * a.nheads * a.d_state * a.headdim;
+  const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+  if (pairs) hipLaunchKernelGGL(scan2_join_kernel<true>, grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL(scan2_join_kernel<false>, grid, dim3(256), 0, stream, a);
+  return hipGetLastError();
+}
+
+// Walks too few to fill the 256 CUs are cut into their chunks, which costs one more launch and the
+// states read and written once more.  The whole call, walks whole -> cut: bf16, headdim 64, d_state
+// 128, one batch row: 8 heads x 4096 steps 191 -> 70 us, 24 x 4096 224 -> 145, 48 x 2048 149 -> 137,
+// 48 x 512 66 -> 66, 64 x 4096 331 -> 354, 24 x 256 44 -> 44, 24 x 128 36 -> 39; float32: 3 x 777,
+// 6 heads of 48 x 40, 76 -> 48, 1 x 16384, 24 heads of 64 x 128, 1972 -> 1242, 1 x 4096, 64 heads,
+// 831 -> 858.
+constexpr int64_t kCutWalks = 96, kCutChunks = 4;
+bool scan2_bwd_cut(int64_t heads, int64_t n_pblk, int64_t nc) {
+  return 2 * heads * n_pblk <= kCutWalks && nc >= kCutChunks;
+}
+
 // Runs of heads: a workgroup for each of the 256 CUs (one fits a CU), at most a head each.
 int64_t scan2_bwd_splits(int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngroups) {
   const int64_t units = batch * ((seqlen + kQ - 1) / kQ) * ngroups, hg = nheads / ngroups;
@@ -613,17 +696,22 @@ int64_t scan2_bwd_ws_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64
   const int64_t splits = scan2_bwd_splits(batch, seqlen, nheads, ngroups);
   const int64_t states = round16(batch * nheads * nc * d_state * headdim);
   const int64_t heads = round16(batch * nc * 3 * nheads);
-  const int64_t runs = splits > 1 ? splits * 2 * batch * seqlen * ngroups * d_state : 0;
+  const int64_t runs = splits > 1 ? round16(splits * 2 * batch * seqlen * ngroups * d_state) : 0;
+  const int64_t n_pblk = (headdim + kQ - 1) / kQ;
+  const bool cut = scan2_bwd_cut(batch * nheads, n_pblk, nc);
+  const int64_t decays = cut ? 2 * batch * nheads * nc : 0;
   if (a) {
     a->n_chunks = nc;
     a->splits = splits;
-    a->n_pblk = (headdim + kQ - 1) / kQ;
+    a->n_pblk = n_pblk;
+    a->cut = cut;
     a->states = ws;
     a->lam = ws + states;
     a->head_part = a->lam + states;
     a->bc_part = a->head_part + heads;
+    a->decay = a->bc_part + runs;
   }
-  return 2 * states + heads + runs;
+  return 2 * states + heads + runs + decays;
 }
 
 hipError_t launch_scan2_bwd(const Scan2BwdArgs& a, bool bf16, hipStream_t stream) {

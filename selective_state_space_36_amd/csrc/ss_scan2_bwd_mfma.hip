@@ -70,18 +70,20 @@ struct alignas(16) StateSmem {
 };
 
 // One workgroup per (batch row, head) and direction; wave w owns channels 16 w .. 16 w + 15.
-template <int N>
+template <int N, bool CUT>
 __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) {
   constexpr int NT = N / 16;
   constexpr int UNITS = 2 * N, UPT = (UNITS + 255) / 256;  // (4-step, 8-state) pieces
   __shared__ StateSmem<N> sm;
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g4 = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t pairs = p.batch * p.nheads;
-  const bool back = blockIdx.x >= pairs;
-  const int64_t bh = xcd_remap(back ? blockIdx.x - pairs : blockIdx.x, pairs);
+  // a walk that is cut: a workgroup has one chunk, from a state of 0
+  const int64_t nc = p.n_chunks, units = p.batch * p.nheads * (CUT ? nc : 1);
+  const bool back = blockIdx.x >= units;
+  const int64_t unit = xcd_remap(back ? blockIdx.x - units : blockIdx.x, units);
+  const int64_t bh = CUT ? unit / nc : unit, only = CUT ? unit - bh * nc : 0;
   const int64_t b = bh / p.nheads, h = bh - b * p.nheads, grp = h / (p.nheads / p.ngroups);
-  const int64_t L = p.seqlen, nc = p.n_chunks, H = p.nheads, gn = p.ngroups * N, hp = H * kP;
+  const int64_t L = p.seqlen, H = p.nheads, gn = p.ngroups * N, hp = H * kP;
   const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
   const uint16_t* in = static_cast<const uint16_t*>(back ? p.C : p.B) + b * L * gn + grp * N;
   const uint16_t* row = static_cast<const uint16_t*>(back ? p.dout : p.x) + b * L * hp + h * kP;
@@ -89,7 +91,7 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
       back && p.z ? static_cast<const uint16_t*>(p.z) + b * L * hp + h * kP : nullptr;
   const uint16_t* dtg = static_cast<const uint16_t*>(p.dt) + b * L * H + h;
   uint4* ws = reinterpret_cast<uint4*>(back ? p.lam : p.states) + bh * nc * (N * kP / 4);
-  const float* init = back ? p.dh_last : p.h0;
+  const float* init = CUT ? nullptr : back ? p.dh_last : p.h0;
   const int rq = tid >> 4, rp = tid & 15;  // this thread's 4 steps x 4 channels of the rows
 
   uint2 xr[4], zr[4];
@@ -133,10 +135,11 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
     for (int r = 0; r < 4; ++r)
       S[nt][r] = init ? init[(bh * N + 16 * nt + 4 * g4 + r) * kP + 16 * wv + l16] : 0.0f;
 
-  fetch(back ? nc - 1 : 0);
-  weigh(back ? nc - 1 : 0, 0);
-  for (int64_t k = 0; k < nc; ++k) {
-    const int64_t ch = back ? nc - 1 - k : k;
+  const int64_t chunks = CUT ? 1 : nc, first = CUT ? only : back ? nc - 1 : 0;
+  fetch(first);
+  weigh(first, 0);
+  for (int64_t k = 0; k < chunks; ++k) {
+    const int64_t ch = back ? first - k : first + k;
     __syncthreads();  // the previous chunk's tiles have been read, this one's weights are there
 #pragma unroll
     for (int u8 = 0; u8 < UPT; ++u8) {
@@ -165,14 +168,16 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
     // the state before the chunk leaves before the next loads are issued, which would be waited
     // for together with it
     uint4* out = ws + ch * (N * kP / 4) + (16 * wv + l16) * 4 + g4;
+    if (!CUT) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint4 w;
-      pair4(S[nt], w);
-      out[nt * kP * 4] = w;
+      for (int nt = 0; nt < NT; ++nt) {
+        uint4 w;
+        pair4(S[nt], w);
+        out[nt * kP * 4] = w;
+      }
     }
     const float d = decay;
-    const bool more = k + 1 < nc;
+    const bool more = k + 1 < chunks;
     const int64_t next = back ? ch - 1 : ch + 1;
     if (more) fetch(next);
     __syncthreads();
@@ -192,7 +197,12 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
     if (more) weigh(next, (k + 1) & 1);
     lds_reads_done();
   }
-  if (back && p.dh0) {
+  if (CUT) {  // the chunk's own part, in float32
+    uint4* out = ws + only * (N * kP / 4) + (16 * wv + l16) * 4 + g4;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) out[nt * kP * 4] = __builtin_bit_cast(uint4, S[nt]);
+    if (tid == 0) p.decay[((back ? p.batch : 0) * H + bh) * nc + only] = decay;
+  } else if (back && p.dh0) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -679,8 +689,16 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
 
 template <int N>
 hipError_t launch_n(const Scan2BwdArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(scan2_states_mfma_kernel<N>,
-                     dim3(static_cast<unsigned>(2 * a.batch * a.nheads)), dim3(256), 0, stream, a);
+  const int64_t walks = 2 * a.batch * a.nheads;
+  if (a.cut) {
+    hipLaunchKernelGGL((scan2_states_mfma_kernel<N, true>),
+                       dim3(static_cast<unsigned>(walks * a.n_chunks)), dim3(256), 0, stream, a);
+    const hipError_t e = launch_scan2_join(a, true, stream);
+    if (e != hipSuccess) return e;
+  } else {
+    hipLaunchKernelGGL((scan2_states_mfma_kernel<N, false>), dim3(static_cast<unsigned>(walks)),
+                       dim3(256), 0, stream, a);
+  }
   const dim3 grid(static_cast<unsigned>(a.batch * a.n_chunks * a.ngroups * a.splits));
   if (a.z)
     hipLaunchKernelGGL((scan2_chunks_mfma_kernel<N, true>), grid, dim3(kThreads), 0, stream, a);

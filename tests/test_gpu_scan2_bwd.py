@@ -106,6 +106,15 @@ def test_runs_of_heads(H, G, batch):
     Case(H, batch, 80, H, 16, G, 16, "f32").check()
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 300, 40, 64, 1, 64), (1, 270, 70, 16, 2, 24),
+                                   (3, 256, 2, 64, 1, 128), (1, 1100, 3, 64, 3, 64),
+                                   (1, 700, 2, 70, 1, 20)], ids=str)
+def test_walks_whole_and_cut(shape, io):
+    """Many heads walk the chunks whole, few are cut into chunks and joined."""
+    Case(sum(shape), *shape, io).check()
+
+
 def test_two_runs_agree_bit_for_bit():
     c = Case(11, 2, 300, 8, 64, 1, 128, "bf16")
     a, b = c.run(), c.run()
