@@ -31,6 +31,24 @@ __device__ __forceinline__ float sum16(float v) {
 }
 __device__ __forceinline__ float sum64(float v) { return sum_rows(sum16(v)); }
 
+// The same of float64 values.
+__device__ __forceinline__ double sum_halves(double v) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = static_cast<uint32_t>(w), hi = static_cast<uint32_t>(w >> 32);
+  const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+  const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(h[0]) << 32 | l[0]) +
+         __builtin_bit_cast(double, static_cast<uint64_t>(h[1]) << 32 | l[1]);
+}
+__device__ __forceinline__ double sum_rows(double v) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = static_cast<uint32_t>(w), hi = static_cast<uint32_t>(w >> 32);
+  const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+  const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+  return sum_halves(__builtin_bit_cast(double, static_cast<uint64_t>(h[0]) << 32 | l[0]) +
+                    __builtin_bit_cast(double, static_cast<uint64_t>(h[1]) << 32 | l[1]));
+}
+
 // Inclusive sum of the log2 decays in float64, as float32 high and low parts: differences of them
 // are exponents, whose error is a relative one of the result.
 struct Step {
@@ -46,6 +64,13 @@ __device__ __forceinline__ double dpp_add(double x) {
   const uint32_t hi =
       __builtin_amdgcn_update_dpp(0, static_cast<int>(w >> 32), CTRL, ROWS, 0xf, CLEAR);
   return x + __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Over the 16 lanes of a row (each has its source), in each of them.
+__device__ __forceinline__ double sum16(double v) {
+  v = dpp_add<0x128, 0xf, true>(v);
+  v = dpp_add<0x124, 0xf, true>(v);
+  v = dpp_add<0x122, 0xf, true>(v);
+  return dpp_add<0x121, 0xf, true>(v);
 }
 // Inclusive sum over the 64 lanes, as wave_prefix_sum.
 __device__ __forceinline__ double scan64(double x) {

@@ -227,7 +227,8 @@ struct alignas(16) ChunkSmem {
   float dt[kQ], c_hi[kQ], c_lo[kQ], before[kQ], after[kQ];
   // sums for dl and ddt, by the tile they come from: E / dt over t and over s (strictly below the
   // diagonal), the diagonal of W M, q, p / dt
-  float ecol[4][kQ], erow[4][kQ], ediag[kQ], near[2][kQ], far[2][kQ];
+  double ecol[4][kQ], erow[4][kQ];
+  float ediag[kQ], near[2][kQ], far[2][kQ];
   float over[kThreads / 64], gx[kThreads / 64];  // <S_in, lam_out>, gy . x, by wave
 };
 
@@ -292,7 +293,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     uint4* m = reinterpret_cast<uint4*>(&sm.mhi[0][0]);
     for (int i = tid; i < 2 * kQ * kPS * 2 / 16; i += kThreads) m[i] = make_uint4(0, 0, 0, 0);
   }
-  for (int i = tid; i < 4 * kQ; i += kThreads) (&sm.ecol[0][0])[i] = (&sm.erow[0][0])[i] = 0.0f;
+  for (int i = tid; i < 4 * kQ; i += kThreads) (&sm.ecol[0][0])[i] = (&sm.erow[0][0])[i] = 0.0;
   __syncthreads();
 
   // The causal 16x16 tiles (s-tile ti <= t-tile tj), dealt to the waves in the order (0,0) (0,1)
@@ -364,9 +365,11 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
   auto finish = [&](int64_t h, float A, const Step& st) {
     const float q = sm.near[0][lane] + sm.near[1][lane];
     const float f = sm.far[0][lane] + sm.far[1][lane];
-    const float col = (sm.ecol[0][lane] + sm.ecol[1][lane]) + (sm.ecol[2][lane] + sm.ecol[3][lane]);
-    const float row = (sm.erow[0][lane] + sm.erow[1][lane]) + (sm.erow[2][lane] + sm.erow[3][lane]);
-    const float xv = f + (col + sm.ediag[lane]);
+    const double col =
+        (sm.ecol[0][lane] + sm.ecol[1][lane]) + (sm.ecol[2][lane] + sm.ecol[3][lane]);
+    const double row =
+        (sm.erow[0][lane] + sm.erow[1][lane]) + (sm.erow[2][lane] + sm.erow[3][lane]);
+    const float xv = f + (static_cast<float>(col) + sm.ediag[lane]);
     float ov = 0.0f, gx = 0.0f;
 #pragma unroll
     for (int k = 0; k < kThreads / 64; ++k) {
@@ -374,7 +377,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       gx += sm.gx[k];
     }
     // inclusive sums in float64; what lies before a step is the sum less its own
-    const double in = static_cast<double>(st.dt) * col - row, ps = static_cast<double>(st.dt) * f;
+    const double in = st.dt * col - row, ps = static_cast<double>(st.dt) * f;
     const double before = scan64(in + ps) - (in + ps);
     const double upto = scan64(q), since = last_lane(upto) - (upto - q);
     const float dl = static_cast<float>(before + since + static_cast<double>(st.end) * ov);
@@ -492,7 +495,8 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       const float4 dt4 = *reinterpret_cast<const float4*>(&sm.dt[s0]);
       const float ch[4] = {csh.x, csh.y, csh.z, csh.w}, cl[4] = {csl.x, csl.y, csl.z, csl.w};
       const float dts[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
-      float m[4], e[4], row = 0.0f;
+      float m[4], e[4];
+      double row = 0.0, col[4];
       const bool diag = ti[i] == tj[i];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -521,13 +525,15 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        row = fmaf(e[r], dts[r], row);
-        e[r] = sum16(e[r]);
+        row = fma(static_cast<double>(e[r]), static_cast<double>(dts[r]), row);
+        col[r] = sum16(static_cast<double>(e[r]));
       }
       row = sum_rows(row);
       if (g4 == 0) sm.erow[ti[i]][t] = row;
-      if (l16 == 0)
-        *reinterpret_cast<float4*>(&sm.ecol[tj[i]][s0]) = make_float4(e[0], e[1], e[2], e[3]);
+      if (l16 == 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sm.ecol[tj[i]][s0 + r] = col[r];
+      }
     }
 
     // ---- S_in^T C^T or lam_out^T B^T

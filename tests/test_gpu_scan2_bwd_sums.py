@@ -1,0 +1,49 @@
+"""What the multi-head scan's gradients keep of float32: sums that cancel, exponents, and the sums
+over all tokens (dA, dD, ddt_bias), against float64 on the same inputs."""
+import pytest
+
+from oracle.rounding import U
+from tests.block_helpers import DTYPES
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from selective_state_space_36_amd import ops
+    ops.lib()
+    yield
+
+
+def ops():
+    from selective_state_space_36_amd import ops as o
+    return o
+
+
+@pytest.mark.parametrize("N", [64, 128, 16])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_steps_of_unlike_size(io, N):
+    """Step 0 reaches step 1 with 2^26 and step 5 with 1.  At steps 2 to 5 only the second passes,
+    from step 6 on nothing does: ddt there is A e^{5 A} and 0, though the first is 2^26 times as
+    large.  One product passes: its exponential is off by the exponent's rounding (|c| < 1, so 2 U),
+    one ulp of exp2 (2 U) and the sum of log decays (2 U), the products by A, dt and 1 / (1 + ...)
+    by U each: 10 U."""
+    o, dt = ops(), DTYPES[io]
+    L, P, A = 16, 64, -2.0 ** -4
+    z = lambda *s: torch.zeros(s, device="cuda", dtype=dt)  # noqa: E731
+    x, B, C, dout = z(1, L, 1, P), z(1, L, 1, N), z(1, L, 1, N), z(1, L, 1, P)
+    B[..., 0] = C[..., 0] = 1
+    x[0, 0, 0, 0], x[0, 0, 0, 1] = 2 ** 13, 1
+    dout[0, 1, 0, 0], dout[0, 5, 0, 1] = 2 ** 13, 1
+    g = o.scan2_bwd(x, torch.ones(1, L, 1, device="cuda", dtype=dt),
+                    torch.full((1,), A, device="cuda"), B, C, dout, dt_softplus=False)
+    ddt = g["ddt"][0, :, 0].double().cpu()
+    want = A * float(torch.tensor(5 * A, dtype=torch.float64).exp())
+    tol = 10 * U + (2 ** -8 if io == "bf16" else 0)
+    for t in range(2, 6):
+        assert abs(float(ddt[t]) - want) <= tol * abs(want), (t, float(ddt[t]), want)
+    assert torch.all(ddt[6:] == 0), ddt
