@@ -105,7 +105,12 @@ __device__ __forceinline__ Step step_of(float dt, bool in, float bias, float A, 
     s.slope = raw >= 0.0f ? r : e * r;
   }
   s.dt = in ? s.dt : 0.0f;
-  const double c = scan64(static_cast<double>(s.dt) * A * 1.4426950408889634);
+  // A step's decay below 2^-10^6 is 0 with all its products.  Held there (and at 2^10^6), sums of 64 of
+  // them stay in float32's range, and so do their differences: an A of the type's lowest value, which
+  // lets no state through, would give infinity less infinity.
+  double log2a = static_cast<double>(s.dt) * A * 1.4426950408889634;
+  log2a = log2a < -1e6 ? -1e6 : log2a > 1e6 ? 1e6 : log2a;
+  const double c = scan64(log2a);
   const double end = last_lane(c);
   s.c_hi = static_cast<float>(c);
   s.c_lo = static_cast<float>(c - s.c_hi);

@@ -1,9 +1,11 @@
 """What the multi-head scan's gradients keep of float32: sums that cancel, exponents, and the sums
 over all tokens (dA, dD, ddt_bias), against float64 on the same inputs."""
+import numpy as np
 import pytest
 
+from oracle import head_twin as ht
 from oracle.rounding import U
-from tests.block_helpers import DTYPES
+from tests.block_helpers import DTYPES, check, gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +49,34 @@ def test_steps_of_unlike_size(io, N):
     for t in range(2, 6):
         assert abs(float(ddt[t]) - want) <= tol * abs(want), (t, float(ddt[t]), want)
     assert torch.all(ddt[6:] == 0), ddt
+
+
+@pytest.mark.parametrize("low", [torch.finfo(torch.float32).min, -1e38, -1e9])
+@pytest.mark.parametrize("io,shape", [("f32", (2, 150, 4, 64, 2, 64)), ("bf16", (2, 150, 4, 64, 2, 64)),
+                                      ("bf16", (1, 70, 3, 64, 1, 128)), ("f32", (1, 300, 2, 17, 1, 9)),
+                                      ("bf16", (4, 320, 40, 64, 1, 64))], ids=str)
+def test_heads_that_forget_at_once(io, shape, low):
+    """An A down to the type's lowest value lets no state through: the head's gradients are those of
+    single steps, the other heads' are what they are.  (The reference and its bound with A = -1e5,
+    whose decays of e^-1000 and less are 0 as well.)"""
+    batch, L, H, P, G, N = shape
+    r = np.random.default_rng(L + N)
+    n = r.standard_normal
+    A = -r.uniform(1.0, 8.0, H)
+    A[1] = -1e5
+    v, t = {}, {}
+    for k, a, dt in (("x", n((batch, L, H, P)), io), ("dt", 0.5 * n((batch, L, H)), io), ("A", A, "f32"),
+                     ("B", n((batch, L, G, N)), io), ("C", n((batch, L, G, N)), io),
+                     ("dout", n((batch, L, H, P)), io), ("D", n(H), "f32"),
+                     ("z", n((batch, L, H, P)), io), ("dt_bias", 0.3 * n(H) - 1.0, "f32"),
+                     ("h0", n((batch, H, N, P)), "f32"), ("dh_last", n((batch, H, N, P)), "f32")):
+        t[k], v[k] = gpu(a, dt)
+    t["A"][1] = low
+    got, want = ops().scan2_bwd(**t), ht.scan2_bwd(**v)
+    # (A dl, of that head: its dl is 0, and the reference's exponents stand in the bound of all)
+    quiet = dict(v, A=np.where(np.arange(H) == 1, -8.0, v["A"]))
+    bound = ht.scan2_bwd(**quiet)
+    for k in ("dx", "ddt", "dz", "dB", "dC", "dA", "dD", "ddt_bias", "dh0"):
+        want[k].e = bound[k].e
+        check(got[k], want[k], io if k in ("dx", "ddt", "dz", "dB", "dC") else "f32", k)
+    assert torch.all(got["dh0"][:, 1] == 0) and float(got["dA"][1]) == 0
