@@ -94,6 +94,17 @@ __device__ __forceinline__ float exp_neg(float x) {
   const float hi = x * kLog2e, lo = fmaf(x, kLog2e, -hi) + x * 1.925963e-8f;
   return exp2_hw(hi) * fmaf(lo, kLn2, 1.0f);
 }
+// 2^x, x in float64: what x loses in float32, half a step of up to 1000, is put back.
+__device__ __forceinline__ float exp2_of(double x) {
+  const float hi = static_cast<float>(x);
+  return exp2_hw(hi) * fmaf(static_cast<float>(x - hi), kLn2, 1.0f);
+}
+// 2^{c_t - c_s} of two such sums, c_t the one of the larger size: what the difference of the high
+// parts loses is found exactly and goes with that of the low ones.
+__device__ __forceinline__ float exp2_diff(float t_hi, float t_lo, float s_hi, float s_lo) {
+  const float d = t_hi - s_hi, lost = (t_hi - d) - s_hi;
+  return exp2_hw(d) * fmaf(lost + (t_lo - s_lo), kLn2, 1.0f);
+}
 __device__ __forceinline__ Step step_of(float dt, bool in, float bias, float A, bool softplus) {
   Step s;
   const float raw = dt + bias;
@@ -114,9 +125,9 @@ __device__ __forceinline__ Step step_of(float dt, bool in, float bias, float A, 
   const double end = last_lane(c);
   s.c_hi = static_cast<float>(c);
   s.c_lo = static_cast<float>(c - s.c_hi);
-  s.before = exp2_hw(s.c_hi) * (1.0f + s.c_lo * kLn2);
-  s.after = exp2_hw(static_cast<float>(end - c));
-  s.end = exp2_hw(static_cast<float>(end));
+  s.before = exp2_of(c);
+  s.after = exp2_of(end - c);
+  s.end = exp2_of(end);
   return s;
 }
 

@@ -345,8 +345,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = row0 + r;
-        const float seg =
-            s <= t ? exp2_hw((sm.c_hi[t] - ch) + (sm.c_lo[t] - cl)) : 0.0f;
+        const float seg = s <= t ? exp2_diff(sm.c_hi[t], sm.c_lo[t], ch, cl) : 0.0f;
         const float m = s <= t ? G[i][r] * seg : 0.0f;
         const float k = s <= t ? W[i][r] * seg * dts : 0.0f;
         const float e = s < t ? W[i][r] * dts * m : 0.0f;

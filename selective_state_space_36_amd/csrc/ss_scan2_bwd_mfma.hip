@@ -500,7 +500,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       const bool diag = ti[i] == tj[i];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float seg = exp2_hw((cth - ch[r]) + (ctl - cl[r]));
+        const float seg = exp2_diff(cth, ctl, ch[r], cl[r]);
         const bool in = !diag || s0 + r <= t;
         m[r] = in ? G[i][r] * seg : 0.0f;
         e[r] = in ? W[r] * m[r] : 0.0f;

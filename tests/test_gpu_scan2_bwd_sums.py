@@ -80,3 +80,43 @@ def test_heads_that_forget_at_once(io, shape, low):
         want[k].e = bound[k].e
         check(got[k], want[k], io if k in ("dx", "ddt", "dz", "dB", "dC") else "f32", k)
     assert torch.all(got["dh0"][:, 1] == 0) and float(got["dA"][1]) == 0
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_what_only_exponents_scale(io):
+    """64 steps of one chunk with one product on every way, scaled by 2^{c}, c to -64: the state's
+    adjoint arriving from behind in dh0 (and, in float32, in dx), one step's dout in the dx of all, the
+    state before in dC.  Off are exp2 by one ulp (2 U), the correction by U, and up to five products
+    and conversions by U each: 8 U, however large the exponent (rounded to float32 it would be 44 U)."""
+    o, dt = ops(), DTYPES[io]
+    L, H, P, N = 64, 12, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    z = lambda *s, d=dt: torch.zeros(s, device="cuda", dtype=d)  # noqa: E731
+    step = (0.5 + 0.25 * torch.rand(1, L, H, device="cuda", generator=g)).to(dt)
+    A = -torch.linspace(0.3, 1.2, H, device="cuda")
+    c = torch.cumsum(step.double() * A.double(), 1)[0]                       # (L, H)
+    assert float(c[-1].min()) < -40
+    B, C, x, dout, S = z(1, L, 1, N), z(1, L, 1, N), z(1, L, H, P), z(1, L, H, P), z(1, H, N, P, d=A.dtype)
+    B[..., 0] = C[..., 0] = 1
+    S[:, :, 0] = 1 + torch.rand(1, H, P, device="cuda", generator=g)
+    tol = 8 * U
+
+    def same(got, want, what, tol=tol):
+        assert torch.all((got.double() - want).abs() <= tol * want.abs()), what
+
+    r = o.scan2_bwd(x, step, A, B, C, dout, dt_softplus=False, dh_last=S)
+    same(r["dh0"][0, :, 0], S[0, :, 0].double() * torch.exp(c[-1])[:, None], "dh0")
+    if io == "bf16":
+        return
+    same(r["dx"][0], step[0, :, :, None].double() * torch.exp(c[-1] - c)[:, :, None]
+         * S[0, :, 0].double(), "dx from behind")
+    dout[0, -1] = S[0, :, 0]
+    r = o.scan2_bwd(x, step, A, B, C, dout, dt_softplus=False)
+    same(r["dx"][0], step[0, :, :, None].double() * torch.exp(c[-1] - c)[:, :, None]
+         * S[0, :, 0].double(), "dx from the last step")
+    dout.zero_()
+    dout[..., 0] = 1
+    one = slice(0, 1)       # (dC is a sum over the heads: one of them)
+    r = o.scan2_bwd(x[:, :, one].contiguous(), step[:, :, one].contiguous(), A[one], B, C,
+                    dout[:, :, one].contiguous(), dt_softplus=False, h0=S[:, one].contiguous())
+    same(r["dC"][0, :, 0, 0], torch.exp(c[:, 0]) * S[0, 0, 0, 0].double(), "dC")
