@@ -138,10 +138,10 @@ int64_t scan2_bwd_ws_floats(int64_t batch, int64_t seqlen, int64_t nheads, int64
                             int64_t ngroups, int64_t d_state, Scan2BwdArgs* a, float* ws);
 hipError_t launch_scan2_bwd(const Scan2BwdArgs& a, bool bf16, hipStream_t stream);
 
-// Joins walks that were cut: every slot of `states` and `lam` holds the chunk's own part in float32
-// and takes the state before it, or the adjoint behind it; `pairs`: as bf16 pairs, in the layout of
-// ss_scan2_bwd_mfma.hip.  Writes dh0.
-hipError_t launch_scan2_join(const Scan2BwdArgs& a, bool pairs, hipStream_t stream);
+// Joins walks that were cut: every slot of `states` and `lam` holds the chunk's own part and takes the
+// state before it, or the adjoint behind it; `tiled`: in the layout of ss_scan2_bwd_mfma.hip.
+// Writes dh0.
+hipError_t launch_scan2_join(const Scan2BwdArgs& a, bool tiled, hipStream_t stream);
 
 // Its first two launches with bf16 matrix products (ss_scan2_bwd_mfma.hip): bf16 io, headdim 64,
 // d_state 64 or 128, 16-byte aligned arrays.

@@ -545,7 +545,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
 // Where walks are cut, S' = decay S + part along the chunks: one value of a state per lane and
 // direction, whose slots hold the chunks' own parts and take what lies before (behind) each chunk.
 // Latency bounds it, so eight chunks' parts are in flight (5 us for 13 chunks of 18 heads of 48 x 40).
-template <bool PAIRS>
+template <bool TILED>
 __global__ __launch_bounds__(256) void scan2_join_kernel(Scan2BwdArgs p) {
   const int64_t np = static_cast<int64_t>(p.d_state) * p.headdim, heads = p.batch * p.nheads;
   const int64_t all = heads * np, nc = p.n_chunks;
@@ -556,7 +556,7 @@ __global__ __launch_bounds__(256) void scan2_join_kernel(Scan2BwdArgs p) {
   const int64_t bh = i / np;
   const int e = static_cast<int>(i - bh * np);
   // the value's place in h0, dh_last and dh0: (state, channel)
-  const int64_t at = PAIRS ? bh * np + (e / (16 * p.headdim) * 16 + e % 16) * p.headdim +
+  const int64_t at = TILED ? bh * np + (e / (16 * p.headdim) * 16 + e % 16) * p.headdim +
                                  e / 16 % p.headdim
                            : i;
   const float* init = back ? p.dh_last : p.h0;
@@ -577,13 +577,7 @@ __global__ __launch_bounds__(256) void scan2_join_kernel(Scan2BwdArgs p) {
     for (int j = 0; j < kAhead; ++j)
       if (k + j < nc) {
         const int64_t ch = back ? nc - 1 - (k + j) : k + j;
-        if constexpr (PAIRS) {
-          uint32_t hi, lo;
-          split2(S, 0.0f, hi, lo);
-          slot[ch * np] = __uint_as_float(hi << 16 | (lo & 0xffffu));
-        } else {
-          slot[ch * np] = S;
-        }
+        slot[ch * np] = S;
         S = fmaf(d[j], S, part[j]);
       }
   }
@@ -666,10 +660,10 @@ int64_t round16(int64_t floats) { return (floats + 3) / 4 * 4; }
 
 }  // namespace
 
-hipError_t launch_scan2_join(const Scan2BwdArgs& a, bool pairs, hipStream_t stream) {
+hipError_t launch_scan2_join(const Scan2BwdArgs& a, bool tiled, hipStream_t stream) {
   const int64_t n = 2 * a.batch * a.nheads * a.d_state * a.headdim;
   const dim3 grid(static_cast<unsigned>((n + 255) / 256));
-  if (pairs) hipLaunchKernelGGL(scan2_join_kernel<true>, grid, dim3(256), 0, stream, a);
+  if (tiled) hipLaunchKernelGGL(scan2_join_kernel<true>, grid, dim3(256), 0, stream, a);
   else hipLaunchKernelGGL(scan2_join_kernel<false>, grid, dim3(256), 0, stream, a);
   return hipGetLastError();
 }

@@ -2,24 +2,31 @@
 // states: the formulas and launches of ss_scan2_bwd.hip, with the products on the bf16 matrix
 // instruction.
 //
-// x, B and C are bf16 and enter the products exactly.  The float32 operands (gy, M, the states and
-// their adjoints, w X, e^c gy) are split into bf16 high and low parts, v = hi + lo to about 2^-17,
-// and take a product each; hi lo + lo hi + hi hi where both operands are split.  Products that have
-// K down the rows of a tile read it with the LDS transpose read, so every tile is staged once.
+// x, B and C are bf16 and enter the products exactly.  float32 operands are split into bf16 parts that
+// take a product each.  On the way to the float32 results (dA, ddt_bias, dh0), which are sums over
+// all tokens, they are three, the whole value: w X and e^c gy that make the states, the states where
+// they meet C and B, gy where it meets X.  With two parts, 2^-17, dA and ddt_bias were 2.7e-6 and
+// 3.2e-6 off at 4 x 4096 x 80 heads, dh0 2.4e-6 (plain float32 1e-7 to 3e-7).  What ends in a bf16
+// result alone, whose half step is 2^-8, has two: M and K, the states where they meet gy and X (dC and
+// dB), gy there and where it meets M (dx).  Products that have K down the rows of a tile read it with
+// the LDS transpose read, so every tile is staged once.
 //
-// The states cross from the first launch to the second as such pairs, one 32-bit word per value,
-// laid out as the first one holds them: [d_state / 16][channel][16 states].
+// The states cross from the first launch to the second in float32, laid out as the first one holds
+// them: [d_state / 16][channel][16 states].  The LDS has room for two 16-bit planes of each, so it
+// holds the words' upper and lower halves, and the parts are formed as operands are read.
 //
-// What bounds it, at 4 x 4096 x 80 heads with 128 states: the states kernel 500 us, for 1.31 GB of
-// states written and 0.56 read (3.7 TB/s; 248 us without the stores, 494 without the products, so it
-// is the stores: splitting each walk's states over two workgroups took 570, non-temporal stores the
-// same 505, loads issued before the stores or another order of the chunks in memory 528).  The chunks
-// kernel 620 to 750 us, for 1.98 GB fetched and 0.38 written: 400 us of loads and staging alone, 660
-// of products and staging without the states' loads.  Per head and CU the LDS is busy for a third of
-// the time, the VALU for a third, the matrix units for an eighth, and with one workgroup on a CU (155
-// KB of tiles) and three barriers a head they overlap little: sixteen waves of half the work took the
-// same (825 against 821 us), 32 x 32 tiles gained 3 %, M in one bf16 4 % (not kept: dx and dz would be
-// off by more than their own rounding), a head's parameters fetched with its tiles 6 %.
+// What bounds it, at 4 x 4096 x 80 heads with 128 states: the states kernel 495 us, for 1.31 GB of
+// states written and 0.56 read (3.8 TB/s; with pairs of bf16 248 without the stores, 494 without the
+// products, so it is the stores: splitting each walk's states over two workgroups took 570,
+// non-temporal stores the same 505, loads issued before the stores or another order of the chunks in
+// memory 528).  The chunks kernel 885 us with the gate, for 1.98 GB fetched and 0.38 written, by
+// barriers and latency: one workgroup of eight waves on a CU (160 KB of tiles) and three barriers a
+// head.  Of them the parts that make the values whole and the float64 sums are 210 (675 with pairs
+// and float32 sums, where the VALU was busy for 0.37 of the time, the LDS for 0.27, the matrix units
+// for 0.14; parts formed by dot products, in two thirds of the instructions, took the same).  Measured
+// then: sixteen waves of half the work the same (825 against 821 us), 32 x 32 tiles gained 3 %, M in one
+// bf16 4 % (not kept: dx and dz would be off by more than their own rounding), a head's parameters
+// fetched with its tiles 6 %.
 #include "ss_head.h"
 #include "ss_mfma.h"
 #include "ss_scan2_bwd.h"
@@ -33,16 +40,7 @@ constexpr int kPS = kP + 8;   // bf16 per row of the (step, channel) and (step, 
                               // dwords, so that the four rows of a transpose read and the sixteen
                               // of a 16-byte read start in different banks
 
-// A pair of bf16 in a word, high part above, and back.
-__device__ __forceinline__ void pair4(f32x4 v, uint4& w) {
-  uint32_t h0, h1, l0, l1;
-  split2(v[0], v[1], h0, l0);
-  split2(v[2], v[3], h1, l1);
-  w.x = __builtin_amdgcn_perm(h0, l0, 0x05040100);
-  w.y = __builtin_amdgcn_perm(h0, l0, 0x07060302);
-  w.z = __builtin_amdgcn_perm(h1, l1, 0x05040100);
-  w.w = __builtin_amdgcn_perm(h1, l1, 0x07060302);
-}
+// The upper and lower halves of four words.
 __device__ __forceinline__ uint2 highs(uint4 w) {
   return make_uint2(__builtin_amdgcn_perm(w.y, w.x, 0x07060302),
                     __builtin_amdgcn_perm(w.w, w.z, 0x07060302));
@@ -51,13 +49,38 @@ __device__ __forceinline__ uint2 lows(uint4 w) {
   return make_uint2(__builtin_amdgcn_perm(w.y, w.x, 0x05040100),
                     __builtin_amdgcn_perm(w.w, w.z, 0x05040100));
 }
-// c + a b of two such pairs: the products of like parts, then of unlike ones.
-__device__ __forceinline__ float dot_pairs(uint32_t a, uint32_t b, float c) {
-  using b2 = __bf16 __attribute__((ext_vector_type(2)));
-  const b2 v = __builtin_bit_cast(b2, a);
-  c = __builtin_amdgcn_fdot2_f32_bf16(v, __builtin_bit_cast(b2, b), c, false);
-  return __builtin_amdgcn_fdot2_f32_bf16(
-      v, __builtin_bit_cast(b2, __builtin_amdgcn_alignbit(b, b, 16)), c, false);
+// (a, b) as three bf16 parts, which hold a float32 value whole.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid,
+                                       uint32_t& rest) {
+  hi = pack_bf16(a, b);
+  const float ra = a - lo_f(hi), rb = b - hi_f(hi);
+  split2(ra, rb, mid, rest);
+}
+// From the upper (a bf16 part as they are) and lower halves of eight float32 values: what the upper
+// ones leave as one more part, or as two, which are the rest of the value.
+__device__ __forceinline__ void left2(uint32_t up, uint32_t low, float& a, float& b) {
+  const uint32_t wa = __builtin_amdgcn_perm(up, low, 0x05040100);
+  const uint32_t wb = __builtin_amdgcn_perm(up, low, 0x07060302);
+  a = __uint_as_float(wa) - __uint_as_float(wa & 0xffff0000u);
+  b = __uint_as_float(wb) - __uint_as_float(wb & 0xffff0000u);
+}
+__device__ __forceinline__ Op left(const Op& up, const Op& low) {
+  Op mid;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    left2(up.w[j], low.w[j], a, b);
+    mid.w[j] = pack_bf16(a, b);
+  }
+  return mid;
+}
+__device__ __forceinline__ void left(const Op& up, const Op& low, Op& mid, Op& rest) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    left2(up.w[j], low.w[j], a, b);
+    split2(a, b, mid.w[j], rest.w[j]);
+  }
 }
 
 // ------------------------------------------------------------------ the states
@@ -65,13 +88,14 @@ __device__ __forceinline__ float dot_pairs(uint32_t a, uint32_t b, float c) {
 template <int N>
 struct alignas(16) StateSmem {
   uint16_t in[kQ][N + 16];        // B or C, (step, state)
-  uint16_t hi[kQ][kPS], lo[kQ][kPS];  // weighted x or gy, (step, channel)
+  uint16_t row[3][kQ][kPS];       // weighted x or gy in three parts, (step, channel)
   float weight[2][kQ];
 };
 
-// One workgroup per (batch row, head) and direction; wave w owns channels 16 w .. 16 w + 15.
+// One workgroup per (batch row, head) and direction; wave w owns channels 16 w .. 16 w + 15.  (Three
+// on a CU: left alone the compiler takes registers for two, 542 us for 496 at 4 x 4096 x 80 heads.)
 template <int N, bool CUT>
-__global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) {
+__global__ __launch_bounds__(256, 3) void scan2_states_mfma_kernel(Scan2BwdArgs p) {
   constexpr int NT = N / 16;
   constexpr int UNITS = 2 * N, UPT = (UNITS + 255) / 256;  // (4-step, 8-state) pieces
   __shared__ StateSmem<N> sm;
@@ -159,22 +183,19 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] *= z[j] * sigmoid_f(z[j]);
       }
-      uint2 h2, l2;
-      split2(v[0] * w, v[1] * w, h2.x, l2.x);
-      split2(v[2] * w, v[3] * w, h2.y, l2.y);
-      *reinterpret_cast<uint2*>(&sm.hi[4 * rq + r][4 * rp]) = h2;
-      *reinterpret_cast<uint2*>(&sm.lo[4 * rq + r][4 * rp]) = l2;
+      uint2 part[3];
+      split3(v[0] * w, v[1] * w, part[0].x, part[1].x, part[2].x);
+      split3(v[2] * w, v[3] * w, part[0].y, part[1].y, part[2].y);
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        *reinterpret_cast<uint2*>(&sm.row[q][4 * rq + r][4 * rp]) = part[q];
     }
     // the state before the chunk leaves before the next loads are issued, which would be waited
     // for together with it
     uint4* out = ws + ch * (N * kP / 4) + (16 * wv + l16) * 4 + g4;
     if (!CUT) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint4 w;
-        pair4(S[nt], w);
-        out[nt * kP * 4] = w;
-      }
+      for (int nt = 0; nt < NT; ++nt) out[nt * kP * 4] = __builtin_bit_cast(uint4, S[nt]);
     }
     const float d = decay;
     const bool more = k + 1 < chunks;
@@ -185,19 +206,20 @@ __global__ __launch_bounds__(256) void scan2_states_mfma_kernel(Scan2BwdArgs p) 
     for (int nt = 0; nt < NT; ++nt) S[nt] *= d;
 #pragma unroll
     for (int kb = 0; kb < kQ; kb += 32) {
-      const Op whi = op_down(&sm.hi[0][0], kPS, kb, 16 * wv, l16, g4);
-      const Op wlo = op_down(&sm.lo[0][0], kPS, kb, 16 * wv, l16, g4);
+      Op w[3];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) w[q] = op_down(&sm.row[q][0][0], kPS, kb, 16 * wv, l16, g4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const Op a = op_down(&sm.in[0][0], N + 16, kb, 16 * nt, l16, g4);
-        S[nt] = mfma(a, whi, S[nt]);
-        S[nt] = mfma(a, wlo, S[nt]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) S[nt] = mfma(a, w[q], S[nt]);
       }
     }
     if (more) weigh(next, (k + 1) & 1);
     lds_reads_done();
   }
-  if (CUT) {  // the chunk's own part, in float32
+  if (CUT) {  // the chunk's own part
     uint4* out = ws + only * (N * kP / 4) + (16 * wv + l16) * 4 + g4;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) out[nt * kP * 4] = __builtin_bit_cast(uint4, S[nt]);
@@ -218,18 +240,21 @@ constexpr int kThreads = 512;  // eight waves, one workgroup on a CU
 template <int N>
 struct alignas(16) ChunkSmem {
   uint16_t b[kQ][N + 8], c[kQ][N + 8];           // B and C, (step, state)
-  // S_in and lam_out, (channel, state)
+  // S_in and lam_out, (channel, state): upper and lower halves
   uint16_t shi[kP][N + 8], slo[kP][N + 8];
   uint16_t lhi[kP][N + 8], llo[kP][N + 8];
   uint16_t x[kQ][kPS];                           // (step, channel)
-  uint16_t ghi[kQ][kPS], glo[kQ][kPS];           // gy
+  uint16_t ghi[kQ][kPS], glo[kQ][kPS];           // gy in parts
+  uint16_t grest[kQ][kP];                        // (8-channel pieces at piece ^ (step & 7))
   uint16_t mhi[kQ][kPS], mlo[kQ][kPS];           // M dt_s, (t, s); at the end K
   float dt[kQ], c_hi[kQ], c_lo[kQ], before[kQ], after[kQ];
-  // sums for dl and ddt, by the tile they come from: E / dt over t and over s (strictly below the
-  // diagonal), the diagonal of W M, q, p / dt
-  double ecol[4][kQ], erow[4][kQ];
-  float ediag[kQ], near[2][kQ], far[2][kQ];
+  // sums for dl and ddt: E / dt over t and E over s of each causal tile (strictly below the diagonal),
+  // q, p / dt
+  double ecol[10][16], erow[10][16];
+  float near[2][kQ], far[2][kQ];
   float over[kThreads / 64], gx[kThreads / 64];  // <S_in, lam_out>, gy . x, by wave
+  // the diagonal of W M, in the 16 bytes behind a row of x that keep the banks apart
+  __device__ __forceinline__ float& ediag(int t) { return *reinterpret_cast<float*>(&x[t][kP]); }
 };
 
 // 32 x 32 tiles: the operand's rows (or columns) are 32 of the tile, lane % 32 each, K = k0 + 8
@@ -293,7 +318,6 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
     uint4* m = reinterpret_cast<uint4*>(&sm.mhi[0][0]);
     for (int i = tid; i < 2 * kQ * kPS * 2 / 16; i += kThreads) m[i] = make_uint4(0, 0, 0, 0);
   }
-  for (int i = tid; i < 4 * kQ; i += kThreads) (&sm.ecol[0][0])[i] = (&sm.erow[0][0])[i] = 0.0;
   __syncthreads();
 
   // The causal 16x16 tiles (s-tile ti <= t-tile tj), dealt to the waves in the order (0,0) (0,1)
@@ -365,11 +389,14 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
   auto finish = [&](int64_t h, float A, const Step& st) {
     const float q = sm.near[0][lane] + sm.near[1][lane];
     const float f = sm.far[0][lane] + sm.far[1][lane];
-    const double col =
-        (sm.ecol[0][lane] + sm.ecol[1][lane]) + (sm.ecol[2][lane] + sm.ecol[3][lane]);
-    const double row =
-        (sm.erow[0][lane] + sm.erow[1][lane]) + (sm.erow[2][lane] + sm.erow[3][lane]);
-    const float xv = f + (static_cast<float>(col) + sm.ediag[lane]);
+    // the step's tiles: those of its row (as t), those of its column (as s)
+    double col = 0.0, row = 0.0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k <= g4) row += sm.erow[g4 * (g4 + 1) / 2 + k][l16];
+      if (k >= g4) col += sm.ecol[k * (k + 1) / 2 + g4][l16];
+    }
+    const float xv = f + (static_cast<float>(col) + sm.ediag(lane));
     float ov = 0.0f, gx = 0.0f;
 #pragma unroll
     for (int k = 0; k < kThreads / 64; ++k) {
@@ -428,15 +455,14 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
       *reinterpret_cast<uint2*>(&sm.slo[ch16][n]) = lows(sr[k]);
       *reinterpret_cast<uint2*>(&sm.lhi[ch16][n]) = highs(lr[k]);
       *reinterpret_cast<uint2*>(&sm.llo[ch16][n]) = lows(lr[k]);
-      const uint32_t a[4] = {sr[k].x, sr[k].y, sr[k].z, sr[k].w};
-      const uint32_t c[4] = {lr[k].x, lr[k].y, lr[k].z, lr[k].w};
+      const f32x4 a = __builtin_bit_cast(f32x4, sr[k]), c = __builtin_bit_cast(f32x4, lr[k]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) over = dot_pairs(a[j], c[j], over);
+      for (int j = 0; j < 4; ++j) over = fmaf(a[j], c[j], over);
     }
     *reinterpret_cast<uint4*>(&sm.x[r8][c8]) = xr;
     {
       const uint32_t gw[4] = {gr.x, gr.y, gr.z, gr.w}, zw[4] = {zr.x, zr.y, zr.z, zr.w};
-      uint32_t hi[4], lo[4];
+      uint32_t hi[4], lo[4], rest[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float a = lo_f(gw[j]), c = hi_f(gw[j]);
@@ -447,10 +473,13 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
         }
         const uint32_t xw = j == 0 ? xr.x : j == 1 ? xr.y : j == 2 ? xr.z : xr.w;
         gx = fmaf(a, lo_f(xw), fmaf(c, hi_f(xw), gx));
-        split2(a, c, hi[j], lo[j]);
+        split3(a, c, hi[j], lo[j], rest[j]);
       }
       *reinterpret_cast<uint4*>(&sm.ghi[r8][c8]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       *reinterpret_cast<uint4*>(&sm.glo[r8][c8]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      if (GATE)
+        *reinterpret_cast<uint4*>(&sm.grest[r8][c8 ^ (r8 & 7) * 8]) =
+            make_uint4(rest[0], rest[1], rest[2], rest[3]);
     }
     __syncthreads();  // the tiles are there
     // z and dout again for the epilogue, in its layout (they lie in the caches); then the next head
@@ -487,6 +516,11 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
         const Op a = op_along(&sm.x[0][0], kPS, 16 * ti[i], kb, l16, g4);
         W = mfma(a, op_along(&sm.ghi[0][0], kPS, 16 * tj[i], kb, l16, g4), W);
         W = mfma(a, op_along(&sm.glo[0][0], kPS, 16 * tj[i], kb, l16, g4), W);
+        if (GATE) {
+          const uint4 r = *reinterpret_cast<const uint4*>(
+              &sm.grest[16 * tj[i] + l16][(kb + 8 * g4) ^ (l16 & 7) * 8]);
+          W = mfma(a, Op{{r.x, r.y, r.z, r.w}}, W);
+        }
       }
       const int t = 16 * tj[i] + l16, s0 = 16 * ti[i] + 4 * g4;
       const float cth = sm.c_hi[t], ctl = sm.c_lo[t];
@@ -521,7 +555,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
           e[r] = on ? 0.0f : e[r];
         }
         ed = sum_rows(ed);
-        if (g4 == 0) sm.ediag[t] = ed;
+        if (g4 == 0) sm.ediag(t) = ed;
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -529,10 +563,10 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
         col[r] = sum16(static_cast<double>(e[r]));
       }
       row = sum_rows(row);
-      if (g4 == 0) sm.erow[ti[i]][t] = row;
+      if (g4 == 0) sm.erow[wv + 8 * i][l16] = row;
       if (l16 == 0) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) sm.ecol[tj[i]][s0 + r] = col[r];
+        for (int r = 0; r < 4; ++r) sm.ecol[wv + 8 * i][4 * g4 + r] = col[r];
       }
     }
 
@@ -542,8 +576,12 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
 #pragma unroll 2
     for (int kb = 0; kb < N; kb += 16) {
       const Op to = along32(bc_t, N + 8, 32 * sh, kb, lane);
-      Y = mfma32(along32(hi_t, N + 8, 32 * ph, kb, lane), to, Y);
-      Y = mfma32(along32(lo_t, N + 8, 32 * ph, kb, lane), to, Y);
+      const Op up = along32(hi_t, N + 8, 32 * ph, kb, lane);
+      Op mid, rest;
+      left(up, along32(lo_t, N + 8, 32 * ph, kb, lane), mid, rest);
+      Y = mfma32(up, to, Y);
+      Y = mfma32(mid, to, Y);
+      Y = mfma32(rest, to, Y);
     }
     // ---- S_in gy^T or lam_out X^T, scaled by their steps into dC or dB
     {
@@ -552,7 +590,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
 #pragma unroll 2
       for (int kb = 0; kb < kP; kb += 16) {
         const Op ah = down32(hi_t, N + 8, kb, 32 * nt, lane);
-        const Op al = down32(lo_t, N + 8, kb, 32 * nt, lane);
+        const Op al = left(ah, down32(lo_t, N + 8, kb, 32 * nt, lane));
 #pragma unroll
         for (int j = 0; j < TPW; ++j) {
           const Op to = along32(by_t, kPS, 32 * (j0 + j), kb, lane);
@@ -588,6 +626,11 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_mfma_kernel(Scan2BwdArg
         const uint2 gl = *reinterpret_cast<const uint2*>(&sm.glo[t][c0 + 8 * q]);
         v[0] = lo_f(gh.x) + lo_f(gl.x), v[1] = hi_f(gh.x) + hi_f(gl.x);
         v[2] = lo_f(gh.y) + lo_f(gl.y), v[3] = hi_f(gh.y) + hi_f(gl.y);
+        if (GATE) {
+          const uint2 gr = *reinterpret_cast<const uint2*>(
+              &sm.grest[t][(c0 + 8 * q) ^ (t & 7) * 8]);
+          v[0] += lo_f(gr.x), v[1] += hi_f(gr.x), v[2] += lo_f(gr.y), v[3] += hi_f(gr.y);
+        }
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {

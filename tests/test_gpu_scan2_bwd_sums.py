@@ -120,3 +120,67 @@ def test_what_only_exponents_scale(io):
     r = o.scan2_bwd(x[:, :, one].contiguous(), step[:, :, one].contiguous(), A[one], B, C,
                     dout[:, :, one].contiguous(), dt_softplus=False, h0=S[:, one].contiguous())
     same(r["dC"][0, :, 0, 0], torch.exp(c[:, 0]) * S[0, 0, 0, 0].double(), "dC")
+
+
+def _sums(t):
+    """In float64: dh0, and of dA and ddt_bias the values and the root of the sum of their terms'
+    squares (a term per step)."""
+    d = {k: v.double() for k, v in t.items()}
+    x, A, B, C, dout, h0 = (d[k] for k in ("x", "A", "B", "C", "dout", "h0"))
+    batch, L, H, P = x.shape
+    raw = d["dt"] + d["dt_bias"]
+    s = torch.clamp(raw, min=0) + torch.log1p(torch.exp(-raw.abs()))
+    a = torch.exp(s * A)
+    gy = dout * d["z"] * torch.sigmoid(d["z"]) if "z" in d else dout
+    per = lambda v: v.repeat_interleave(H // B.shape[2], 1)  # noqa: E731
+    S = torch.empty(L + 1, *h0.shape, device="cuda", dtype=torch.float64)
+    S[0] = h0
+    for k in range(L):
+        S[k + 1] = a[:, k, :, None, None] * S[k] + \
+            (s[:, k, :, None] * per(B[:, k]))[..., None] * x[:, k, :, None]
+    lam, dl, xv = d["dh_last"], torch.empty_like(s), torch.empty_like(s)
+    for k in range(L - 1, -1, -1):
+        lam = lam + per(C[:, k])[..., None] * gy[:, k, :, None]
+        xv[:, k] = ((per(B[:, k])[..., None] * lam).sum(2) * x[:, k]).sum(2)
+        dl[:, k] = a[:, k] * (lam * S[k]).sum((2, 3))
+        lam = a[:, k, :, None, None] * lam
+    terms = dict(dA=s * dl, ddt_bias=(A * dl + xv) * torch.sigmoid(raw))
+    return lam, {k: (v.sum((0, 1)), v.square().sum((0, 1)).sqrt()) for k, v in terms.items()}
+
+
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("shape", [(16, 1000, 5, 64, 1, 128), (16, 1000, 5, 64, 1, 64),
+                                   (8, 1000, 6, 64, 2, 128), (2, 300, 8, 64, 1, 128),
+                                   (4, 1000, 24, 32, 1, 16)], ids=str)
+def test_many_heads_a_workgroup(shape, gate):
+    """bf16.  In all but the fourth shape (few walks, cut) the chunks number the card's CUs, so that one
+    workgroup walks several heads of a group, or all of them: 5, 5, 3, and at the end 24 in the kernel
+    for any shape.  The last batch row's gradients against the bounds of float32 products; what is
+    float32 by more: a term of it is a product of about ten factors, each off by one rounding or by the
+    two U of a hardware function, and the terms' errors differ, so that dh0 is within 16 U of its
+    norm and the sums over all tokens within 16 U of the root of their squares (with operands of
+    bf16 pairs, 2^-18 each, they were 40 U off)."""
+    o = ops()
+    batch, L, H, P, G, N = shape
+    g = torch.Generator(device="cuda").manual_seed(N + L + H)
+    n = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    b = lambda *s: n(*s).bfloat16()  # noqa: E731
+    t = dict(x=b(batch, L, H, P), dt=(0.5 * n(batch, L, H)).bfloat16(),
+             A=-1 - 7 * torch.rand(H, device="cuda", generator=g), B=b(batch, L, G, N),
+             C=b(batch, L, G, N), dout=b(batch, L, H, P), D=n(H), dt_bias=0.3 * n(H) - 3,
+             h0=n(batch, H, N, P), dh_last=n(batch, H, N, P))
+    if gate:
+        t["z"] = b(batch, L, H, P)
+    got = o.scan2_bwd(**t)
+    dh0, sums = _sums(t)
+    assert float((got["dh0"] - dh0).norm() / dh0.norm()) <= 16 * U
+    for k, (want, size) in sums.items():
+        assert float((got[k] - want).norm() / size.norm()) <= 16 * U, k
+    last = {k: (v[-1:] if v.dim() > 1 else v).double().cpu().numpy() for k, v in t.items()}
+    want = ht.scan2_bwd(**last)
+    for k in ("dx", "ddt", "dz", "dB", "dC"):
+        if want[k] is not None:
+            check(got[k][-1:], want[k], "bf16", k)
+    again = o.scan2_bwd(**t)
+    for k, v in got.items():
+        assert v is None or torch.equal(v, again[k]), k
