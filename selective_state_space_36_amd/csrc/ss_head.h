@@ -101,6 +101,7 @@ hipError_t launch_scan2_step(const Scan2StepArgs& a, bool bf16, hipStream_t stre
 
 // Gradients of the multi-head scan.
 constexpr int kScan2BwdChunk = 64;
+constexpr int64_t kScan2BwdMaxWalks = 0xffffffffll / 512;  // (a launch counts threads in 32 bits)
 struct Scan2BwdArgs {
   const void* x;
   const void* dt;

@@ -674,9 +674,11 @@ hipError_t launch_scan2_join(const Scan2BwdArgs& a, bool tiled, hipStream_t stre
 // 48 x 512 66 -> 66, 64 x 4096 331 -> 354, 24 x 256 44 -> 44, 24 x 128 36 -> 39; float32: 3 x 777,
 // 6 heads of 48 x 40, 76 -> 48, 1 x 16384, 24 heads of 64 x 128, 1972 -> 1242, 1 x 4096, 64 heads,
 // 831 -> 858.
+// Walks of more chunks than a launch has workgroups for stay whole.
 constexpr int64_t kCutWalks = 96, kCutChunks = 4;
 bool scan2_bwd_cut(int64_t heads, int64_t n_pblk, int64_t nc) {
-  return 2 * heads * n_pblk <= kCutWalks && nc >= kCutChunks;
+  const int64_t walks = 2 * heads * n_pblk;
+  return walks <= kCutWalks && nc >= kCutChunks && walks * nc <= kScan2BwdMaxWalks;
 }
 
 // Runs of heads: a workgroup for each of the 256 CUs (one fits a CU), at most a head each.
