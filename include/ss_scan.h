@@ -555,8 +555,8 @@ ss_status ss_causal_conv_update(void* conv_state, const void* x, const float* we
  *                       before and the adjoints behind every 64 steps.  Its contents need no
  *                       preparation and mean nothing after the call; calls that may run at the
  *                       same time need one each.
- * d_state outside 1..256, headdim or nheads above 2^24 or seqlen above 2^31 - 1 ->
- * SS_ERR_UNSUPPORTED.  Outputs must not overlap inputs, each other or the workspace.
+ * nheads == 0 is a no-op (dB and dC are not written).  d_state outside 1..256, headdim or nheads
+ * above 2^24 or seqlen above 2^31 - 1 -> SS_ERR_UNSUPPORTED.  Outputs must not overlap inputs, each other or the workspace.
  * The products are formed for 64 steps at a time, pairs in the wrong order times 0: an infinity or
  * a NaN at a step reaches the gradients of other steps of its 64, also ones that do not depend on
  * it (as in ss_scan2_fwd's matrix form).
@@ -597,6 +597,7 @@ ss_status ss_scan2_state_update(float* state, const void* x, const void* dt, con
  *                elements apart (z_stride means nothing without z).
  *   workspace  : ss_scan2_state_update_conv_workspace_bytes() bytes, 16-byte aligned; one per
  *                call that may run at the same time.
+ * batch, nheads or headdim == 0 is a no-op (the window is not shifted either).
  * state, conv_state and out must not overlap the inputs, each other or the workspace.
  */
 ss_status ss_scan2_state_update_conv(float* state, void* conv_state, const void* xbc,

@@ -911,6 +911,9 @@ def scan2_bwd(x, dt, A, B, C, dout, D=None, z=None, dt_bias=None, dt_softplus=Tr
              dB=like(B), dC=like(C), dD=like(A) if want_dD else None,
              ddt_bias=like(A) if want_ddt_bias else None,
              dh0=A.new_empty((batch, H, N, P)) if want_dh0 else None)
+    if not H:  # the library writes nothing then
+        g["dB"].zero_()
+        g["dC"].zero_()
     l = lib()
     nbytes = l.ss_scan2_bwd_workspace_bytes(batch, L, H, P, G, N, code)
     ws, ws_len, keep = _scratch(workspace, nbytes, dev)
@@ -957,8 +960,8 @@ def scan2_state_update_conv(state, conv_state, xbc, conv_weight, conv_bias, dt, 
     advanced in place.  xbc: (batch, width) with width = nheads headdim + 2 ngroups d_state, the
     columns [x | B | C] before the convolution; conv_weight: (width, k) float32, k in 1..4;
     conv_bias: (width,) float32 or None; dt: (batch, nheads); z: (batch, nheads headdim) or None.
-    The rows of xbc, dt and z may be parts of one projection's.  Returns out (batch, nheads,
-    headdim)."""
+    The rows of xbc, dt and z may be parts of one projection's.  Without heads or channels
+    nothing is advanced.  Returns out (batch, nheads, headdim)."""
     if _elsewhere(xbc, stream):
         return _moved(scan2_state_update_conv, xbc, stream,
                       (state, conv_state, xbc, conv_weight, conv_bias, dt, A),

@@ -184,3 +184,14 @@ def test_many_heads_a_workgroup(shape, gate):
     again = o.scan2_bwd(**t)
     for k, v in got.items():
         assert v is None or torch.equal(v, again[k]), k
+
+
+def test_no_heads(monkeypatch):
+    """Without heads nothing reaches B and C: their gradients are 0, not what the memory held."""
+    o = ops()
+    z = lambda *s: torch.zeros(s, device="cuda")  # noqa: E731
+    like = torch.empty_like
+    monkeypatch.setattr(torch, "empty_like", lambda t, **kw: like(t, **kw).fill_(7))
+    g = o.scan2_bwd(z(2, 5, 0, 8), z(2, 5, 0), z(0), z(2, 5, 1, 8), z(2, 5, 1, 8), z(2, 5, 0, 8))
+    assert torch.all(g["dB"] == 0) and torch.all(g["dC"] == 0)
+    assert g["dB"].shape == (2, 5, 1, 8) and g["dx"].numel() == 0 and g["dA"].numel() == 0
