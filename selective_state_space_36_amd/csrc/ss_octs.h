@@ -61,14 +61,14 @@ __device__ __forceinline__ Oct<IO> load_oct(const typename IO::elem* p, int n) {
   }
   return o;
 }
-template <class IO, bool PAST = false>
+template <class IO>
 __device__ __forceinline__ void load8(const typename IO::elem* p, int n, float (&v)[8]) {
-  const Oct<IO> o = load_oct<IO, PAST>(p, n);
+  const Oct<IO> o = load_oct<IO>(p, n);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = o[j];
 }
 
-template <class IO, bool PAST = false>
+template <class IO>
 __device__ __forceinline__ void store8(typename IO::elem* p, int n, const float (&v)[8]) {
   using E = typename IO::elem;
   using raw = typename OctBytes<E>::raw;
@@ -82,8 +82,7 @@ __device__ __forceinline__ void store8(typename IO::elem* p, int n, const float 
       for (int j = 0; j < 4; ++j)
         a[j] = __builtin_bit_cast(uint32_t,
                                   __builtin_convertvector((f2{v[2 * j], v[2 * j + 1]}), b2));
-      if constexpr (PAST) __builtin_nontemporal_store(a, q);
-      else *q = a;
+      *q = a;
     } else {
       raw a, b;
 #pragma unroll
@@ -91,13 +90,8 @@ __device__ __forceinline__ void store8(typename IO::elem* p, int n, const float 
         a[j] = __float_as_uint(v[j]);
         b[j] = __float_as_uint(v[4 + j]);
       }
-      if constexpr (PAST) {
-        __builtin_nontemporal_store(a, q);
-        __builtin_nontemporal_store(b, q + 1);
-      } else {
-        q[0] = a;
-        q[1] = b;
-      }
+      q[0] = a;
+      q[1] = b;
     }
   } else {
 #pragma unroll

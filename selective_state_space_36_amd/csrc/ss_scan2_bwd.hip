@@ -96,7 +96,7 @@ __device__ __forceinline__ Step steps(const Scan2BwdArgs& p, int64_t b, int64_t 
 
 // A thread's eight values of a 64 x 64 tile: row tid / 8, columns 8 (tid % 8).. of the `rows` x
 // `cols` that are there (the rest 0).
-template <class IO, int THREADS>
+template <class IO>
 __device__ __forceinline__ void tile8(const typename IO::elem* base, int64_t pitch, int rows,
                                       int cols, int r, int c, float (&v)[8]) {
   load8<IO>(base + r * pitch + c, r < rows ? cols - c : 0, v);
@@ -275,9 +275,9 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
 
   auto stage_bc = [&](int nb) {
     float v[8];
-    tile8<IO, kThreads>(Bg + nb * kQ, gn, rows, N - nb * kQ, r8, c8, v);
+    tile8<IO>(Bg + nb * kQ, gn, rows, N - nb * kQ, r8, c8, v);
     put8(sm.b, r8, c8, v);
-    tile8<IO, kThreads>(Cg + nb * kQ, gn, rows, N - nb * kQ, r8, c8, v);
+    tile8<IO>(Cg + nb * kQ, gn, rows, N - nb * kQ, r8, c8, v);
     put8(sm.c, r8, c8, v);
   };
 
@@ -312,11 +312,11 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
     // x and gy of a block of channels
     auto stage_rows = [&](int p0) {
       float v[8], z[8];
-      tile8<IO, kThreads>(static_cast<const E*>(p.x) + at + p0, hp, rows, P - p0, r8, c8, v);
+      tile8<IO>(static_cast<const E*>(p.x) + at + p0, hp, rows, P - p0, r8, c8, v);
       put8(sm.x, r8, c8, v);
-      tile8<IO, kThreads>(static_cast<const E*>(p.dout) + at + p0, hp, rows, P - p0, r8, c8, v);
+      tile8<IO>(static_cast<const E*>(p.dout) + at + p0, hp, rows, P - p0, r8, c8, v);
       if (p.z) {
-        tile8<IO, kThreads>(static_cast<const E*>(p.z) + at + p0, hp, rows, P - p0, r8, c8, z);
+        tile8<IO>(static_cast<const E*>(p.z) + at + p0, hp, rows, P - p0, r8, c8, z);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= silu_f(z[j]);
       }
@@ -449,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void scan2_chunks_kernel(Scan2BwdArgs p) 
               const float z = IO::widen(static_cast<const E*>(p.z)[o]);
               const float go = IO::widen(static_cast<const E*>(p.dout)[o]);
               const float sg = sigmoid_f(z);
-                  static_cast<E*>(p.dz)[o] = IO::from_float(
+              static_cast<E*>(p.dz)[o] = IO::from_float(
                   go * fmaf(Dh, x, Y[i][r]) * (sg * fmaf(z, 1.0f - sg, 1.0f)));
             }
           }
