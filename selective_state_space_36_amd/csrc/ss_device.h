@@ -92,6 +92,11 @@ __device__ __forceinline__ float hold_gain_da(float e, float y, float dt, float 
   return fabsf(y) < 0.125f ? (dt * dt) * q : fmaf(dt, e, -fmaf(e, ia, -ia)) * ia;
 }
 
+// sigmoid as 1 / (1 + 2^(-z log2 e)): 0 at -infinity, 1 at +infinity.
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
+}
+
 // silu(z) = z * sigmoid(z) = z / (1 + e^{-z}).
 __device__ __forceinline__ float silu_f(float z) {
   return z * rcp_hw(1.0f + exp2_hw(-z * kLog2e));

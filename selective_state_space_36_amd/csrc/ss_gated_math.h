@@ -7,9 +7,6 @@ namespace ss {
 
 __device__ __forceinline__ float sqrt_hw(float x) { return __builtin_amdgcn_sqrtf(x); }
 __device__ __forceinline__ float rsq_hw(float x) { return __builtin_amdgcn_rsqf(x); }
-__device__ __forceinline__ float sigmoid_f(float v) {
-  return rcp_hw(1.0f + exp2_hw(-v * kLog2e));
-}
 // sigmoid(v + bias) for nb = -bias log2(e): one fused multiply-add instead of two operations.
 __device__ __forceinline__ float sigmoid_biased(float v, float nb) {
   return rcp_hw(1.0f + exp2_hw(fmaf(v, -kLog2e, nb)));

@@ -48,7 +48,8 @@ ss_status head_sizes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t head
   int64_t n, m;
   if (!mul_ok(batch, nheads, &z->heads) || !mul_ok(z->heads, seqlen, &z->dts) ||
       !mul_ok(z->dts, headdim, &z->elems) || !mul_ok(batch, ngroups, &z->bcs) ||
-      !mul_ok(z->bcs, seqlen, &z->bcs) || !mul_ok(z->bcs, d_state, &z->bcs) || !mul_ok(z->heads, d_state * headdim, &z->states) ||
+      !mul_ok(z->bcs, seqlen, &z->bcs) || !mul_ok(z->bcs, d_state, &z->bcs) ||
+      !mul_ok(z->heads, d_state * headdim, &z->states) ||
       !mul_ok(z->states, z->chunks + 1, &n) || !mul_ok(n, 64, &m) || !mul_ok(z->elems, 64, &m) ||
       !mul_ok(z->bcs, 64, &n) || !mul_ok(n, nheads > 0 ? nheads : 1, &m))
     return fail(SS_ERR_INVALID_ARG, "sizes overflow 64-bit byte offsets");
@@ -352,7 +353,7 @@ static ss_status check_groups(int64_t rows, int64_t dim, int64_t groups) {
     return fail(SS_ERR_INVALID_ARG, "dim=%lld is not a multiple of groups=%lld",
                 static_cast<long long>(dim), static_cast<long long>(groups));
   // rows * groups, and the workgroups of the backward, whose number is a multiple of the groups
-  if (rows * groups > kMaxGrid || groups > (int64_t(1) << 20))
+  if (groups > (int64_t(1) << 20) || rows * groups > kMaxGrid)
     return fail(SS_ERR_INVALID_ARG, "too many groups");
   return SS_OK;
 }

@@ -21,11 +21,6 @@
 namespace ss {
 namespace {
 
-// sigmoid as 1 / (1 + 2^(-z log2 e)): 0 at -infinity, 1 at +infinity.
-__device__ __forceinline__ float sigmoid_f(float z) {
-  return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
-}
-
 __device__ __forceinline__ float inv_root(float sumsq, float n, float eps) {
   return 1.0f / __builtin_sqrtf(sumsq / n + eps);
 }

@@ -6,10 +6,6 @@
 
 namespace ss {
 
-__device__ __forceinline__ float sigmoid_f(float z) {
-  return rcp_hw(1.0f + exp2_hw(-z * kLog2e));
-}
-
 // Sum over the four 16-lane rows of a wave, in each of them: an exchange of odd and even rows, then
 // of halves (both operands the same value: one result holds the first of each pair twice, the other
 // the second).
