@@ -556,7 +556,11 @@ ss_status ss_causal_conv_update(void* conv_state, const void* x, const float* we
  *                       preparation and mean nothing after the call; calls that may run at the
  *                       same time need one each.
  * nheads == 0 is a no-op (dB and dC are not written).  d_state outside 1..256, headdim or nheads
- * above 2^24 or seqlen above 2^31 - 1 -> SS_ERR_UNSUPPORTED.  Outputs must not overlap inputs, each other or the workspace.
+ * above 2^24 or seqlen above 2^31 - 1 -> SS_ERR_UNSUPPORTED.  Outputs must not overlap inputs, each
+ * other or the workspace.
+ * dA, dD, ddt_bias and dh0 are what float32 products and sums give, for either io dtype.  With bf16
+ * io, headdim 64 and 64 or 128 states the products run on bf16 parts: three of a float32 operand (all
+ * of it) towards those, two (2^-17 of it) towards gradients that are rounded to bf16.
  * The products are formed for 64 steps at a time, pairs in the wrong order times 0: an infinity or
  * a NaN at a step reaches the gradients of other steps of its 64, also ones that do not depend on
  * it (as in ss_scan2_fwd's matrix form).

@@ -59,8 +59,8 @@ __device__ __forceinline__ uint32_t keep8(const PhiloxKey& k, uint32_t col8, uin
   return keep;
 }
 
-// v times `up` where it is kept, else 0 (chosen, not multiplied: an infinity or a NaN that is dropped
-// is gone).
+// v times `up` where it is kept, else 0 (chosen, not multiplied: an infinity or a NaN that is
+// dropped is gone).
 __device__ __forceinline__ void drop8(float (&v)[8], uint32_t keep, float up) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = keep >> j & 1 ? v[j] * up : 0.0f;

@@ -2,17 +2,24 @@
 // residual stream, and the gated RMS norm in groups, with their gradients.
 //
 // A unit (a row, or one group of a row's columns) lies in the registers of 8 to 1024 lanes, K octs
-// of columns each, so every array is read once.  Units wider than 16384 columns are read again for
-// each pass by the wide kernels.  Parameter gradients are added in registers while a workgroup
-// walks its units, written as one line per workgroup (or unit place) and summed by
-// column_sums_kernel in a fixed order.
+// of columns each, so every array is read once: units of up to 16384 columns in the forward, of up
+// to 8192 in the backward.  Wider ones are read again for each pass by the wide kernels, whose
+// backward also reads and writes its line of sums for every unit.  Parameter gradients are otherwise
+// added in registers while a workgroup walks its units, written as one line per workgroup (or unit
+// place) and summed by column_sums_kernel in a fixed order.
 //
 // What bounds it: memory.  16384 x 2560 bf16 with residual, scale and dropout: forward 504 MB in
 // 106 us (4.8 TB/s; a copy of 1 GiB reaches 5.2), backward 756 MB in 140 us (5.4, some of it from the
 // 256 MB cache) and 5 us for the sums; the generator's 14 slots an element hide behind the loads.
-// Gated, 16384 x 5120 bf16, z part of longer rows: forward 504 MB in 140 us, backward 840 MB in 140
-// to 170.  One row: 2.8 us, a launch.  Non-temporal loads are kept to the backward: in the forward
+// Gated, 16384 x 5120 bf16, z part of longer rows: backward 840 MB in 138 us behind its forward (some
+// of it from the cache; 175 alone), forward 504 MB in 138 (128 alone), 3.6 TB/s and so not memory's
+// rate: a workgroup loads its one row, meets at a barrier, stores and ends, with nothing on its way
+// meanwhile.  One row: 2.8 us, a launch.  Non-temporal loads are kept to the backward: in the forward
 // they gain 11 us and cost the backward, which finds less in the cache, 20.
+//
+// RMS backward alone with everything asked for, 16384 rows bf16, TB/s: 512 columns 4.6, 768 3.1, 1024
+// 4.6, 2560 5.3, 4096 5.4; 5120 4.3 and 8192 4.7 with 1024 lanes' spills; 8192 rows of 12288 or 16384
+// 3.2 and 3.1 (wide).  The forward is at 4.8 to 5.7 throughout.
 #include "ss_head.h"
 #include "ss_octs.h"
 #include "ss_philox.h"
@@ -163,10 +170,10 @@ __device__ __forceinline__ void write_lines(float (&acc)[N][8], const UnitLayout
                 acc[q]);
 }
 
-// One oct per lane: a place's sums, its row and the next one take about 140 registers.  (The next row
-// asked for ahead: 210 -> 140 us at 16384 x 2560 bf16, where its rows are not spilled: MOST 512, for
-// up to 4096 columns; with 1024 lanes the compiler has 128 registers and spills 8 to 24.)  Rows of
-// over 8192 columns go to the wide kernels.
+// One oct per lane: a place's sums, its row and the next one take about 140 registers.  (The next
+// row asked for ahead: 210 -> 140 us at 16384 x 2560 bf16, where its rows are not spilled: MOST 512,
+// for up to 4096 columns; with 1024 lanes the compiler has 128 registers and spills 1 to 24, 16 for
+// bf16 with a float32 sum and dropout.)  Rows of over 8192 columns go to the wide kernels.
 template <class IO, class S, bool DROP, bool PAST, int MOST>
 __global__ __launch_bounds__(MOST) void rms_bwd_kernel(RmsArgs p, UnitLayout l, float* part) {
   using E = typename IO::elem;
@@ -655,8 +662,9 @@ struct Shape {
 constexpr int64_t kFwdBlocks = 1 << 20;
 // Workgroups, and so lines of sums, of the backward.  Few rows: one each as long as the lines are
 // few (1001 x 1027 f32, 1001 workgroups 12.3 + 5.2 us for the sums, 256 of four rows 18.1 + 3.9).
-// Many: about as many workgroups as run at once (16384 x 2560 bf16, 512 workgroups 140 + 4.7 us,
-// 1024 144 + 5.2, 3276 196 + 14).
+// Many: about as many workgroups as run at once at 2560 columns, five waves each (16384 x 2560 bf16,
+// 512 workgroups 140 + 4.7 us, 1024 144 + 5.2, 3276 196 + 14).  Rows of 520 to 1024 columns are two
+// waves, of which 512 leave two thirds of the places empty; the number was not tried there.
 constexpr int64_t kFewRowsBlocks = 1024, kManyRowsBlocks = 512;
 
 int64_t gcd(int64_t a, int64_t b) { return b ? gcd(b, a % b) : a; }

@@ -1,5 +1,5 @@
-// ss_scan2_bwd.h -- step sizes, decays and sums over a wave that the kernels of the multi-head scan's
-// gradients share.
+// ss_scan2_bwd.h -- step sizes, decays and sums over a wave that the kernels of the multi-head
+// scan's gradients share.
 #pragma once
 
 #include "ss_device.h"
@@ -112,9 +112,9 @@ __device__ __forceinline__ Step step_of(float dt, bool in, float bias, float A, 
     s.slope = raw >= 0.0f ? r : e * r;
   }
   s.dt = in ? s.dt : 0.0f;
-  // A step's decay below 2^-10^6 is 0 with all its products.  Held there (and at 2^10^6), sums of 64 of
-  // them stay in float32's range, and so do their differences: an A of the type's lowest value, which
-  // lets no state through, would give infinity less infinity.
+  // A step's decay below 2^-10^6 is 0 with all its products.  Held there (and at 2^10^6), sums of 64
+  // of them stay in float32's range, and so do their differences: an A of the type's lowest value,
+  // which lets no state through, would give infinity less infinity.
   double log2a = static_cast<double>(s.dt) * A * 1.4426950408889634;
   log2a = log2a < -1e6 ? -1e6 : log2a > 1e6 ? 1e6 : log2a;
   const double c = scan64(log2a);

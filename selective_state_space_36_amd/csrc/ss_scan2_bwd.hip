@@ -28,10 +28,14 @@
 // and ddt_bias, in a fixed order.
 //
 // All products run as v_mfma_f32_16x16x4_f32 here: operands of every type and size, exact in
-// float32.  Sizes that are not multiples of the tiles are filled with zeros.  What bounds it: the
-// float32 products (at 4 x 4096 x 80 heads the chunks took 2308 us, the states 1223; the bf16 kernels
-// of ss_scan2_bwd_mfma.hip take such calls) and, for few heads, latency: 3 x 777, 6 heads of 48 x 40
-// float32, 36 walks of 13 chunks, states 10 us and their join 5 (37 walked whole), chunks 27.
+// float32.  Sizes that are not multiples of the tiles are filled with zeros.  What bounds it: at
+// 4 x 4096, 80 heads of 64 x 128 float32 the chunks take 2340 us and the states 1080, three times
+// what the chunks' products, 1.1e11 operations, take at the rate of a large float32 product (147
+// TFLOP/s).  dC and dB of every block of 64 states stay in registers through the heads, and the
+// chunks kernel spills: 19, 41, 57 and 77 of its 256 for one to four blocks, stored and reloaded in
+// every head, with one workgroup on a CU (125 KB of tiles) and its barriers beside them.  4 x 2048, 40
+// heads of 64 x 256 bf16: chunks 995, states 660.  For few heads it is latency: 3 x 777, 6 heads of 48
+// x 40 float32, 36 walks of 13 chunks, states 10 us and their join 5 (37 walked whole), chunks 27.
 #include "ss_head.h"
 #include "ss_mfma.h"
 #include "ss_octs.h"
@@ -670,10 +674,10 @@ hipError_t launch_scan2_join(const Scan2BwdArgs& a, bool tiled, hipStream_t stre
 
 // Walks too few to fill the 256 CUs are cut into their chunks, which costs one more launch and the
 // states read and written once more.  The whole call, walks whole -> cut: bf16, headdim 64, d_state
-// 128, one batch row: 8 heads x 4096 steps 191 -> 70 us, 24 x 4096 224 -> 145, 48 x 2048 149 -> 137,
-// 48 x 512 66 -> 66, 64 x 4096 331 -> 354, 24 x 256 44 -> 44, 24 x 128 36 -> 39; float32: 3 x 777,
-// 6 heads of 48 x 40, 76 -> 48, 1 x 16384, 24 heads of 64 x 128, 1972 -> 1242, 1 x 4096, 64 heads,
-// 831 -> 858.
+// 128, one batch row: 8 heads x 4096 steps 196 -> 74 us, 24 x 4096 239 -> 153, 48 x 2048 165 -> 149,
+// 48 x 512 73 -> 70, 64 x 4096 380 -> 394, 24 x 256 48 -> 49, 24 x 128 41 -> 44; float32: 3 x 777,
+// 6 heads of 48 x 40, 73 -> 49, 1 x 16384, 24 heads of 64 x 128, 1820 -> 1150, 1 x 4096, 64 heads,
+// 765 -> 785.
 // Walks of more chunks than a launch has workgroups for stay whole.
 constexpr int64_t kCutWalks = 96, kCutChunks = 4;
 bool scan2_bwd_cut(int64_t heads, int64_t n_pblk, int64_t nc) {
@@ -681,7 +685,11 @@ bool scan2_bwd_cut(int64_t heads, int64_t n_pblk, int64_t nc) {
   return walks <= kCutWalks && nc >= kCutChunks && walks * nc <= kScan2BwdMaxWalks;
 }
 
-// Runs of heads: a workgroup for each of the 256 CUs (one fits a CU), at most a head each.
+// Runs of heads: a workgroup for each of the 256 CUs (one fits a CU), at most a head each.  The rule
+// counts workgroups, not their rounds over the CUs, so that a little more than a multiple of 256 units
+// costs a whole round more.  Backward of 80 heads of 64 x 128 bf16, one group, us for a thousand steps:
+// 4 x 4096 (256 units) 83, 8 x 4096 79, 6 x 4096 97, 5 x 4096 111, 4 x 4160 130; 3 x 4096 (192 units) 97,
+// 2 x 4160 138, 1 x 4160 153.
 int64_t scan2_bwd_splits(int64_t batch, int64_t seqlen, int64_t nheads, int64_t ngroups) {
   const int64_t units = batch * ((seqlen + kQ - 1) / kQ) * ngroups, hg = nheads / ngroups;
   const int64_t want = (256 + units - 1) / units;

@@ -2,31 +2,31 @@
 // states: the formulas and launches of ss_scan2_bwd.hip, with the products on the bf16 matrix
 // instruction.
 //
-// x, B and C are bf16 and enter the products exactly.  float32 operands are split into bf16 parts that
-// take a product each.  On the way to the float32 results (dA, ddt_bias, dh0), which are sums over
-// all tokens, they are three, the whole value: w X and e^c gy that make the states, the states where
-// they meet C and B, gy where it meets X.  With two parts, 2^-17, dA and ddt_bias were 2.7e-6 and
-// 3.2e-6 off at 4 x 4096 x 80 heads, dh0 2.4e-6 (plain float32 1e-7 to 3e-7).  What ends in a bf16
-// result alone, whose half step is 2^-8, has two: M and K, the states where they meet gy and X (dC and
-// dB), gy there and where it meets M (dx).  Products that have K down the rows of a tile read it with
-// the LDS transpose read, so every tile is staged once.
+// x, B and C are bf16 and enter the products exactly.  float32 operands are split into bf16 parts
+// that take a product each.  On the way to the float32 results (dA, ddt_bias, dh0) they are three,
+// the whole value: w X and e^c gy that make the states, the states where they meet C and B, gy where
+// it meets X.  (Two parts, 2^-17, left dA and ddt_bias 2.7e-6 and 3.2e-6 off at 4 x 4096 x 80 heads
+// and dh0 2.4e-6; three 1.8e-7, 2.5e-7 and 1.2e-7, as plain float32.)  What ends in a bf16 result
+// alone, whose half step is 2^-8, has two: M and K, the states where they meet gy and X (dC and dB),
+// gy there and where it meets M (dx).  Products that have K down the rows of a tile read it with the
+// LDS transpose read, so every tile is staged once.
 //
 // The states cross from the first launch to the second in float32, laid out as the first one holds
 // them: [d_state / 16][channel][16 states].  The LDS has room for two 16-bit planes of each, so it
 // holds the words' upper and lower halves, and the parts are formed as operands are read.
 //
 // What bounds it, at 4 x 4096 x 80 heads with 128 states: the states kernel 495 us, for 1.31 GB of
-// states written and 0.56 read (3.8 TB/s; with pairs of bf16 248 without the stores, 494 without the
+// states written and 0.62 fetched (3.9 TB/s; with two parts 248 without the stores, 494 without the
 // products, so it is the stores: splitting each walk's states over two workgroups took 570,
 // non-temporal stores the same 505, loads issued before the stores or another order of the chunks in
-// memory 528).  The chunks kernel 885 us with the gate, for 1.98 GB fetched and 0.38 written, by
-// barriers and latency: one workgroup of eight waves on a CU (160 KB of tiles) and three barriers a
-// head.  Of them the parts that make the values whole and the float64 sums are 210 (675 with pairs
-// and float32 sums, where the VALU was busy for 0.37 of the time, the LDS for 0.27, the matrix units
-// for 0.14; parts formed by dot products, in two thirds of the instructions, took the same).  Measured
-// then: sixteen waves of half the work the same (825 against 821 us), 32 x 32 tiles gained 3 %, M in one
-// bf16 4 % (not kept: dx and dz would be off by more than their own rounding), a head's parameters
-// fetched with its tiles 6 %.
+// memory 528).  The chunks kernel 865 us with the gate, for 2.02 GB fetched and 0.38 written: the
+// VALU is busy for half of the time, the LDS for a quarter, the matrix units for a seventh, and with
+// one workgroup of eight waves on a CU (160 KB of tiles) and three barriers a head they overlap
+// little.  The third parts and the float64 sums are 190 us of it (675 before, the VALU busy for 0.37;
+// the parts by dot products, in two thirds of the instructions, took the same).  Measured with two
+// parts: sixteen waves of half the work the same (825 against 821 us), 32 x 32 tiles gained 3 %, M
+// in one bf16 4 % (not kept: dx and dz would be off by more than their own rounding), a head's
+// parameters fetched with its tiles 6 %.
 #include "ss_head.h"
 #include "ss_mfma.h"
 #include "ss_scan2_bwd.h"
