@@ -149,13 +149,16 @@ def _sums(t):
 
 
 @pytest.mark.parametrize("gate", [True, False])
-@pytest.mark.parametrize("shape", [(16, 1000, 5, 64, 1, 128), (16, 1000, 5, 64, 1, 64),
-                                   (8, 1000, 6, 64, 2, 128), (2, 300, 8, 64, 1, 128),
-                                   (4, 1000, 24, 32, 1, 16)], ids=str)
-def test_many_heads_a_workgroup(shape, gate):
-    """bf16.  In all but the fourth shape (few walks, cut) the chunks number the card's CUs, so that one
-    workgroup walks several heads of a group, or all of them: 5, 5, 3, and at the end 24 in the kernel
-    for any shape.  The last batch row's gradients against the bounds of float32 products; what is
+@pytest.mark.parametrize("io,shape", [("bf16", (16, 1000, 5, 64, 1, 128)),
+                                      ("bf16", (16, 1000, 5, 64, 1, 64)),
+                                      ("bf16", (8, 1000, 6, 64, 2, 128)),
+                                      ("bf16", (2, 300, 8, 64, 1, 128)),
+                                      ("bf16", (16, 1000, 6, 32, 1, 16)),
+                                      ("f32", (16, 1000, 6, 32, 1, 130))], ids=str)
+def test_many_heads_a_workgroup(io, shape, gate):
+    """In all but the fourth shape (few walks, cut) the chunks number the card's CUs, so that one
+    workgroup walks all heads of a group: 5, 5, 3, and at the end 6 in the kernel for any shape.  The
+    last batch row's gradients against the bounds of float32 products; what is
     float32 by more: a term of it is a product of about ten factors, each off by one rounding or by the
     two U of a hardware function, and the terms' errors differ, so that dh0 is within 16 U of its
     norm and the sums over all tokens within 16 U of the root of their squares (with operands of
@@ -164,8 +167,8 @@ def test_many_heads_a_workgroup(shape, gate):
     batch, L, H, P, G, N = shape
     g = torch.Generator(device="cuda").manual_seed(N + L + H)
     n = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
-    b = lambda *s: n(*s).bfloat16()  # noqa: E731
-    t = dict(x=b(batch, L, H, P), dt=(0.5 * n(batch, L, H)).bfloat16(),
+    b = lambda *s: n(*s).to(DTYPES[io])  # noqa: E731
+    t = dict(x=b(batch, L, H, P), dt=(0.5 * n(batch, L, H)).to(DTYPES[io]),
              A=-1 - 7 * torch.rand(H, device="cuda", generator=g), B=b(batch, L, G, N),
              C=b(batch, L, G, N), dout=b(batch, L, H, P), D=n(H), dt_bias=0.3 * n(H) - 3,
              h0=n(batch, H, N, P), dh_last=n(batch, H, N, P))
@@ -180,7 +183,7 @@ def test_many_heads_a_workgroup(shape, gate):
     want = ht.scan2_bwd(**last)
     for k in ("dx", "ddt", "dz", "dB", "dC"):
         if want[k] is not None:
-            check(got[k][-1:], want[k], "bf16", k)
+            check(got[k][-1:], want[k], io, k)
     again = o.scan2_bwd(**t)
     for k, v in got.items():
         assert v is None or torch.equal(v, again[k]), k
